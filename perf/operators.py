@@ -120,7 +120,8 @@ def draw(rng):
         len_hi = _log(rng, 1, 2048)
         new_hi = min(_log(rng, 1, 2048), len_hi) if causal else _log(rng, 1, 2048)
         cost = len_hi * new_hi * c["q_heads"] * head_dim
-        seqs = _log(rng, 1, max(1, min(64, 2048 * 2048 * 32 * 128 * 2 // cost, 2 ** 26 // (row * max(len_hi, new_hi)))))
+        seqs = _log(rng, 1, max(1, min(64, 2048 * 2048 * 32 * 128 * 2 // cost, 2 ** 26 // (row * len_hi),
+                                       2 ** 26 // (c["q_heads"] * head_dim * new_hi))))
         c.update(seqs=seqs, causal=causal, cache="e4m3" if causal else rng.choice(("f16", "e4m3")), len_hi=len_hi,
                  len_lo=rng.randint(new_hi if causal else 0, len_hi), new_hi=new_hi,
                  new_lo=rng.randint(1, new_hi))
