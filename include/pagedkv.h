@@ -23,7 +23,8 @@
  *   positions) cannot be checked on the host: kernels that find a value out
  *   of range skip that access and record a flag readable with
  *   pf_device_status(); results for the affected rows are then undefined.
- * - fp16 is IEEE binary16 (PF_F16); fp32 (PF_F32) is only an output option.
+ * - fp16 is IEEE binary16 (PF_F16); fp32 (PF_F32) is only an output option;
+ *   PF_E4M3 is only a pool's type.
  *
  * Pool layout
  * -----------
@@ -36,6 +37,12 @@
  *     row[t / block_size] * block_size + t % block_size
  * ("Why Naive KV-Caches Waste >60% VRAM", section 1 "Physical Block Pool &
  * Block Tables"; PageFault README, "The OS analogy").
+ *
+ * 8-bit pools (PF_E4M3, pf_pool_create_e4m3) have the same layout in e4m3
+ * codes, and one fp32 scale per layer, block and kv-head for each of K and V
+ * ([n_layers][n_blocks][n_kv_heads]): a row is code * scale.  Scales are
+ * powers of two, set by pf_append_kv.  The pool's type decides what a call
+ * does; calls that do not exist for it give PF_ERR_UNSUPPORTED.
  *
  * Block tables are int32 [n_seqs][max_blocks_per_seq], row-major; entries
  * past a sequence's ceil(L / block_size) used blocks are never read.
@@ -65,14 +72,15 @@ enum pf_status {
     PF_ERR_UNSUPPORTED = 5  /* valid but not built (e.g. no sm_103a device) */
 };
 
-enum pf_dtype { PF_F16 = 1, PF_F32 = 2 };
+enum pf_dtype { PF_F16 = 1, PF_F32 = 2, PF_E4M3 = 3 };
 
 /* Flags in the device status word (pf_device_status). */
 enum pf_device_flag {
     PF_DEV_BAD_BLOCK_ID = 1,  /* a block id outside [0, n_blocks) was met */
     PF_DEV_BAD_LENGTH = 2,    /* a context length < 0 or > max_blocks * B */
     PF_DEV_BAD_POSITION = 4,  /* a write position < 0 or past the table row */
-    PF_DEV_WAIT_TIMEOUT = 8   /* a bounded on-chip wait gave up (kernel bug) */
+    PF_DEV_WAIT_TIMEOUT = 8,  /* a bounded on-chip wait gave up (kernel bug) */
+    PF_DEV_NONFINITE = 16     /* an appended row held inf or NaN (8-bit pools) */
 };
 
 typedef struct pf_pool pf_pool;
@@ -88,7 +96,7 @@ PF_API int pf_abi_version(void);
 /* ------------------------------------------------------------- pool ---- */
 
 /* Bytes of ONE of the two pools (K or V) for these dimensions; 0 if a
- * dimension is not positive or dtype is not PF_F16.  An implementation
+ * dimension is not positive or dtype is neither PF_F16 nor PF_E4M3.  An implementation
  * call with no counterpart on the pages: the size of the pool layout below,
  * for the caller who allocates it. */
 PF_API size_t pf_pool_bytes(int n_layers, int n_blocks, int block_size,
@@ -104,6 +112,19 @@ PF_API int pf_pool_create(pf_pool **out, void *k_base, void *v_base, int n_layer
                    int n_blocks, int block_size, int n_kv_heads, int head_dim,
                    int dtype);
 PF_API int pf_pool_destroy(pf_pool *pool);
+
+/* Bytes of the scales of ONE of an 8-bit pool's two halves (K or V); 0 if a
+ * dimension is not positive. */
+PF_API size_t pf_scale_bytes(int n_layers, int n_blocks, int n_kv_heads);
+
+/* Describe caller-owned 8-bit K and V pools (pf_pool_bytes(..., PF_E4M3) bytes
+ * each, 16-byte aligned) and their scales (pf_scale_bytes() bytes each, 4-byte
+ * aligned).  Nothing needs initialising: a block is read up to the rows that
+ * pf_append_kv wrote into it.  Half the bytes of an fp16 pool per cached
+ * token, for a relative error of at most 2^-4 per value (e4m3 has three
+ * mantissa bits).  Non-owning, as pf_pool_create. */
+PF_API int pf_pool_create_e4m3(pf_pool **out, void *k_base, void *v_base, float *k_scale, float *v_scale,
+                        int n_layers, int n_blocks, int block_size, int n_kv_heads, int head_dim);
 
 /* -------------------------------------------------- host allocator ---- */
 /* O(1) free-list allocator over block ids [0, n_blocks).  A LIFO stack
@@ -148,6 +169,17 @@ PF_API int pf_alloc_cow(pf_alloc *a, int32_t *entry, int32_t *src_out, int32_t *
  * (max_blocks entries) is too short. */
 PF_API int pf_seq_fork(pf_alloc *a, int block_size, const int32_t *parent_row,
                        int len, int32_t *child_row, int max_blocks);
+/* Compact: referenced blocks move so that they are exactly the ids 0 ..
+ * live - 1 (to give the tail of a pool back, or to make room at its end).
+ * The *n_out moves are block src_out[i] -> dst_out[i] (sources at or above the
+ * live count, destinations free ids below it, both ascending, so no
+ * destination is a source); map_out[b] is block b's new id (b itself if it
+ * stays).  References move with their blocks, and the free ids are handed out
+ * from the lowest on.  src_out, dst_out, map_out: host int32, n_blocks entries
+ * each.  The allocator speaks of the new ids from here on: move the contents
+ * and the device tables with pf_compact_blocks, and send host table rows
+ * through map_out, before the pool is used again. */
+PF_API int pf_alloc_compact(pf_alloc *a, int32_t *src_out, int32_t *dst_out, int32_t *map_out, int *n_out);
 /* Number of free blocks, or -1 for a null handle. */
 PF_API int pf_alloc_free_count(const pf_alloc *a);
 /* Demand paging (PagedAttention blog, "Architecture"): grow one sequence
@@ -173,19 +205,48 @@ PF_API int pf_seq_release(pf_alloc *a, int block_size, const int32_t *table_row,
  * contiguous, device) are copied to its slot of layer `layer`.  One launch
  * covers all tokens and heads.  block_tables, seq_idx, pos: device int32.
  * Two tokens of one call must not target the same slot.  Bit-exact copy.
- * n_tokens == 0 is a no-op. */
+ * n_tokens == 0 is a no-op.  fp16 pools only (pf_append_kv fills 8-bit
+ * ones). */
 PF_API int pf_write_kv(const pf_pool *pool, int layer, const void *k_new,
                 const void *v_new, const int32_t *block_tables,
                 int n_table_rows, int max_blocks_per_seq,
                 const int32_t *seq_idx, const int32_t *pos, int n_tokens,
                 void *stream);
 
+/* Quantising append into an 8-bit pool (no counterpart on the pages): the
+ * last n_s tokens of sequence s, n_s = cu_new[s + 1] - cu_new[s], of its
+ * L = context_lens[s] (the new ones included), are rows cu_new[s] ..
+ * cu_new[s + 1] - 1 of k_new / v_new (fp16 [T][Hkv][D], contiguous): the
+ * lengths and offsets that pf_paged_prefill_attention takes.  cu_new: device
+ * int32 [n_seqs + 1], non-decreasing, or NULL for one new token (row s) of
+ * every sequence with L > 0 (a decode step; max_new_tokens must be 1).
+ * max_new_tokens bounds every n_s.  For each touched block and kv-head, K and
+ * V apart, with x its new rows:
+ *   scale' = 2^k, k the smallest integer >= -24 with max |x| <= 448 * 2^k,
+ *            or the block's scale where that is larger and earlier tokens of
+ *            the sequence lie in the block;
+ *   code   = x / scale' rounded to e4m3 (nearest even), its magnitude at most
+ *            min(448, 61440 / scale'), so that every row is a finite fp16.
+ * Where the scale grows, the block's earlier rows are rounded again to it (an
+ * exponent shift: exact but for codes below 2^-6).  Sequences append in
+ * order: tokens past L in a block count as unwritten, and after a rollback
+ * the block keeps its scale.  No block may be touched through two sequences
+ * of one call, nor be shared (pf_alloc_cow first).  inf and NaN set
+ * PF_DEV_NONFINITE and are stored as the largest magnitude and as 0; they do
+ * not count for the scale.  n_s > L or > max_new_tokens, or a length outside
+ * the table, sets PF_DEV_BAD_LENGTH and is clamped; bad block ids are flagged
+ * and skipped. */
+PF_API int pf_append_kv(const pf_pool *pool, int layer, const void *k_new, const void *v_new,
+                 const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                 const int32_t *cu_new, int n_seqs, int max_new_tokens, void *stream);
+
 /* Gather (PageForge, "Four layers, one pointer": gather_kv assembles a
  * sequence's scattered pages into a contiguous buffer).  For every sequence
  * s and t < context_lens[s], row cu_off[s] + t of k_out / v_out
  * ([rows][Hkv][D] fp16, device) receives token t of layer `layer`.
  * context_lens: device int32 [n_seqs]; cu_off: device int64 [n_seqs]
- * (row offsets; the caller sizes the outputs).  Bit-exact copy. */
+ * (row offsets; the caller sizes the outputs).  Bit-exact copy; from an
+ * 8-bit pool, code * scale rounded to fp16. */
 PF_API int pf_gather_kv(const pf_pool *pool, int layer, const int32_t *block_tables,
                  int max_blocks_per_seq, const int32_t *context_lens,
                  const int64_t *cu_off, int n_seqs, void *k_out, void *v_out,
@@ -194,16 +255,31 @@ PF_API int pf_gather_kv(const pf_pool *pool, int layer, const int32_t *block_tab
 /* ------------------------------------------- whole-block copies ---- */
 
 /* Bytes of one block image: block b's K then V rows of layer 0, then of
- * layer 1, ...: [n_layers][2][B][Hkv][D] fp16.  0 for a null pool. */
+ * layer 1, ...: [n_layers][2][B][Hkv][D] fp16.  8-bit pools: each of the
+ * n_layers * 2 parts is [B][Hkv][D] codes followed by Hkv scales, padded to 16
+ * bytes.  0 for a null pool. */
 PF_API size_t pf_block_image_bytes(const pf_pool *pool);
 /* Copy-on-write copies (PagedAttention blog, "Copy-on-Write for Parallel
  * Sampling"): for i < n, block dst_ids[i] takes the contents of block
  * src_ids[i] in every layer, K and V.  src_ids, dst_ids: device int32 [n].
  * A destination must not also be a source or another pair's destination.
  * Ids outside [0, n_blocks) set PF_DEV_BAD_BLOCK_ID and that pair is
- * skipped.  Bit-exact.  n == 0 is a no-op. */
+ * skipped.  Bit-exact (an 8-bit pool's scales too).  n == 0 is a no-op. */
 PF_API int pf_copy_blocks(const pf_pool *pool, const int32_t *src_ids,
                           const int32_t *dst_ids, int n, void *stream);
+/* The device side of a compaction (pf_alloc_compact), one launch: for i < n
+ * block dst_ids[i] takes the contents of block src_ids[i] in every layer, and
+ * the entries of block_tables that a context uses (entry j of row s where
+ * j * B < context_lens[s]) become block_map[entry].  src_ids, dst_ids: device
+ * int32 [n], no destination a source or another's destination; block_map:
+ * device int32 [n_blocks]; block_tables: device int32 [n_table_rows]
+ * [max_blocks_per_seq], changed in place (n_table_rows == 0: no tables, the
+ * three pointers may be NULL).  Ids and map entries outside [0, n_blocks) are
+ * flagged and skipped, lengths outside the table flagged and clamped.  Kernels
+ * that use the pool or the tables must be ordered before or after the call. */
+PF_API int pf_compact_blocks(const pf_pool *pool, const int32_t *src_ids, const int32_t *dst_ids, int n,
+                             const int32_t *block_map, int32_t *block_tables, int n_table_rows,
+                             int max_blocks_per_seq, const int32_t *context_lens, void *stream);
 /* Swap out (same blog, "Preemption and Swapping": under memory pressure a
  * sequence's blocks are evicted to CPU memory, per block): the images of
  * blocks ids[0..n) (device int32) are written to host_dst[i] (n images of
@@ -265,7 +341,11 @@ PF_API int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stre
  * cores.
  * workspace: device memory of at least pf_decode_workspace_bytes(...) bytes,
  * initialised once with pf_decode_workspace_init; calls sharing a workspace
- * must not overlap on the GPU. */
+ * must not overlap on the GPU.
+ * 8-bit pools: split_tokens 0 only (any page size, up to 16 q-heads per
+ * kv-head); K and V are code * scale, the products run on tensor cores as
+ * above (codes are exact in fp16), and a workspace of this call may be used by
+ * captured graphs as often as they are replayed. */
 PF_API int pf_paged_decode_attention(const pf_pool *pool, int layer, const void *q,
                               const int32_t *block_tables,
                               int max_blocks_per_seq,
@@ -295,7 +375,10 @@ PF_API int pf_paged_decode_attention(const pf_pool *pool, int layer, const void 
  * does not write context_lens or block_tables (for instance when it is the
  * previous layer's or step's pf_decode_step).  If the previous operation on
  * the stream is not a kernel, the flag changes nothing.  Unknown bits give
- * PF_ERR_INVALID. */
+ * PF_ERR_INVALID.
+ * 8-bit pools: pf_append_kv of one token per sequence, then
+ * pf_paged_decode_attention, two launches (a block's scale is needed before
+ * any of its rows); PF_STEP_OVERLAP_PREVIOUS changes nothing. */
 enum pf_step_flags { PF_STEP_OVERLAP_PREVIOUS = 1 };
 PF_API int pf_decode_step(const pf_pool *pool, int layer, const void *q,
                           const void *k_new, const void *v_new,
@@ -335,7 +418,10 @@ PF_API int pf_decode_step(const pf_pool *pool, int layer, const void *q,
  * to fp16 (within the attention tolerance).
  * Up to 16 q-heads per kv-head; the tcgen05 kernel holds one block per SM
  * (165 KB of shared memory at head_dim 64, 197 KB at 128, and all 512
- * tensor-memory columns). */
+ * tensor-memory columns).
+ * 8-bit pools (rows written by pf_append_kv): with a workspace and rows <= 16
+ * on any page size, a kernel that reads every K/V byte once; otherwise the
+ * tcgen05 kernel, its loaders widening the codes. */
 PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
                                       const void *q,
                                       const int32_t *block_tables,
@@ -353,6 +439,31 @@ PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
 PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
                                          int n_q_heads, int max_blocks_per_seq,
                                          int max_new_tokens);
+
+/* Cross attention (no counterpart on the pages): the queries are another
+ * sequence than the cached one -- a decoder's tokens against the states of an
+ * encoder whose K/V rows were written into pages once -- so every query sees
+ * the whole context, and their count is free of its length.  Queries of
+ * sequence s are rows cu_q[s] .. cu_q[s + 1] - 1 of q (fp16 [T_q][n_q_heads]
+ * [D]); L = context_lens[s]:
+ *   out[row][hq][d] = sum_{t < L} softmax_t(scale * q . K[slot(s, t)][h]) V[..][h][d]
+ * with h = hq / (n_q_heads / Hkv), fp32 accumulation; L = 0 gives zeros.
+ * Arguments as pf_paged_prefill_attention; max_q_tokens bounds every query
+ * count (more are flagged with PF_DEV_BAD_LENGTH and left out).  Block tables
+ * of several rows may name the same pages (several hypotheses of one input).
+ * Either pool type.  With a workspace (pf_cross_workspace_bytes, initialised
+ * once with pf_decode_workspace_init, not shared by overlapping calls) and at
+ * most 16 query rows (tokens x q-heads) per kv-head, a kernel that cuts long
+ * contexts over the SMs, fp32 output with the weights to about 22 bits;
+ * otherwise the tcgen05 kernel, the weights rounded to fp16. */
+PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q,
+                             int n_seqs, int max_q_tokens, int n_q_heads, float scale, void *out, int out_dtype,
+                             void *workspace, size_t ws_bytes, void *stream);
+/* Workspace bytes of pf_paged_cross_attention for these sizes, or 0 when it
+ * needs none (more than 16 rows per kv-head) or on bad arguments. */
+PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                                int max_q_tokens);
 
 /* The decode attention call for callers that cannot allocate device memory.
  * No counterpart on the pages: it exists for code that may only touch the

@@ -22,11 +22,13 @@ PF_ERR_UNSUPPORTED = 5
 
 PF_F16 = 1
 PF_F32 = 2
+PF_E4M3 = 3
 
 PF_DEV_BAD_BLOCK_ID = 1
 PF_DEV_BAD_LENGTH = 2
 PF_DEV_BAD_POSITION = 4
 PF_DEV_WAIT_TIMEOUT = 8
+PF_DEV_NONFINITE = 16
 PF_STEP_OVERLAP_PREVIOUS = 1
 
 _lib = None
@@ -67,6 +69,8 @@ def lib():
         "pf_abi_version": (I, []),
         "pf_pool_bytes": (Z, [I, I, I, I, I, I]),
         "pf_pool_create": (I, [ctypes.POINTER(P), P, P, I, I, I, I, I, I]),
+        "pf_pool_create_e4m3": (I, [ctypes.POINTER(P), P, P, P, P, I, I, I, I, I]),
+        "pf_scale_bytes": (Z, [I, I, I]),
         "pf_pool_destroy": (I, [P]),
         "pf_alloc_create": (I, [ctypes.POINTER(P), I, U64]),
         "pf_alloc_destroy": (I, [P]),
@@ -78,14 +82,19 @@ def lib():
         "pf_alloc_share": (I, [P, P, I]),
         "pf_alloc_refcount": (I, [P, ctypes.c_int32]),
         "pf_alloc_cow": (I, [P, P, P, P]),
+        "pf_alloc_compact": (I, [P, P, P, P, ctypes.POINTER(I)]),
         "pf_seq_fork": (I, [P, I, P, I, P, I]),
         "pf_block_image_bytes": (Z, [P]),
         "pf_paged_prefill_attention": (I, [P, I, P, P, I, P, P, I, I, I, F, P, I, P, Z, P]),
         "pf_prefill_workspace_bytes": (Z, [P, I, I, I, I]),
+        "pf_paged_cross_attention": (I, [P, I, P, P, I, P, P, I, I, I, F, P, I, P, Z, P]),
+        "pf_cross_workspace_bytes": (Z, [P, I, I, I, I]),
         "pf_copy_blocks": (I, [P, P, P, I, P]),
+        "pf_compact_blocks": (I, [P, P, P, I, P, P, I, I, P, P]),
         "pf_swap_out": (I, [P, P, I, P, P]),
         "pf_swap_in": (I, [P, P, P, I, P]),
         "pf_write_kv": (I, [P, I, P, P, P, I, I, P, P, I, P]),
+        "pf_append_kv": (I, [P, I, P, P, P, I, P, P, I, I, P]),
         "pf_gather_kv": (I, [P, I, P, I, P, P, I, P, P, P]),
         "pf_decode_workspace_bytes": (Z, [P, I, I, I, I]),
         "pf_decode_workspace_init": (I, [P, Z, P]),
@@ -134,6 +143,18 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_current_device(pool, **tensors):
+    """The pool and these tensors lie on torch's current device (whose current
+    stream the call takes by default)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if pool.k_pool.get_device() != dev:
+        raise PagedKVError(PF_ERR_INVALID, f"the pool is on {pool.k_pool.device}, the current device is cuda:{dev}")
+
+
 def _host_i32(a, name):
     import numpy as np
     if not isinstance(a, np.ndarray) or a.dtype != np.int32 or not a.flags.c_contiguous:
@@ -156,13 +177,16 @@ def pf_pool_bytes(n_layers, n_blocks, block_size, n_kv_heads, head_dim, dtype=PF
 
 
 class Pool:
-    """Handle of a pf_pool over two caller-owned [L, N, B, Hkv, D] fp16 tensors
-    (kept referenced here so they outlive the handle)."""
+    """Handle of a pf_pool over two caller-owned [L, N, B, Hkv, D] tensors, fp16
+    or e4m3 with [L, N, Hkv] fp32 scales (kept referenced here so they outlive
+    the handle)."""
 
-    def __init__(self, handle, k_pool, v_pool):
+    def __init__(self, handle, k_pool, v_pool, k_scale=None, v_scale=None):
         self.handle = handle
         self.k_pool = k_pool
         self.v_pool = v_pool
+        self.k_scale = k_scale
+        self.v_scale = v_scale
         self.n_layers, self.n_blocks, self.block_size, self.n_kv_heads, self.head_dim = k_pool.shape
 
     def __del__(self):
@@ -171,8 +195,37 @@ class Pool:
             self.handle = None
 
 
-def pf_pool_create(k_pool, v_pool):
+def pf_scale_bytes(n_layers, n_blocks, n_kv_heads):
+    return lib().pf_scale_bytes(n_layers, n_blocks, n_kv_heads)
+
+
+def pf_pool_create_e4m3(k_pool, v_pool, k_scale, v_scale):
+    """8-bit pool: torch.float8_e4m3fn tensors [L, N, B, Hkv, D] and fp32
+    scales [L, N, Hkv], filled by pf_append_kv."""
     import torch
+    if k_pool.dim() != 5 or k_pool.shape != v_pool.shape:
+        raise PagedKVError(PF_ERR_INVALID, "pools must both be [n_layers, n_blocks, block_size, n_kv_heads, head_dim]")
+    L, N, B, H, D = k_pool.shape
+    if k_scale is None or v_scale is None or tuple(k_scale.shape) != (L, N, H) or tuple(v_scale.shape) != (L, N, H):
+        raise PagedKVError(PF_ERR_INVALID, "an e4m3 pool needs k_scale and v_scale [n_layers, n_blocks, n_kv_heads]")
+    if len({t.get_device() for t in (k_pool, v_pool, k_scale, v_scale)}) != 1:
+        raise PagedKVError(PF_ERR_INVALID, "pools and scales must lie on one device")
+    h = ctypes.c_void_p()
+    _check(lib().pf_pool_create_e4m3(ctypes.byref(h), _dev_ptr(k_pool, "k_pool", torch.float8_e4m3fn),
+                                     _dev_ptr(v_pool, "v_pool", torch.float8_e4m3fn),
+                                     _dev_ptr(k_scale, "k_scale", torch.float32),
+                                     _dev_ptr(v_scale, "v_scale", torch.float32), L, N, B, H, D))
+    return Pool(h, k_pool, v_pool, k_scale, v_scale)
+
+
+def pf_pool_create(k_pool, v_pool, k_scale=None, v_scale=None):
+    """Pool over fp16 tensors, or over torch.float8_e4m3fn tensors and their
+    scales (pf_pool_create_e4m3)."""
+    import torch
+    if k_pool.dtype == torch.float8_e4m3fn:
+        return pf_pool_create_e4m3(k_pool, v_pool, k_scale, v_scale)
+    if k_scale is not None or v_scale is not None:
+        raise PagedKVError(PF_ERR_INVALID, "an fp16 pool has no scales")
     if k_pool.dim() != 5 or k_pool.shape != v_pool.shape:
         raise PagedKVError(PF_ERR_INVALID, "pools must both be [n_layers, n_blocks, block_size, n_kv_heads, head_dim]")
     kp = _dev_ptr(k_pool, "k_pool", torch.float16)
@@ -225,6 +278,18 @@ def pf_free_blocks(alloc, ids):
     import numpy as np
     ids = np.ascontiguousarray(ids, dtype=np.int32)
     _check(lib().pf_free_blocks(alloc.handle, ids.ctypes.data_as(ctypes.c_void_p), ids.size))
+
+
+def pf_alloc_compact(alloc):
+    """Pack the referenced blocks into the lowest ids.  Returns (src, dst,
+    block_map), host int32 arrays: move the contents and the device tables
+    with pf_compact_blocks, host rows by block_map[row]."""
+    import numpy as np
+    src, dst, block_map = (np.zeros(alloc.n_blocks, dtype=np.int32) for _ in range(3))
+    n = ctypes.c_int()
+    _check(lib().pf_alloc_compact(alloc.handle, *(a.ctypes.data_as(ctypes.c_void_p) for a in (src, dst, block_map)),
+                                  ctypes.byref(n)))
+    return src[:n.value].copy(), dst[:n.value].copy(), block_map
 
 
 def pf_alloc_free_count(alloc):
@@ -286,6 +351,27 @@ def pf_copy_blocks(pool, src_ids, dst_ids, stream=None):
                                 _dev_ptr(dst_ids, "dst_ids", torch.int32), n, _stream_ptr(stream)))
 
 
+def pf_compact_blocks(pool, src_ids, dst_ids, block_map, block_tables, context_lens, stream=None):
+    """Block dst_ids[i] := block src_ids[i] in every layer, and the used entries
+    of block_tables (in place) through block_map, in one launch (device int32)."""
+    import torch
+    n = src_ids.numel()
+    if dst_ids.numel() != n:
+        raise PagedKVError(PF_ERR_INVALID, "src_ids and dst_ids must have the same length")
+    if block_map.numel() != pool.n_blocks:
+        raise PagedKVError(PF_ERR_INVALID, "block_map must have n_blocks entries")
+    if block_tables.dim() != 2 or context_lens.numel() != block_tables.shape[0]:
+        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_rows, max_blocks]; context_lens [n_rows]")
+    _on_current_device(pool, src_ids=src_ids, dst_ids=dst_ids, block_map=block_map, block_tables=block_tables,
+                       context_lens=context_lens)
+    _check(lib().pf_compact_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32),
+                                   _dev_ptr(dst_ids, "dst_ids", torch.int32), n,
+                                   _dev_ptr(block_map, "block_map", torch.int32),
+                                   _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[0],
+                                   block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
+                                   _stream_ptr(stream)))
+
+
 def _pinned_ptr(t, name, nbytes):
     import torch
     if not isinstance(t, torch.Tensor) or t.is_cuda or not t.is_pinned() or not t.is_contiguous():
@@ -338,6 +424,62 @@ def pf_paged_prefill_attention(pool, layer, q, block_tables, context_lens, cu_q,
         _dev_ptr(out, "out"), out_dtype,
         None if workspace is None else _dev_ptr(workspace, "workspace"),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+
+
+def pf_cross_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens):
+    """Workspace bytes of pf_paged_cross_attention (0: it needs none)."""
+    return lib().pf_cross_workspace_bytes(pool.handle, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens)
+
+
+def pf_paged_cross_attention(pool, layer, q, block_tables, context_lens, cu_q, max_q_tokens, scale, out,
+                             workspace=None, stream=None):
+    """Attention of each sequence's queries (q rows cu_q[s]..cu_q[s+1]-1) over
+    all of its context, whose length is its own (device tensors).  With a
+    workspace, calls of few rows are cut over the SMs."""
+    import torch
+    n = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or cu_q.numel() != n + 1:
+        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
+    if q.dim() != 3 or q.shape[2] != pool.head_dim or tuple(out.shape) != tuple(q.shape):
+        raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out of its shape")
+    out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
+    if out_dtype is None:
+        raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
+    _on_current_device(pool, q=q, block_tables=block_tables, context_lens=context_lens, cu_q=cu_q, out=out,
+                       workspace=workspace)
+    if q.numel() == 0:
+        return
+    _check(lib().pf_paged_cross_attention(
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
+        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
+        _dev_ptr(cu_q, "cu_q", torch.int32), n, int(max_q_tokens), q.shape[1], float(scale),
+        _dev_ptr(out, "out"), out_dtype,
+        None if workspace is None else _dev_ptr(workspace, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+
+
+def pf_append_kv(pool, layer, k_new, v_new, block_tables, context_lens, cu_new, max_new_tokens=1, stream=None):
+    """Quantise new rows into an 8-bit pool: sequence s's last
+    cu_new[s+1]-cu_new[s] tokens are rows cu_new[s].. of k_new / v_new; cu_new
+    None: one token per sequence with a context, row s."""
+    import torch
+    n = context_lens.numel()
+    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (pool.n_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
+        raise PagedKVError(PF_ERR_INVALID, "k_new / v_new must be [n_tokens, n_kv_heads, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
+    if k_new.shape[0] != n if cu_new is None else cu_new.numel() != n + 1:
+        raise PagedKVError(PF_ERR_INVALID, "cu_new must have n_seqs + 1 entries, or be None with one row per sequence")
+    _on_current_device(pool, k_new=k_new, v_new=v_new, block_tables=block_tables, context_lens=context_lens,
+                       cu_new=cu_new)
+    if k_new.numel() == 0:
+        return
+    _check(lib().pf_append_kv(pool.handle, layer, _dev_ptr(k_new, "k_new", torch.float16),
+                              _dev_ptr(v_new, "v_new", torch.float16),
+                              _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+                              _dev_ptr(context_lens, "context_lens", torch.int32),
+                              None if cu_new is None else _dev_ptr(cu_new, "cu_new", torch.int32), n,
+                              int(max_new_tokens), _stream_ptr(stream)))
 
 
 def pf_write_kv(pool, layer, k_new, v_new, block_tables, seq_idx, pos, stream=None):

@@ -36,6 +36,13 @@ bool valid_block_size(int b) { return b == 1 || b == 16 || b == 64 || b == 256; 
 
 bool valid_head_dim(int d) { return d == 64 || d == 128; }
 
+// Calls that exist for one pool type only.
+int need_dtype(const pf_pool *pool, int dtype, const char *fn, const char *instead) {
+    if (pool->dtype == dtype) return PF_OK;
+    return pkv::set_error(PF_ERR_UNSUPPORTED, std::string(fn) + ": not built for " +
+                                                  (pool->dtype == PF_E4M3 ? "PF_E4M3" : "PF_F16") + " pools" + instead);
+}
+
 int check_pool(const pf_pool *pool, int layer, const char *fn) {
     if (!pool) return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": pool is null");
     if (layer < 0 || layer >= pool->n_layers)
@@ -55,21 +62,24 @@ int pf_abi_version(void) { return PF_ABI_VERSION; }
 size_t pf_pool_bytes(int n_layers, int n_blocks, int block_size, int n_kv_heads, int head_dim,
                      int dtype) {
     if (n_layers <= 0 || n_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0 ||
-        dtype != PF_F16)
+        (dtype != PF_F16 && dtype != PF_E4M3))
         return 0;
     return (size_t)n_layers * (size_t)n_blocks * (size_t)block_size * (size_t)n_kv_heads *
-           (size_t)head_dim * 2u;
+           (size_t)head_dim * (dtype == PF_F16 ? 2u : 1u);
 }
 
-int pf_pool_create(pf_pool **out, void *k_base, void *v_base, int n_layers, int n_blocks,
-                   int block_size, int n_kv_heads, int head_dim, int dtype) {
-    pkv::clear_error();
+size_t pf_scale_bytes(int n_layers, int n_blocks, int n_kv_heads) {
+    if (n_layers <= 0 || n_blocks <= 0 || n_kv_heads <= 0) return 0;
+    return (size_t)n_layers * (size_t)n_blocks * (size_t)n_kv_heads * sizeof(float);
+}
+
+static int pool_create(pf_pool **out, void *k_base, void *v_base, float *k_scale, float *v_scale, int n_layers,
+                       int n_blocks, int block_size, int n_kv_heads, int head_dim, int dtype) {
     if (!out) return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: out is null");
     *out = nullptr;
     if (!k_base || !v_base) return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: null pool pointer");
     if (!aligned16(k_base) || !aligned16(v_base))
         return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: pool pointers must be 16-byte aligned");
-    if (dtype != PF_F16) return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: dtype must be PF_F16");
     if (!valid_head_dim(head_dim))
         return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: head_dim must be 64 or 128");
     if (!valid_block_size(block_size))
@@ -85,6 +95,8 @@ int pf_pool_create(pf_pool **out, void *k_base, void *v_base, int n_layers, int 
     if (!p) return pkv::set_error(PF_ERR_OOM, "pf_pool_create: host allocation failed");
     p->k_base = k_base;
     p->v_base = v_base;
+    p->k_scale = k_scale;
+    p->v_scale = v_scale;
     p->n_layers = n_layers;
     p->n_blocks = n_blocks;
     p->block_size = block_size;
@@ -99,6 +111,28 @@ int pf_pool_create(pf_pool **out, void *k_base, void *v_base, int n_layers, int 
     return PF_OK;
 }
 
+int pf_pool_create(pf_pool **out, void *k_base, void *v_base, int n_layers, int n_blocks, int block_size,
+                   int n_kv_heads, int head_dim, int dtype) {
+    pkv::clear_error();
+    if (out) *out = nullptr;
+    if (dtype != PF_F16)
+        return pkv::set_error(PF_ERR_INVALID, "pf_pool_create: dtype must be PF_F16 (PF_E4M3 pools have scales: "
+                                              "pf_pool_create_e4m3)");
+    return pool_create(out, k_base, v_base, nullptr, nullptr, n_layers, n_blocks, block_size, n_kv_heads, head_dim,
+                       dtype);
+}
+
+int pf_pool_create_e4m3(pf_pool **out, void *k_base, void *v_base, float *k_scale, float *v_scale, int n_layers,
+                        int n_blocks, int block_size, int n_kv_heads, int head_dim) {
+    pkv::clear_error();
+    if (out) *out = nullptr;
+    if (!k_scale || !v_scale) return pkv::set_error(PF_ERR_INVALID, "pf_pool_create_e4m3: null scale pointer");
+    if (((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u) != 0)
+        return pkv::set_error(PF_ERR_INVALID, "pf_pool_create_e4m3: scale pointers must be 4-byte aligned");
+    return pool_create(out, k_base, v_base, k_scale, v_scale, n_layers, n_blocks, block_size, n_kv_heads, head_dim,
+                       PF_E4M3);
+}
+
 int pf_pool_destroy(pf_pool *pool) {
     pkv::clear_error();
     delete pool;
@@ -111,6 +145,7 @@ int pf_write_kv(const pf_pool *pool, int layer, const void *k_new, const void *v
     pkv::clear_error();
     int rc = check_pool(pool, layer, "pf_write_kv");
     if (rc) return rc;
+    if ((rc = need_dtype(pool, PF_F16, "pf_write_kv", ": pf_append_kv quantises")) != PF_OK) return rc;
     if (n_tokens < 0) return pkv::set_error(PF_ERR_INVALID, "pf_write_kv: negative n_tokens");
     if (n_tokens == 0) return PF_OK;
     if (!k_new || !v_new || !block_tables || !seq_idx || !pos)
@@ -123,6 +158,29 @@ int pf_write_kv(const pf_pool *pool, int layer, const void *k_new, const void *v
     pkv::WriteArgs a{pool, layer, k_new, v_new, block_tables, n_table_rows, max_blocks_per_seq,
                      seq_idx, pos, n_tokens};
     return pkv::launch_write_kv(a, static_cast<cudaStream_t>(stream));
+}
+
+int pf_append_kv(const pf_pool *pool, int layer, const void *k_new, const void *v_new, const int32_t *block_tables,
+                 int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_new, int n_seqs,
+                 int max_new_tokens, void *stream) {
+    pkv::clear_error();
+    int rc = check_pool(pool, layer, "pf_append_kv");
+    if (rc) return rc;
+    if ((rc = need_dtype(pool, PF_E4M3, "pf_append_kv", ": pf_write_kv copies")) != PF_OK) return rc;
+    if (n_seqs < 0 || max_new_tokens < 0)
+        return pkv::set_error(PF_ERR_INVALID, "pf_append_kv: negative n_seqs or max_new_tokens");
+    if (n_seqs == 0 || max_new_tokens == 0) return PF_OK;
+    if (!k_new || !v_new || !block_tables || !context_lens)
+        return pkv::set_error(PF_ERR_INVALID, "pf_append_kv: null pointer");
+    if (!aligned16(k_new) || !aligned16(v_new))
+        return pkv::set_error(PF_ERR_INVALID, "pf_append_kv: k_new / v_new must be 16-byte aligned");
+    if (max_blocks_per_seq <= 0 || (long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
+        return pkv::set_error(PF_ERR_INVALID, "pf_append_kv: bad max_blocks_per_seq");
+    if (!cu_new && max_new_tokens != 1)
+        return pkv::set_error(PF_ERR_INVALID, "pf_append_kv: max_new_tokens must be 1 without cu_new");
+    pkv::AppendArgs a{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, cu_new, n_seqs,
+                      max_new_tokens};
+    return pkv::launch_append(a, static_cast<cudaStream_t>(stream));
 }
 
 int pf_gather_kv(const pf_pool *pool, int layer, const int32_t *block_tables, int max_blocks_per_seq,
@@ -141,11 +199,19 @@ int pf_gather_kv(const pf_pool *pool, int layer, const int32_t *block_tables, in
         return pkv::set_error(PF_ERR_INVALID, "pf_gather_kv: max_blocks_per_seq must be positive");
     pkv::GatherArgs a{pool, layer, block_tables, max_blocks_per_seq, context_lens, cu_off,
                       n_seqs, k_out, v_out};
+    if (pool->dtype == PF_E4M3) {
+        if ((long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
+            return pkv::set_error(PF_ERR_INVALID, "pf_gather_kv: max_blocks_per_seq is too large");
+        return pkv::launch_gather_e4m3(a, static_cast<cudaStream_t>(stream));
+    }
     return pkv::launch_gather_kv(a, static_cast<cudaStream_t>(stream));
 }
 
 size_t pf_block_image_bytes(const pf_pool *pool) {
     if (!pool) return 0;
+    if (pool->dtype == PF_E4M3)   // codes, then the scales padded to 16 bytes
+        return (size_t)pool->n_layers * 2 *
+               ((size_t)pool->block_size * pool->n_kv_heads * pool->head_dim + ((size_t)pool->n_kv_heads * 4 + 15) / 16 * 16);
     return (size_t)pool->n_layers * 2 * pool->block_size * pool->n_kv_heads * pool->head_dim * sizeof(uint16_t);
 }
 
@@ -155,7 +221,26 @@ int pf_copy_blocks(const pf_pool *pool, const int32_t *src_ids, const int32_t *d
     if (n < 0) return pkv::set_error(PF_ERR_INVALID, "pf_copy_blocks: negative count");
     if (n == 0) return PF_OK;
     if (!src_ids || !dst_ids) return pkv::set_error(PF_ERR_INVALID, "pf_copy_blocks: null id array");
-    pkv::BlockCopyArgs a{pool, src_ids, dst_ids, nullptr, n};
+    pkv::BlockCopyArgs a{pool, src_ids, dst_ids, nullptr, n, nullptr, nullptr, 0, 0, nullptr};
+    return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
+}
+
+int pf_compact_blocks(const pf_pool *pool, const int32_t *src_ids, const int32_t *dst_ids, int n,
+                      const int32_t *block_map, int32_t *block_tables, int n_table_rows, int max_blocks_per_seq,
+                      const int32_t *context_lens, void *stream) {
+    pkv::clear_error();
+    if (!pool) return pkv::set_error(PF_ERR_INVALID, "pf_compact_blocks: pool is null");
+    if (n < 0 || n_table_rows < 0) return pkv::set_error(PF_ERR_INVALID, "pf_compact_blocks: negative count");
+    if (n > 0 && (!src_ids || !dst_ids)) return pkv::set_error(PF_ERR_INVALID, "pf_compact_blocks: null id array");
+    if (n_table_rows > 0) {
+        if (!block_map || !block_tables || !context_lens)
+            return pkv::set_error(PF_ERR_INVALID, "pf_compact_blocks: null pointer");
+        if (max_blocks_per_seq <= 0)
+            return pkv::set_error(PF_ERR_INVALID, "pf_compact_blocks: max_blocks_per_seq must be positive");
+    }
+    if (n == 0 && n_table_rows == 0) return PF_OK;
+    pkv::BlockCopyArgs a{pool,   src_ids, dst_ids, nullptr, n, block_map, n_table_rows > 0 ? block_tables : nullptr,
+                         n_table_rows, max_blocks_per_seq, context_lens};
     return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -186,7 +271,7 @@ int pf_swap_out(const pf_pool *pool, const int32_t *ids, int n, void *host_dst, 
     void *img = nullptr;
     int rc = host_image_ptr(host_dst, &img, "pf_swap_out");
     if (rc) return rc;
-    pkv::BlockCopyArgs a{pool, ids, nullptr, img, n};
+    pkv::BlockCopyArgs a{pool, ids, nullptr, img, n, nullptr, nullptr, 0, 0, nullptr};
     return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -199,7 +284,7 @@ int pf_swap_in(const pf_pool *pool, const void *host_src, const int32_t *ids, in
     void *img = nullptr;
     int rc = host_image_ptr(host_src, &img, "pf_swap_in");
     if (rc) return rc;
-    pkv::BlockCopyArgs a{pool, nullptr, ids, img, n};
+    pkv::BlockCopyArgs a{pool, nullptr, ids, img, n, nullptr, nullptr, 0, 0, nullptr};
     return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -210,6 +295,16 @@ size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads,
         n_q_heads % pool->n_kv_heads) {
         pkv::set_error(PF_ERR_INVALID, "pf_decode_workspace_bytes: bad arguments");
         return 0;
+    }
+    if (pool->dtype == PF_E4M3) {
+        const int group = n_q_heads / pool->n_kv_heads;
+        if (group > pkv::kMaxRows || split_tokens != 0) {
+            pkv::set_error(PF_ERR_UNSUPPORTED, "pf_decode_workspace_bytes: PF_E4M3 pools take split_tokens = 0 and "
+                                               "at most 16 q-heads per kv-head");
+            return 0;
+        }
+        pkv::RowsPlan rows;
+        return pkv::rows_plan(pool, group, false, &rows) == PF_OK ? rows.bytes : 0;
     }
     pkv::AttnPlan plan;
     if (pkv::attention_plan(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens, false, &plan)) return 0;
@@ -223,6 +318,22 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
     cudaError_t e = cudaMemsetAsync(workspace, 0, ws_bytes, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return pkv::cuda_error(e, "pf_decode_workspace_init: cudaMemsetAsync");
     return PF_OK;
+}
+
+// The few-rows kernel with a checked workspace (decode and short appends over
+// PF_E4M3 pools, short cross attention).
+static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const char *fn, void *stream) {
+    if (!aligned16(workspace))
+        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace must be 16-byte aligned");
+    if (a.max_blocks <= 0 || (long long)a.max_blocks * a.pool->block_size > (1ll << 30))
+        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad max_blocks_per_seq");
+    int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan);
+    if (rc) return rc;
+    if (ws_bytes < a.plan.bytes)
+        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
+                                                  " bytes, needs " + std::to_string(a.plan.bytes));
+    a.workspace = workspace;
+    return pkv::launch_rows(a, static_cast<cudaStream_t>(stream));
 }
 
 // Checks and launch shared by pf_paged_decode_attention (k_new = v_new =
@@ -246,7 +357,7 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
         return pkv::set_error(PF_ERR_INVALID,
                               "pf_paged_decode_attention: n_q_heads must be a positive multiple of n_kv_heads");
     int group = n_q_heads / pool->n_kv_heads;
-    if (group > 16 || (group > 8 && (split_tokens != 0 || pool->block_size < 16)))
+    if (group > 16 || (group > 8 && (split_tokens != 0 || (pool->block_size < 16 && pool->dtype == PF_F16))))
         return pkv::set_error(PF_ERR_UNSUPPORTED,
                               "pf_paged_decode_attention: at most 8 q-heads per kv-head are built (16 with "
                               "split_tokens = 0 and pages of at least 16 tokens)");
@@ -254,6 +365,29 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
         return pkv::set_error(PF_ERR_INVALID, "pf_paged_decode_attention: max_blocks_per_seq must be positive");
     if (!(scale > 0.0f) || scale != scale)
         return pkv::set_error(PF_ERR_INVALID, "pf_paged_decode_attention: scale must be a positive number");
+    if (pool->dtype == PF_E4M3) {
+        if (split_tokens != 0)
+            return pkv::set_error(PF_ERR_UNSUPPORTED,
+                                  "pf_paged_decode_attention: PF_E4M3 pools take split_tokens = 0");
+        pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, nullptr, n_seqs, n_q_heads,
+                        group, true, scale, out, out_dtype, {}, nullptr};
+        if (k_new) {
+            // the append first: a launch of its own, since a page's new scale is needed before any of its rows
+            pkv::AppendArgs w{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, nullptr,
+                              n_seqs, 1};
+            pkv::RowsPlan plan8;
+            rc = pkv::rows_plan(pool, group, true, &plan8);
+            if (rc) return rc;
+            if (ws_bytes < plan8.bytes)   // nothing is launched by a call that fails
+                return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: workspace has " + std::to_string(ws_bytes) +
+                                                          " bytes, needs " + std::to_string(plan8.bytes));
+            if ((long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
+                return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: bad max_blocks_per_seq");
+            rc = pkv::launch_append(w, static_cast<cudaStream_t>(stream));
+            if (rc) return rc;
+        }
+        return rows_call(a, workspace, ws_bytes, "pf_paged_decode_attention", stream);
+    }
     pkv::AttnPlan plan;
     // host-only checks first (no device query), then the device-sized plan
     rc = pkv::attention_plan(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens, false, &plan);
@@ -310,7 +444,7 @@ int pf_decode_step(const pf_pool *pool, int layer, const void *q, const void *k_
 static int append_rows(const pf_pool *pool, int n_q_heads, int max_new_tokens) {
     if (n_q_heads <= 0 || n_q_heads % pool->n_kv_heads) return 0;
     const long long rows = (long long)max_new_tokens * (n_q_heads / pool->n_kv_heads);
-    const int cap = pool->block_size >= 16 ? 16 : 8;
+    const int cap = pool->block_size >= 16 || pool->dtype == PF_E4M3 ? 16 : 8;
     return rows >= 1 && rows <= cap ? (int)rows : 0;
 }
 
@@ -323,6 +457,10 @@ size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads
     }
     const int rows = append_rows(pool, n_q_heads, max_new_tokens);
     if (rows == 0) return 0;   // the call takes the kernel that needs no workspace
+    if (pool->dtype == PF_E4M3) {
+        pkv::RowsPlan plan8;
+        return pkv::rows_plan(pool, rows, false, &plan8) == PF_OK ? plan8.bytes : 0;
+    }
     pkv::AttnPlan plan;
     // sized like pf_decode_workspace_bytes: by the resident grid, or by a
     // bound on it when no device can be queried
@@ -357,6 +495,11 @@ int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, co
     if (!(scale > 0.0f) || scale != scale)
         return pkv::set_error(PF_ERR_INVALID, "pf_paged_prefill_attention: scale must be a positive number");
     const int rows = append_rows(pool, n_q_heads, max_new_tokens);
+    if (workspace != nullptr && rows > 0 && pool->dtype == PF_E4M3) {
+        pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
+                        rows, true, scale, out, out_dtype, {}, nullptr};
+        return rows_call(a, workspace, ws_bytes, "pf_paged_prefill_attention", stream);
+    }
     if (workspace != nullptr && rows > 0) {
         // The decode kernel, its G rows per kv-head being the query tokens x
         // q-heads: balanced spans over the contexts, merged in the kernel.
@@ -376,7 +519,63 @@ int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, co
         return pkv::launch_attention(a, static_cast<cudaStream_t>(stream));
     }
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_new_tokens,
-                       n_q_heads, scale, out, out_dtype};
+                       n_q_heads, scale, out, out_dtype, true};
+    return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+}
+
+// Rows per kv-head of cross attention on the few-rows kernel, 0 = too many.
+static int cross_rows(const pf_pool *pool, int n_q_heads, int max_q_tokens) {
+    if (n_q_heads <= 0 || n_q_heads % pool->n_kv_heads) return 0;
+    const long long rows = (long long)max_q_tokens * (n_q_heads / pool->n_kv_heads);
+    return rows >= 1 && rows <= pkv::kMaxRows ? (int)rows : 0;
+}
+
+size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                                int max_q_tokens) {
+    pkv::clear_error();
+    if (!pool || n_seqs < 0 || max_blocks_per_seq <= 0 || max_q_tokens < 0) {
+        pkv::set_error(PF_ERR_INVALID, "pf_cross_workspace_bytes: bad arguments");
+        return 0;
+    }
+    const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
+    if (rows == 0) return 0;   // the call takes the kernel that needs no workspace
+    pkv::RowsPlan plan;
+    return pkv::rows_plan(pool, rows, false, &plan) == PF_OK ? plan.bytes : 0;
+}
+
+int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q, int n_seqs,
+                             int max_q_tokens, int n_q_heads, float scale, void *out, int out_dtype, void *workspace,
+                             size_t ws_bytes, void *stream) {
+    pkv::clear_error();
+    int rc = check_pool(pool, layer, "pf_paged_cross_attention");
+    if (rc) return rc;
+    if (n_seqs < 0 || max_q_tokens < 0)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: negative n_seqs or max_q_tokens");
+    if (n_seqs == 0 || max_q_tokens == 0) return PF_OK;
+    if (!q || !block_tables || !context_lens || !cu_q || !out)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: null pointer");
+    if (!aligned16(q) || !aligned16(out))
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: q and out must be 16-byte aligned");
+    if (out_dtype != PF_F16 && out_dtype != PF_F32)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: out_dtype must be PF_F16 or PF_F32");
+    if (n_q_heads <= 0 || n_q_heads % pool->n_kv_heads)
+        return pkv::set_error(PF_ERR_INVALID,
+                              "pf_paged_cross_attention: n_q_heads must be a positive multiple of n_kv_heads");
+    if (n_q_heads / pool->n_kv_heads > pkv::kMaxRows)
+        return pkv::set_error(PF_ERR_UNSUPPORTED, "pf_paged_cross_attention: at most 16 q-heads per kv-head are built");
+    if (max_blocks_per_seq <= 0 || (long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: bad max_blocks_per_seq");
+    if (!(scale > 0.0f))
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: scale must be a positive number");
+    const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
+    if (workspace != nullptr && rows > 0) {
+        pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
+                        rows, false, scale, out, out_dtype, {}, nullptr};
+        return rows_call(a, workspace, ws_bytes, "pf_paged_cross_attention", stream);
+    }
+    pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_q_tokens,
+                       n_q_heads, scale, out, out_dtype, false};
     return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
 }
 

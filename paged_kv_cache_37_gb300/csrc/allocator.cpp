@@ -16,6 +16,10 @@
 // a fresh block for a block others still reference and patches only the
 // writer's table entry; the caller copies the contents (pf_copy_blocks).
 //
+// Compaction packs the referenced blocks into the lowest ids: a block above
+// the live count moves into a hole below it (both in ascending order, so a
+// destination is never a source), its references with it.
+//
 // shuffle_seed != 0 permutes the initial hand-out order (a pool after churn,
 // PageFault README "Four stages") with Fisher-Yates driven by SplitMix64
 // (Steele, Lea and Flood, OOPSLA 2014), drawing j uniform in [0, i] by
@@ -182,6 +186,30 @@ int pf_alloc_cow(pf_alloc *a, int32_t *entry, int32_t *src_out, int32_t *dst_out
     --a->refs[b];
     *entry = d;
     *dst_out = d;
+    return PF_OK;
+}
+
+int pf_alloc_compact(pf_alloc *a, int32_t *src_out, int32_t *dst_out, int32_t *map_out, int *n_out) {
+    pkv::clear_error();
+    if (!a || !src_out || !dst_out || !map_out || !n_out)
+        return pkv::set_error(PF_ERR_INVALID, "pf_alloc_compact: null argument");
+    const int32_t live = a->n_blocks - (int32_t)a->stack.size();
+    int n = 0;
+    int32_t hole = 0;
+    for (int32_t b = 0; b < a->n_blocks; ++b) map_out[b] = b;
+    for (int32_t b = live; b < a->n_blocks; ++b) {
+        if (a->refs[b] == 0) continue;
+        while (a->refs[hole] != 0) ++hole;   // holes below the live count are as many as blocks above it
+        a->refs[hole] = a->refs[b];
+        a->refs[b] = 0;
+        map_out[b] = hole;
+        src_out[n] = b;
+        dst_out[n] = hole;
+        ++n;
+    }
+    // the free ids are live .. n_blocks - 1, the lowest handed out next
+    for (size_t i = 0; i < a->stack.size(); ++i) a->stack[i] = a->n_blocks - 1 - (int32_t)i;
+    *n_out = n;
     return PF_OK;
 }
 

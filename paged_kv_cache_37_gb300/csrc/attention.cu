@@ -203,11 +203,6 @@ int resident_grid(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_core
 // Merge-job stamp of each main-kernel launch (never 0, so a zeroed
 // workspace holds no job of any launch).
 std::atomic<unsigned> g_epoch{0};
-unsigned next_epoch() {
-    unsigned e = ++g_epoch;
-    if (e == 0) e = ++g_epoch;
-    return e;
-}
 
 // Grid bound used to size span records when no device can be queried.
 constexpr int kGridBoundNoDevice = 4096;
@@ -219,6 +214,12 @@ std::atomic<int> g_inject_timeout{0};
 
 
 }  // namespace
+
+unsigned next_epoch() {
+    unsigned e = ++g_epoch;
+    if (e == 0) e = ++g_epoch;
+    return e;
+}
 
 int attention_plan(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks, int split_tokens,
                    bool need_device, AttnPlan *plan) {

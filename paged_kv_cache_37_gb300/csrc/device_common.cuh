@@ -290,6 +290,13 @@ __device__ __forceinline__ void st_stream(uint4 *p, uint4 v) {
                  : "memory");
 }
 
+// Two e4m3 codes (the low 16 bits) -> fp16, exact.
+__device__ __forceinline__ __half2 widen_e4m3(uint32_t pair) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)pair));
+    return *reinterpret_cast<const __half2 *>(&h);
+}
+
 // Eight fp16 values packed in a uint4 -> eight floats (exact).
 __device__ __forceinline__ void half8_to_float(const uint4 &v, float (&f)[8]) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&v);

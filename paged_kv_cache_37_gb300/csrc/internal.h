@@ -42,6 +42,9 @@ struct pf_pool {
     int n_kv_heads;
     int head_dim;
     int dtype;
+    // PF_E4M3 pools: fp32 scales [n_layers][n_blocks][n_kv_heads], else null
+    float *k_scale;
+    float *v_scale;
     // TMA descriptors over K and V viewed as [rows][n_kv_heads][head_dim]
     // with rows = n_layers * n_blocks * block_size, encoded lazily per device.
     std::mutex mu;
@@ -82,6 +85,21 @@ struct WriteArgs {
 };
 int launch_write_kv(const WriteArgs &a, cudaStream_t stream);
 
+// Quantising append into a PF_E4M3 pool (pf_append_kv).
+struct AppendArgs {
+    const pf_pool *pool;
+    int layer;
+    const void *k_new;
+    const void *v_new;
+    const int32_t *block_tables;
+    int max_blocks;
+    const int32_t *context_lens;
+    const int32_t *cu_new;   // null: one token per sequence with a context, row s
+    int n_seqs;
+    int max_new;
+};
+int launch_append(const AppendArgs &a, cudaStream_t stream);
+
 // Whole-block copies: pool -> pool (both id arrays set), pool -> image
 // (dst_ids null: destination i is image i of `image`), image -> pool
 // (src_ids null).  Ids are device int32 arrays of n entries.
@@ -91,10 +109,17 @@ struct BlockCopyArgs {
     const int32_t *dst_ids;
     const void *image;   // device-accessible address of the host images
     int n;
+    // compaction: entries of the tables that a context uses go through
+    // block_map in the same launch (null: no tables)
+    const int32_t *block_map;
+    int32_t *block_tables;
+    int n_rows;
+    int max_blocks;
+    const int32_t *context_lens;
 };
 int launch_block_copy(const BlockCopyArgs &a, cudaStream_t stream);
 
-// Multi-token append attention (pf_paged_prefill_attention).
+// Multi-token attention (pf_paged_prefill_attention, pf_paged_cross_attention).
 struct PrefillArgs {
     const pf_pool *pool;
     int layer;
@@ -109,8 +134,9 @@ struct PrefillArgs {
     float scale;
     void *out;
     int out_dtype;
+    bool causal;   // the queries are the context's last tokens
 };
-int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu
+int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu (causal, fp16 pools)
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);   // prefill_tc.cu
 
 struct GatherArgs {
@@ -125,6 +151,41 @@ struct GatherArgs {
     void *v_out;
 };
 int launch_gather_kv(const GatherArgs &a, cudaStream_t stream);
+int launch_gather_e4m3(const GatherArgs &a, cudaStream_t stream);
+
+// Stamp of each launch that leaves records of cut work in a workspace (never
+// 0, so a zeroed workspace holds none of any launch).
+unsigned next_epoch();
+
+// Attention of at most kMaxRows query rows per (sequence, kv-head):
+// rows_attention.cuh.  Every schedule detail follows from the device and the
+// rows; the workspace holds the parts of cut sequences.
+constexpr int kMaxRows = 16;
+struct RowsPlan {
+    int grid;
+    size_t counter_bytes;
+    size_t bytes;   // of the workspace
+};
+int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan);
+struct RowsArgs {
+    const pf_pool *pool;
+    int layer;
+    const void *q;
+    const int32_t *block_tables;
+    int max_blocks;
+    const int32_t *context_lens;
+    const int32_t *cu_q;   // null: one query per sequence, row s
+    int n_seqs;
+    int n_q_heads;
+    int rows;              // most query tokens of a sequence x q-heads per kv-head
+    bool causal;           // the queries are the context's last tokens
+    float scale;
+    void *out;
+    int out_dtype;
+    RowsPlan plan;
+    void *workspace;
+};
+int launch_rows(const RowsArgs &a, cudaStream_t stream);
 
 // How an attention call is scheduled and what workspace it needs.
 struct AttnPlan {

@@ -1,7 +1,8 @@
 // prefill_tc.cu -- prompt attention through the block tables on the
 // fifth-generation tensor cores: tcgen05.mma with fp32 accumulators in
 // tensor memory (pf_paged_prefill_attention calls with 128 or more query
-// rows per (sequence, kv-head)).
+// rows per (sequence, kv-head)); also, in instances of their own, over e4m3
+// pools and without the causal limit (pf_paged_cross_attention).
 //
 // Sequence s has L_s tokens, the last n_s of them new (PagedAttention blog,
 // "Architecture": append into the last block, then attend); the query of new
@@ -44,6 +45,13 @@
 // 4 warps -> 11.8, 23.4, 44 bytes a cycle per SM on 8 KB boxes), hence two
 // loader warps per tensor; 16-byte cp.async from the loader warps was several
 // times slower than TMA.
+//
+// e4m3 pools (Q8): the loader warps bring each tile's codes into a ring of
+// raw stages by 16-byte cp.async (a lane copies the chunks that it widens
+// itself), widen them to fp16, multiply by the page's scale (exact but where
+// the product falls below fp16's smallest normal, then off by at most 2^-25)
+// and store them into the swizzled stage that the MMAs read; rows past the
+// last position are zero-filled.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -71,20 +79,24 @@ constexpr int REG_SOFTMAX = 200;
 constexpr int REG_OTHER = 56;
 static_assert(2 * 128 * REG_SOFTMAX + 2 * 128 * REG_OTHER == NTHREADS * 128, "the split is the launch's registers");
 static_assert(32 * (2 * REG_SOFTMAX + 2 * REG_OTHER) <= 16384, "a sub-partition's registers");
-constexpr int NS = 4;            // K/V stages
+constexpr int kRawStages = 3;    // e4m3: raw K/V stages
 constexpr int TMEM_COLS = 512;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr unsigned FULL = 0xffffffffu;
 
-template <int D>
+template <int D, bool Q8>
 struct Cfg {
+    static constexpr int NS = Q8 ? 3 : 4;               // K/V stages
     static constexpr int BN = D == 64 ? 128 : 64;       // tokens per K/V tile (the scores' N)
     static constexpr int HALVES = D / 64;               // 64-element halves of a row
     static constexpr int Q_BYTES = QT * D * 2;          // one query tile
     static constexpr int KV_BYTES = BN * D * 2;         // one K or V tile
     static constexpr int OFF_K = 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
-    static constexpr int DATA = OFF_V + NS * KV_BYTES;
+    static constexpr int OFF_RAW = OFF_V + NS * KV_BYTES;
+    // e4m3: codes of a K or V tile, then the scales of its tokens
+    static constexpr int RAW_BYTES = Q8 ? BN * D + BN * 4 : 0;
+    static constexpr int DATA = OFF_RAW + 2 * kRawStages * RAW_BYTES;
     static constexpr int SMEM = DATA + 1024;            // slack to align the base to 1024 bytes
     // tensor memory (fp32 columns): S of query tile g at g BN, O of tile g at
     // 2 BN + g D, and the fp16 weights P of tile g, two per column (token 2c
@@ -97,8 +109,10 @@ struct Cfg {
 
 struct Params {
     const __half *q;
-    const __half *k_pool;
-    const __half *v_pool;
+    const void *k_pool;
+    const void *v_pool;
+    const float *k_scale;   // e4m3 pools
+    const float *v_scale;
     void *out;
     const int32_t *bt;
     const int32_t *lens;
@@ -115,15 +129,16 @@ struct Params {
     int n_items;      // sequences x kv-heads
     int n_qp;         // 256-row tiles of the longest (sequence, kv-head)
     long long layer_row0;
+    long long layer_page0;   // layer * n_blocks
     int out_f32;
     float scale_log2;
 };
 
 struct Bars {
-    unsigned long long k_full[NS];
-    unsigned long long v_full[NS];
-    unsigned long long k_empty[NS];
-    unsigned long long v_empty[NS];
+    unsigned long long k_full[4];
+    unsigned long long v_full[4];
+    unsigned long long k_empty[4];
+    unsigned long long v_empty[4];
     unsigned long long s_full[2];
     unsigned long long s_free[2];
     unsigned long long p_full[2];
@@ -274,12 +289,21 @@ __device__ __forceinline__ uint32_t swz(int t, int c, int rows) {
     return (uint32_t)((((c >> 3) * rows + t) << 7) + (((c & 7) ^ (t & 7)) << 4));
 }
 
-template <int D>
+// 16-byte cp.async that reads `bytes` (16 or 0) and zero-fills the rest.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t smem, const void *gmem, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t smem, const void *gmem, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+
+template <int D, bool CAUSAL, bool Q8>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const Params p) {
-    using C = Cfg<D>;
+    using C = Cfg<D, Q8>;
     constexpr int BN = C::BN;
+    constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -304,15 +328,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     const int q0 = p.cu_q[s];
     int n = p.cu_q[s + 1] - q0;
-    if (n < 0 || n > L || n > p.max_new) {
+    if (n < 0 || (CAUSAL && n > L) || n > p.max_new) {
         if (flagger) atomicOr(p.status, PF_DEV_BAD_LENGTH);
-        n = n < 0 ? 0 : min(min(n, L), p.max_new);
+        n = n < 0 ? 0 : min(CAUSAL ? min(n, L) : n, p.max_new);
     }
     const int rows = n * p.gh;
     const int r0 = qp * 2 * QT;
     if (r0 >= rows) return;                  // the whole CTA: no row here
     const int r_end = min(r0 + 2 * QT, rows);
-    const int base = L - n;                  // position of new token 0
+    if (!CAUSAL && L == 0) {                 // nothing to attend to: zeros
+        const size_t o0 = ((size_t)q0 * p.n_q_heads + (size_t)h * p.gh) * D;
+        for (int e = threadIdx.x; e < (r_end - r0) * (D / 8); e += NTHREADS) {
+            const int r = r0 + e / (D / 8);
+            const size_t o = o0 + ((size_t)(r / p.gh) * p.n_q_heads + r % p.gh) * D + e % (D / 8) * 8;
+            if (p.out_f32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + o);
+                dst[0] = dst[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + o) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        return;
+    }
+    const int base = L - n;                  // position of new token 0 (causal)
     // per query tile: its last position and its number of K/V tiles
     int nt[2], pmax[2];
 #pragma unroll
@@ -322,7 +360,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             nt[g] = 0;
             pmax[g] = 0;
         } else {
-            pmax[g] = base + (min(gr0 + QT, r_end) - 1) / p.gh;
+            pmax[g] = CAUSAL ? base + (min(gr0 + QT, r_end) - 1) / p.gh : L - 1;
             nt[g] = pmax[g] / BN + 1;
         }
     }
@@ -341,7 +379,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int r = r0 + g * QT + t;
     const bool valid = warp < SOFTMAX_WARPS && r < r_end;
     const int i = valid ? r / p.gh : 0;
-    const int lim = valid ? base + i : pmax[g];                // last position this row sees
+    const int lim = CAUSAL && valid ? base + i : pmax[g];      // last position this row sees
     const size_t ob = valid ? ((size_t)(q0 + i) * p.n_q_heads + (size_t)h * p.gh + (r - i * p.gh)) * D : 0;
     if (warp < SOFTMAX_WARPS) {
         const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ob);
@@ -359,7 +397,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int box = p.box_rows;
     auto n_boxes = [&](int j) { return min(BN / box, (p_max - j * BN) / box + 1); };
     auto raw_id = [&](int j) {
-        return (p.block_size >= 16 && j < ntt && lane < n_boxes(j)) ? bt_row[(j * BN + lane * box) / p.block_size] : 0;
+        return (!Q8 && p.block_size >= 16 && j < ntt && lane < n_boxes(j)) ? bt_row[(j * BN + lane * box) / p.block_size] : 0;
     };
     // Loaders (two warps for K, two for V, each issuing every other page
     // box of a tile; a stage is refilled once the MMAs of the tile that used
@@ -373,7 +411,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     unsigned long long *full = is_v ? bars.v_full : bars.k_full;
     unsigned long long *empty = is_v ? bars.v_empty : bars.k_empty;
     const uint32_t s_base = is_v ? s_v : s_k;
-    const __half *pool_base = is_v ? p.v_pool : p.k_pool;
+    const __half *pool_base = static_cast<const __half *>(is_v ? p.v_pool : p.k_pool);
     const int B = p.block_size;
     int issued = 0;
     // tile j into its stage (box `lane` from block id `id`); false if a wait ran out
@@ -418,23 +456,112 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ++issued;
         return true;
     };
+    // e4m3: the tile's 512 16-byte chunks are dealt to the 64 lanes of the
+    // tensor's two warps; chunk i of a lane is of token 2 TPI i + TPI li +
+    // lane / CPR.  Lane l looks up the block ids (one tile ahead of their
+    // copy) and copies the scales of the warp's tokens l, l + 32 (in order).
+    constexpr int CPR = D / 16;                              // chunks of a row of codes
+    constexpr int TPI = 32 / CPR;                            // tokens of a warp per chunk index
+    constexpr int TW = BN / 2;                               // tokens of a warp
+    constexpr int IDS = TW / 32;
+    const uint32_t raw = smem_addr(sm + C::OFF_RAW) + (is_v ? kRawStages * C::RAW_BYTES : 0);
+    const float *scale_base = is_v ? p.v_scale : p.k_scale;
+    int q_id[IDS];                                           // raw ids of the next tile to copy (-2: no token)
+    auto tile_token = [&](int lt) { return lt / TPI * (2 * TPI) + li * TPI + lt % TPI; };
+    auto q8_look_up = [&](int j) {
+#pragma unroll
+        for (int k = 0; k < IDS; ++k) {
+            const int tok = j * BN + tile_token(lane + 32 * k);
+            q_id[k] = tok <= p_max ? bt_row[tok / B] : -2;
+        }
+    };
+    auto q8_copy = [&](int j) {                              // tile j into raw stage j mod kRawStages
+        const uint32_t dst = raw + (uint32_t)(j % kRawStages) * C::RAW_BYTES;
+        if (j < ntt) {
+            int row[IDS];
+#pragma unroll
+            for (int k = 0; k < IDS; ++k) {
+                int id = q_id[k];
+                const int lt = lane + 32 * k;
+                if (id != -2 && (id < 0 || id >= p.n_blocks)) {
+                    atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                    id = -2;
+                }
+                row[k] = id < 0 ? -1 : (int)(p.layer_row0 + (long long)id * B + (j * BN + tile_token(lt)) % B);
+                cp_async4_zfill(dst + BN * D + (li * TW + lt) * 4,
+                                scale_base + (id < 0 ? 0 : (size_t)(p.layer_page0 + id) * p.n_kv_heads + h),
+                                id < 0 ? 0u : 4u);
+            }
+            const uint8_t *codes = reinterpret_cast<const uint8_t *>(pool_base);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int lt = i * TPI + lane / CPR;
+                const int r8 = __shfl_sync(FULL, row[i * TPI / 32], lt % 32);
+                cp_async16_zfill(dst + (tile_token(lt) * CPR + lane % CPR) * 16,
+                                 codes + (r8 < 0 ? 0 : ((size_t)r8 * p.n_kv_heads + h) * D + lane % CPR * 16),
+                                 r8 < 0 ? 0u : 16u);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (j + 1 < ntt) q8_look_up(j + 1);
+    };
+    // tile j from its raw stage into its swizzled stage; false if a wait ran out
+    auto q8_widen = [&](int j) -> bool {
+        const uint32_t src = raw + (uint32_t)(j % kRawStages) * C::RAW_BYTES;
+        const int st = j % NS;
+        const uint32_t dst = s_base + st * C::KV_BYTES;
+        if (j >= NS && !wait_lanes(bar(empty[st]), ((j / NS) - 1) & 1, p.status)) return false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int lt = i * TPI + lane / CPR;
+            const int tk = tile_token(lt), c = lane % CPR;
+            uint32_t w[4];
+            float f;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(src + (tk * CPR + c) * 16));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(src + BN * D + (li * TW + lt) * 4));
+            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 v = __hmul2(widen_e4m3(w[2 * k + e / 2] >> (16 * (e & 1))), f2);
+                    x[e] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + swz(tk, 2 * c + k, BN)), "r"(x[0]),
+                             "r"(x[1]), "r"(x[2]), "r"(x[3])
+                             : "memory");
+            }
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(bar(full[st]));
+        return true;
+    };
     int id0 = 0, id1 = 0;
     if (loader) {
         if (warp == LOAD_WARP0 && lane == 0) {
             // two loader warps arrive on each full barrier
             for (int k = 0; k < NS; ++k) {
-                mbar_init(bar(bars.k_full[k]), B >= 16 ? 2u : 64u);
-                mbar_init(bar(bars.v_full[k]), B >= 16 ? 2u : 64u);
+                mbar_init(bar(bars.k_full[k]), !Q8 && B >= 16 ? 2u : 64u);
+                mbar_init(bar(bars.v_full[k]), !Q8 && B >= 16 ? 2u : 64u);
                 mbar_init(bar(bars.k_empty[k]), 1);
                 mbar_init(bar(bars.v_empty[k]), 1);
             }
             mbar_init_fence();
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");   // the loader warps: barriers initialised
-        prefetch_tensormap(map);
-        id0 = raw_id(0);
-        id1 = raw_id(1);
-        if (B >= 16) {
+        if constexpr (Q8) {
+            q8_look_up(0);
+#pragma unroll
+            for (int j = 0; j < kRawStages - 1; ++j) q8_copy(j);
+        } else {
+            prefetch_tensormap(map);
+            id0 = raw_id(0);
+            id1 = raw_id(1);
+        }
+        if (!Q8 && B >= 16) {
             const int id = id0;
             id0 = id1;
             id1 = raw_id(2);
@@ -591,14 +718,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
     } else if (loader) {
         // ---------------------------------------------------------- loaders
-        for (int j = issued; j < ntt; ++j) {
+        if constexpr (Q8) {
+            for (int j = 0; j < ntt; ++j) {
+                __syncwarp();                                  // the raw stage of tile j - 1 has been read
+                q8_copy(j + kRawStages - 1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRawStages - 1) : "memory");
+                __syncwarp();
+                if (!q8_widen(j)) break;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        for (int j = Q8 ? ntt : issued; j < ntt; ++j) {
             int id = id0;
             id0 = id1;
             id1 = raw_id(j + 2);
             if (!load_tile(j, id)) break;
         }
         // copies still in flight (only after a wait ran out) land before the CTA exits
-        if (B >= 16) {
+        if (!Q8 && B >= 16) {
             for (int j = max(0, issued - NS); j < issued; ++j) wait_lanes(bar(full[j % NS]), (j / NS) & 1, p.status);
         }
     } else if (warp == MMA_S_WARP) {
@@ -639,7 +776,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int j = 0; ok && j < ntt; ++j) {
             const int st = j % NS;
             if (!wait_lanes(bar(bars.v_full[st]), (j / NS) & 1, p.status)) break;
-            if (j == ntt - 1 && p_max - j * BN < BN - 1) {
+            if (!Q8 && j == ntt - 1 && p_max - j * BN < BN - 1) {
                 // V rows past the CTA's last position: zeros (a zero weight
                 // times a non-finite value would not vanish)
                 uint8_t *vt = sm + C::OFF_V + st * C::KV_BYTES;
@@ -728,12 +865,27 @@ int encode(CUtensorMap *map, void *base, const pf_pool *pool, int box_rows) {
 }  // namespace
 }  // namespace prefill_tc
 
+namespace prefill_tc {
+namespace {
+
+using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
+
+template <int D>
+KernelFn pick(bool causal, bool q8) {
+    if (q8) return causal ? prefill_tc_kernel<D, true, true> : prefill_tc_kernel<D, false, true>;
+    return causal ? prefill_tc_kernel<D, true, false> : prefill_tc_kernel<D, false, false>;
+}
+
+}  // namespace
+}  // namespace prefill_tc
+
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     int *status = device_status_ptr();
     if (!status) return PF_ERR_CUDA;
     pf_pool *pool = const_cast<pf_pool *>(a.pool);
     const int D = pool->head_dim;
-    const int BN = D == 64 ? prefill_tc::Cfg<64>::BN : prefill_tc::Cfg<128>::BN;
+    const bool q8 = pool->dtype == PF_E4M3;
+    const int BN = D == 64 ? prefill_tc::Cfg<64, false>::BN : prefill_tc::Cfg<128, false>::BN;
     const int gh = a.n_q_heads / pool->n_kv_heads;
     const long long n_items = (long long)a.n_seqs * pool->n_kv_heads;
     const long long n_qp = ((long long)a.max_new * gh + 2 * prefill_tc::QT - 1) / (2 * prefill_tc::QT);
@@ -744,7 +896,7 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: cudaGetDevice");
     if (dev < 0 || dev >= kMaxDevices) return set_error(PF_ERR_UNSUPPORTED, "device index out of range");
-    {
+    if (!q8) {   // e4m3 tiles are not copied by TMA
         std::lock_guard<std::mutex> lock(pool->mu);
         if (!pool->tmap_pf_ready[dev]) {
             int rc = prefill_tc::encode(&pool->tmap_pf_k[dev], pool->k_base, pool, box_rows);
@@ -756,8 +908,10 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     }
     prefill_tc::Params p;
     p.q = static_cast<const __half *>(a.q);
-    p.k_pool = static_cast<const __half *>(pool->k_base);
-    p.v_pool = static_cast<const __half *>(pool->v_base);
+    p.k_pool = pool->k_base;
+    p.v_pool = pool->v_base;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
     p.out = a.out;
     p.bt = a.block_tables;
     p.lens = a.context_lens;
@@ -773,12 +927,14 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     p.box_rows = box_rows;
     p.n_items = (int)n_items;
     p.n_qp = (int)n_qp;
-    p.layer_row0 = (long long)a.layer * pool->n_blocks * pool->block_size;
+    p.layer_page0 = (long long)a.layer * pool->n_blocks;
+    p.layer_row0 = p.layer_page0 * pool->block_size;
     p.out_f32 = a.out_dtype == PF_F32;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    void (*fn)(CUtensorMap, CUtensorMap, prefill_tc::Params) =
-        D == 64 ? prefill_tc::prefill_tc_kernel<64> : prefill_tc::prefill_tc_kernel<128>;
-    const int smem = D == 64 ? prefill_tc::Cfg<64>::SMEM : prefill_tc::Cfg<128>::SMEM;
+    const prefill_tc::KernelFn fn =
+        D == 64 ? prefill_tc::pick<64>(a.causal, q8) : prefill_tc::pick<128>(a.causal, q8);
+    const int smem = D == 64 ? (q8 ? prefill_tc::Cfg<64, true>::SMEM : prefill_tc::Cfg<64, false>::SMEM)
+                             : (q8 ? prefill_tc::Cfg<128, true>::SMEM : prefill_tc::Cfg<128, false>::SMEM);
     e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: cudaFuncSetAttribute");
     fn<<<(unsigned)(n_items * n_qp), prefill_tc::NTHREADS, smem, stream>>>(pool->tmap_pf_k[dev], pool->tmap_pf_v[dev],

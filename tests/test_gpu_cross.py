@@ -1,0 +1,119 @@
+"""Cross attention on the GPU against a plain 64-bit form: queries that see
+the whole of a context whose length is its own, over fp16 and e4m3 pages, on
+the few-rows kernel (with a workspace) and on the prompt kernel."""
+import numpy as np
+import pytest
+
+from e4m3_util import assert_within, attention64
+from gpu_util import PagedCase, dev, host
+from test_gpu_e4m3 import F16, F32, Case
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    # context lengths, query tokens, q-heads, kv-heads, head_dim, page, workspace
+    ([100, 0, 17, 1], [1, 2, 0, 3], 12, 12, 64, 16, True),
+    ([600, 33, 1], [2, 2, 1], 14, 2, 64, 64, True),
+    ([40, 90], [16, 3], 5, 5, 128, 1, True),
+    ([1, 700], [4, 4], 12, 3, 128, 256, True),
+    ([3000], [1], 2, 1, 128, 16, True),
+    ([2000], [5], 3, 1, 64, 16, True),
+    ([50, 0, 7], [5, 2, 0], 4, 4, 64, 16, False),             # few rows, no workspace
+    ([0, 129, 1, 64], [130, 300, 140, 0], 2, 2, 64, 16, True),  # more queries than context
+    ([512, 65], [100, 257], 8, 2, 128, 16, False),
+    ([200, 31], [64, 40], 6, 2, 64, 1, False),
+    ([700], [33], 4, 4, 128, 256, True),
+]
+
+
+@pytest.mark.parametrize("lens,new,hq,h,d,page,ws", CASES)
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32):
+    import torch
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    rng = np.random.default_rng(9)
+    q = rng.standard_normal((int(offs[-1]), hq, d)).astype(np.float16)
+    scale = float(np.float32(1.0 / np.sqrt(d)))
+    work_small = ws and max(new) * (hq // h) <= 16
+    step = 2.0 ** -21 if f32 and work_small else F16
+    if cache == "f16":
+        c = PagedCase(pkv, cuda_dev, lens, hq, h, d, page, n_layers=2)
+        pool, table, lens_dev = c.pool, c.bt_dev, c.lens_dev
+        # rows past a context's end hold what must not be read as numbers
+        for s, L in enumerate(lens):
+            for t in range(L, -(-L // page) * page):
+                for x in (c.k_dev, c.v_dev):
+                    x[1, c.bt[s, t // page], t % page] = float("nan")
+
+        def rows(x, s, L):
+            t = np.arange(L)
+            return x[1][c.bt[s][t // page], t % page]
+        got = [attention64(q[offs[s]:offs[s + 1]], rows(c.k_host, s, L), rows(c.v_host, s, L), scale, False, step,
+                           F32 if f32 else F16) for s, L in enumerate(lens)]
+        want, tol = np.concatenate([o for o, _ in got]), np.concatenate([t for _, t in got])
+    else:
+        c = Case(pkv, cuda_dev, lens, hq, h, d, page)
+        c.fill()
+        pool, table, lens_dev = c.pool, c.table_dev, dev(c.lens, cuda_dev)
+        want, tol = c.want(q, offs, False, step, F32 if f32 else F16)
+        tol = tol + 2.0 ** -25 + 2 * 2.0 ** -25 * scale * np.abs(q.astype(np.float64)).sum(-1).max() * 64
+    out = torch.full((int(offs[-1]) + 1, hq, d), 7.0, dtype=torch.float32 if f32 else torch.float16, device=cuda_dev)
+    work = pkv.make_cross_workspace(pool, len(lens), hq, table.shape[1], max(new)) if ws else None
+    assert (work is not None) == work_small
+    pkv.pf_device_status(reset=True)
+    for _ in range(2):
+        pkv.pf_paged_cross_attention(pool, 1, dev(q, cuda_dev), table, lens_dev, dev(offs, cuda_dev), max(new), scale,
+                                     out[:-1], work)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out)[:-1], want, tol)
+    assert bool((out[-1] == 7.0).all())
+
+
+def test_one_query_is_decode_attention(pkv, cuda_dev):
+    """A single query per sequence: the result of pf_paged_decode_attention, to the fp32 output's bound."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [300, 40, 1], 8, 4, 64, 16)
+    plain = host(c.attention(0.125, out_dtype=torch.float32)).astype(np.float64)
+    out = torch.empty((3, 8, 64), dtype=torch.float32, device=cuda_dev)
+    ws = pkv.make_cross_workspace(c.pool, 3, 8, c.bt.shape[1], 1)
+    pkv.pf_paged_cross_attention(c.pool, 0, c.q_dev, c.bt_dev, c.lens_dev, dev(np.arange(4, dtype=np.int32), cuda_dev),
+                                 1, 0.125, out, ws)
+    assert np.abs(host(out) - plain).max() <= 2e-5    # each within 1e-5 of the exact result
+
+
+def test_rows_of_shared_pages(pkv, cuda_dev):
+    """Several hypotheses of one input: table rows that name the same pages."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [200], 4, 4, 64, 16)
+    table = np.repeat(c.bt, 5, axis=0)
+    lens = np.full(5, 200, np.int32)
+    q = np.random.default_rng(1).standard_normal((5, 4, 64)).astype(np.float16)
+    out = torch.empty((5, 4, 64), dtype=torch.float16, device=cuda_dev)
+    ws = pkv.make_cross_workspace(c.pool, 5, 4, table.shape[1], 1)
+    pkv.pf_paged_cross_attention(c.pool, 0, dev(q, cuda_dev), dev(table, cuda_dev), dev(lens, cuda_dev),
+                                 dev(np.arange(6, dtype=np.int32), cuda_dev), 1, 0.125, out, ws)
+    t = np.arange(200)
+    k, v = (x[0][c.bt[0][t // 16], t % 16] for x in (c.k_host, c.v_host))
+    got = [attention64(q[i:i + 1], k, v, 0.125, False, F16, F16) for i in range(5)]
+    assert_within(host(out), np.concatenate([o for o, _ in got]), np.concatenate([t for _, t in got]))
+
+
+def test_flags(pkv, cuda_dev):
+    import torch
+    c = PagedCase(pkv, cuda_dev, [40, 40], 2, 2, 64, 16)
+    q = dev(np.zeros((6, 2, 64), np.float16), cuda_dev)
+    cu = dev(np.array([0, 3, 6], np.int32), cuda_dev)
+    ws = pkv.make_cross_workspace(c.pool, 2, 2, c.bt.shape[1], 3)
+    for work in (ws, None):
+        out = torch.empty_like(q)
+        pkv.pf_device_status(reset=True)
+        pkv.pf_paged_cross_attention(c.pool, 0, q, c.bt_dev, dev(np.array([40, 10 ** 6], np.int32), cuda_dev), cu, 3,
+                                     0.125, out, work)
+        assert pkv.pf_device_status(reset=True) == pkv.PF_DEV_BAD_LENGTH
+        pkv.pf_paged_cross_attention(c.pool, 0, q, c.bt_dev, c.lens_dev, cu, 2, 0.125, out, work)
+        assert pkv.pf_device_status(reset=True) == pkv.PF_DEV_BAD_LENGTH
+        bad = c.bt.copy()
+        bad[1, 1] = 10 ** 6
+        pkv.pf_paged_cross_attention(c.pool, 0, q, dev(bad, cuda_dev), c.lens_dev, cu, 3, 0.125, out, work)
+        assert pkv.pf_device_status(reset=True) == pkv.PF_DEV_BAD_BLOCK_ID
