@@ -122,6 +122,8 @@ def _check(rc):
 # --------------------------------------------------------------- helpers
 
 def _dev_ptr(t, name, dtype=None):
+    """Address of a contiguous CUDA tensor (an int: what ctypes takes for a
+    pointer argument without a wrapper object)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -131,28 +133,31 @@ def _dev_ptr(t, name, dtype=None):
         raise PagedKVError(PF_ERR_INVALID, f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise PagedKVError(PF_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream_ptr(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of torch's current stream; building the Stream object
+        # around it takes 2.9 us of a call's 11 (GB300 host), this 0.1
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
-def _on_current_device(pool, **tensors):
+def _on_current_device(pool, tensors):
     """The pool and these tensors lie on torch's current device (whose current
     stream the call takes by default)."""
     import torch
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for t in (pool.k_pool, *tensors):
         if t is not None and t.get_device() != dev:
-            raise PagedKVError(PF_ERR_INVALID, f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if pool.k_pool.get_device() != dev:
-        raise PagedKVError(PF_ERR_INVALID, f"the pool is on {pool.k_pool.device}, the current device is cuda:{dev}")
+            raise PagedKVError(PF_ERR_INVALID, f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def _host_i32(a, name):
@@ -362,8 +367,7 @@ def pf_compact_blocks(pool, src_ids, dst_ids, block_map, block_tables, context_l
         raise PagedKVError(PF_ERR_INVALID, "block_map must have n_blocks entries")
     if block_tables.dim() != 2 or context_lens.numel() != block_tables.shape[0]:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_rows, max_blocks]; context_lens [n_rows]")
-    _on_current_device(pool, src_ids=src_ids, dst_ids=dst_ids, block_map=block_map, block_tables=block_tables,
-                       context_lens=context_lens)
+    _on_current_device(pool, (src_ids, dst_ids, block_map, block_tables, context_lens))
     _check(lib().pf_compact_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32),
                                    _dev_ptr(dst_ids, "dst_ids", torch.int32), n,
                                    _dev_ptr(block_map, "block_map", torch.int32),
@@ -412,8 +416,10 @@ def pf_paged_prefill_attention(pool, layer, q, block_tables, context_lens, cu_q,
     n = context_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != n or cu_q.numel() != n + 1:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
-    if tuple(out.shape) != tuple(q.shape):
-        raise PagedKVError(PF_ERR_INVALID, "out must have the shape of q")
+    if tuple(out.shape) != tuple(q.shape) or q.shape[-1] != pool.head_dim:
+        raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out must have the shape of q")
+    if pool.k_scale is not None:
+        _on_current_device(pool, (q, block_tables, context_lens, cu_q, out, workspace))
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
@@ -445,8 +451,7 @@ def pf_paged_cross_attention(pool, layer, q, block_tables, context_lens, cu_q, m
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
-    _on_current_device(pool, q=q, block_tables=block_tables, context_lens=context_lens, cu_q=cu_q, out=out,
-                       workspace=workspace)
+    _on_current_device(pool, (q, block_tables, context_lens, cu_q, out, workspace))
     if q.numel() == 0:
         return
     _check(lib().pf_paged_cross_attention(
@@ -470,8 +475,7 @@ def pf_append_kv(pool, layer, k_new, v_new, block_tables, context_lens, cu_new, 
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
     if k_new.shape[0] != n if cu_new is None else cu_new.numel() != n + 1:
         raise PagedKVError(PF_ERR_INVALID, "cu_new must have n_seqs + 1 entries, or be None with one row per sequence")
-    _on_current_device(pool, k_new=k_new, v_new=v_new, block_tables=block_tables, context_lens=context_lens,
-                       cu_new=cu_new)
+    _on_current_device(pool, (k_new, v_new, block_tables, context_lens, cu_new))
     if k_new.numel() == 0:
         return
     _check(lib().pf_append_kv(pool.handle, layer, _dev_ptr(k_new, "k_new", torch.float16),
@@ -527,8 +531,10 @@ def pf_paged_decode_attention(pool, layer, q, block_tables, context_lens, scale,
     n, hq, d = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.numel() != n:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; context_lens [n_seqs]")
-    if tuple(out.shape) != (n, hq, d):
-        raise PagedKVError(PF_ERR_INVALID, "out must have the shape of q")
+    if tuple(out.shape) != (n, hq, d) or d != pool.head_dim:
+        raise PagedKVError(PF_ERR_INVALID, "q must be [n_seqs, n_q_heads, head_dim], out must have the shape of q")
+    if pool.k_scale is not None:
+        _on_current_device(pool, (q, block_tables, context_lens, out, workspace))
     if out.dtype == torch.float16:
         out_dtype = PF_F16
     elif out.dtype == torch.float32:
@@ -554,8 +560,10 @@ def pf_decode_step(pool, layer, q, k_new, v_new, block_tables, context_lens, sca
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; context_lens [n_seqs]")
     if tuple(k_new.shape) != (n, pool.n_kv_heads, d) or tuple(v_new.shape) != tuple(k_new.shape):
         raise PagedKVError(PF_ERR_INVALID, "k_new / v_new must be [n_seqs, n_kv_heads, head_dim]")
-    if tuple(out.shape) != (n, hq, d):
-        raise PagedKVError(PF_ERR_INVALID, "out must have the shape of q")
+    if tuple(out.shape) != (n, hq, d) or d != pool.head_dim:
+        raise PagedKVError(PF_ERR_INVALID, "q must be [n_seqs, n_q_heads, head_dim], out must have the shape of q")
+    if pool.k_scale is not None:
+        _on_current_device(pool, (q, k_new, v_new, block_tables, context_lens, out, workspace))
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")

@@ -58,12 +58,6 @@ struct AppendShape {
     static constexpr int GROUPS = kThreads / GT;
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Largest magnitude of the finite halves of w, as fp16 bits.
 __device__ __forceinline__ uint32_t finite_max(uint32_t w, bool &bad) {
     uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
@@ -76,13 +70,6 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t w, bool &bad) {
         hi = 0;
     }
     return max(lo, hi);
-}
-
-// 2^k, k the smallest integer >= -24 with amax <= 448 * 2^k (448 = 1.75 * 2^8).
-__device__ __forceinline__ float scale_for(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    const int k = (int)((b + 0x1fffffu) >> 23) - 127 - 8;   // one more when the mantissa is above 1.75
-    return __uint_as_float((uint32_t)(max(k, -24) + 127) << 23);
 }
 
 template <int B, int D>
@@ -155,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     }
     if (!live) return;
 
-    float scale = fmaxf(scale_for(__half2float(__ushort_as_half((unsigned short)top))), old);
+    float scale = fmaxf(e4m3_scale(__half2float(__ushort_as_half((unsigned short)top)), -24), old);
     const float inv = 1.0f / scale;                // exact: powers of two
     const float lim = fminf(448.0f, 61440.0f * inv);
     uint8_t *page_at = (kv ? p.v_pool : p.k_pool) + ((size_t)(p.layer_page0 + blk) * B * H + h) * D;

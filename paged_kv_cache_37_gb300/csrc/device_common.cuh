@@ -140,6 +140,19 @@ __device__ __forceinline__ unsigned long long ld_tagged(const unsigned long long
 __device__ __forceinline__ float tagged_value(unsigned long long w) { return __uint_as_float((unsigned)w); }
 __device__ __forceinline__ unsigned tagged_epoch(unsigned long long w) { return (unsigned)(w >> 32); }
 
+__device__ __forceinline__ void st_relaxed(unsigned *p, unsigned v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// A kernel launched as a programmatic dependent waits here for the kernels
+// before it (complete, their writes visible).
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 1-D bulk copy global -> shared, completing `bytes` on the mbarrier.
 // Both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -295,6 +308,20 @@ __device__ __forceinline__ __half2 widen_e4m3(uint32_t pair) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)pair));
     return *reinterpret_cast<const __half2 *>(&h);
+}
+
+// Two fp32 values -> e4m3 codes, nearest even, magnitudes above 448 to 448.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^k, k the smallest integer >= k_min with amax <= 448 * 2^k (448 = 1.75 *
+// 2^8: one more than the exponent minus 8 when the mantissa is above 1.75).
+__device__ __forceinline__ float e4m3_scale(float amax, int k_min) {
+    const int k = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 127 - 8;
+    return __uint_as_float((uint32_t)(max(k, k_min) + 127) << 23);
 }
 
 // Eight fp16 values packed in a uint4 -> eight floats (exact).

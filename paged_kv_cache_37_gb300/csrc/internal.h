@@ -163,7 +163,7 @@ unsigned next_epoch();
 constexpr int kMaxRows = 16;
 struct RowsPlan {
     int grid;
-    size_t counter_bytes;
+    size_t flag_bytes;
     size_t bytes;   // of the workspace
 };
 int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan);

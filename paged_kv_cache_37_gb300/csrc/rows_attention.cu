@@ -1,6 +1,6 @@
 // rows_attention.cu -- host side of rows_attention.cuh: the partition's grid,
 // the workspace and the launches.
-#include <mutex>
+#include <atomic>
 
 #include "rows_attention.cuh"
 
@@ -9,7 +9,7 @@ namespace {
 
 // SMs assumed when no device can be queried (sizes a workspace only).
 constexpr int kSmsNoDevice = 256;
-constexpr size_t kReserved = 256;   // front of every workspace, unused here
+constexpr size_t kReserved = 256;   // front of every workspace, unused
 
 // Warps per team: as many as 4 of the kv-heads, spread evenly over the groups
 // (5 heads: 3 + 2, so that one warp in six idles instead of three in eight).
@@ -19,16 +19,23 @@ int heads_per_team(int n_kv_heads) {
 }
 
 rows::Kernel kernel_for(const pf_pool *pool, int n_rows, bool f32) {
-    return pool->dtype == PF_E4M3 ? rows::kernel_e4m3(pool->head_dim, n_rows, f32)
-                                  : rows::kernel_f16(pool->head_dim, n_rows, f32);
+    const bool paged = pool->block_size >= 16;
+    if (pool->dtype == PF_E4M3)
+        return pool->head_dim == 64 ? rows::kernel_e4m3_d64(n_rows, f32, paged) : rows::kernel_e4m3_d128(n_rows, f32, paged);
+    return pool->head_dim == 64 ? rows::kernel_f16_d64(n_rows, f32, paged) : rows::kernel_f16_d128(n_rows, f32, paged);
 }
 
 }  // namespace
 
 int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan) {
+    static std::atomic<int> known[kMaxDevices];   // SMs per device, 0: not asked yet
     int sms = 0, dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) sms = known[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && sms == 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) {
         cudaGetLastError();
         if (need_device) return cuda_error(e, "attention: SM count");
@@ -36,10 +43,9 @@ int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan)
     }
     plan->grid = sms;
     const int hg = heads_per_team(pool->n_kv_heads);
-    const size_t warps = (size_t)sms * (rows::NW / hg) * hg;
-    plan->counter_bytes = (warps * sizeof(unsigned long long) + 255) / 256 * 256;
-    plan->bytes = kReserved + plan->counter_bytes +
-                  warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
+    const size_t warps = (size_t)plan->grid * (kernel_for(pool, n_rows, false).warps / hg) * hg;
+    plan->flag_bytes = (warps * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    plan->bytes = kReserved + plan->flag_bytes + warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
     return PF_OK;
 }
 
@@ -48,18 +54,28 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     int *status = device_status_ptr();
     if (!status) return PF_ERR_CUDA;
     const rows::Kernel k = kernel_for(pool, a.rows, a.out_dtype == PF_F32);
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k.fn),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-    if (e != cudaSuccess) return cuda_error(e, "attention: cudaFuncSetAttribute");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "attention: cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return set_error(PF_ERR_UNSUPPORTED, "device index out of range");
+    // once per device and kernel (setting it twice does no harm)
+    static std::atomic<bool> ready[kMaxDevices][32];
+    std::atomic<bool> &done = ready[dev][(pool->dtype == PF_E4M3) + 2 * (pool->head_dim == 64) + 4 * (a.rows <= 8) +
+                                         8 * (a.out_dtype == PF_F32) + 16 * (pool->block_size >= 16)];
+    if (!done.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 k.smem);
+        if (e != cudaSuccess) return cuda_error(e, "attention: cudaFuncSetAttribute");
+        done.store(true, std::memory_order_release);
+    }
     rows::Params p;
     p.k_pool = static_cast<const uint8_t *>(pool->k_base);
     p.v_pool = static_cast<const uint8_t *>(pool->v_base);
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
     p.status = status;
-    uint8_t *ws = static_cast<uint8_t *>(a.workspace) + kReserved;
-    p.counters = reinterpret_cast<unsigned long long *>(ws);
-    p.recs = reinterpret_cast<float *>(ws + a.plan.counter_bytes);
+    p.flags = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(a.workspace) + kReserved);
+    p.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kReserved + a.plan.flag_bytes);
     p.max_blocks = a.max_blocks;
     p.n_blocks = pool->n_blocks;
     p.block_size = pool->block_size;
@@ -78,18 +94,33 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     p.scale_log2 = a.scale * 1.4426950408889634f;
     const size_t row = (size_t)a.n_q_heads * pool->head_dim;
     const size_t out_elem = a.out_dtype == PF_F32 ? 4 : 2;
-    // Sequences are independent: larger batches are consecutive launches.
-    for (int s0 = 0; s0 < a.n_seqs; s0 += rows::kMaxSeqs) {
+    // Sequences are independent: larger batches are consecutive launches, of
+    // as many as keep the work units below 2^31 however long the contexts are.
+    const long long most = ((long long)a.max_blocks * pool->block_size / 16 + 1 + rows::kPairCost) * p.n_groups;
+    if (most > 0x7fffffffll) return set_error(PF_ERR_INVALID, "attention: max_blocks_per_seq is too large for the heads");
+    const int step = (int)(0x7fffffffll / most < rows::kMaxSeqs ? 0x7fffffffll / most : rows::kMaxSeqs);
+    for (int s0 = 0; s0 < a.n_seqs; s0 += step) {
         const size_t q0 = a.cu_q ? 0 : (size_t)s0 * row;   // cu_q holds absolute rows
         p.q = static_cast<const __half *>(a.q) + q0;
         p.out = static_cast<uint8_t *>(a.out) + q0 * out_elem;
         p.bt = a.block_tables + (size_t)s0 * a.max_blocks;
         p.lens = a.context_lens + s0;
         p.cu_q = a.cu_q ? a.cu_q + s0 : nullptr;
-        p.n_seqs = a.n_seqs - s0 < rows::kMaxSeqs ? a.n_seqs - s0 : rows::kMaxSeqs;
-        p.epoch = next_epoch();
-        k.fn<<<(unsigned)a.plan.grid, rows::NTHREADS, k.smem, stream>>>(p);
-        e = cudaGetLastError();
+        p.n_seqs = a.n_seqs - s0 < step ? a.n_seqs - s0 : step;
+        p.stamp = next_epoch() | 0x80000000u;
+        // a programmatic dependent of the kernel before it: its blocks take
+        // their SMs as that kernel's leave them, and then wait for its end
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)a.plan.grid);
+        cfg.blockDim = dim3((unsigned)k.warps * 32);
+        cfg.dynamicSmemBytes = (size_t)k.smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k.fn, p);
         if (e != cudaSuccess) return cuda_error(e, "attention: launch");
     }
     return PF_OK;
