@@ -53,23 +53,27 @@ struct AppendParams {
 template <int B, int D>
 struct AppendShape {
     static constexpr int CHUNKS = B * D / 8;                                     // 16-byte chunks of a page's head
-    static constexpr int GT = CHUNKS < 32 ? CHUNKS : (B == 16 ? 32 : (B == 64 ? 128 : 256));   // threads of a group
+    // threads of a group: 8 chunks each, at least a warp (below 32 chunks one each), at most the CTA
+    static constexpr int GT = CHUNKS < 32 ? CHUNKS : (CHUNKS / 8 < 32 ? 32 : (CHUNKS / 8 > kThreads ? kThreads : CHUNKS / 8));
     static constexpr int VPT = CHUNKS / GT;
     static constexpr int GROUPS = kThreads / GT;
 };
 
-// Largest magnitude of the finite halves of w, as fp16 bits.
-__device__ __forceinline__ uint32_t finite_max(uint32_t w, bool &bad) {
-    uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-    if (lo >= 0x7c00u) {
-        bad = true;
-        lo = 0;
-    }
-    if (hi >= 0x7c00u) {
-        bad = true;
-        hi = 0;
-    }
-    return max(lo, hi);
+// Magnitudes of w's two halves, as fp16 bits (which order as integers).
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7fff7fffu; }
+
+// The same with inf and NaN as 0.
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t w) {
+    const uint32_t m = magnitudes(w);
+    return ((m & 0xffffu) < 0x7c00u ? m & 0xffffu : 0u) | (m < 0x7c000000u ? m & 0xffff0000u : 0u);
+}
+
+// Two halves, times a power of two, to e4m3 codes.
+__device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t w, __half2 by) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&w), by);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    return r;
 }
 
 template <int B, int D>
@@ -115,8 +119,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     const float old = live && lo > 0 ? *scale_at : 0.0f;
 
     uint4 x[S::VPT];
-    uint32_t top = 0;
-    bool bad = false;
+    uint32_t top2 = 0;
     const __half *rows = (kv ? p.v_new : p.k_new) + ((ptrdiff_t)(q0 + page * B - start) * H + h) * D;   // the page's row 0, new or not
 #pragma unroll
     for (int i = 0; i < S::VPT; ++i) {
@@ -127,10 +130,20 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     }
 #pragma unroll
     for (int i = 0; i < S::VPT; ++i)
-        top = max(max(top, max(finite_max(x[i].x, bad), finite_max(x[i].y, bad))),
-                  max(finite_max(x[i].z, bad), finite_max(x[i].w, bad)));
-    if (bad) atomicOr(p.status, PF_DEV_NONFINITE);
-    // the group's maximum (fp16 bits of magnitudes order as integers)
+        top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(magnitudes(x[i].x), magnitudes(x[i].y))),
+                        __vmaxu2(magnitudes(x[i].z), magnitudes(x[i].w)));
+    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    const bool bad = top >= 0x7c00u;               // inf or NaN among this thread's values
+    if (bad) {
+        atomicOr(p.status, PF_DEV_NONFINITE);
+        top2 = 0;
+#pragma unroll
+        for (int i = 0; i < S::VPT; ++i)
+            top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(finite_magnitudes(x[i].x), finite_magnitudes(x[i].y))),
+                            __vmaxu2(finite_magnitudes(x[i].z), finite_magnitudes(x[i].w)));
+        top = max(top2 & 0xffffu, top2 >> 16);
+    }
+    // the group's maximum
 #pragma unroll
     for (int o = 1; o < (S::GT < 32 ? S::GT : 32); o <<= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
     if constexpr (S::GT > 32) {
@@ -146,20 +159,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     const float inv = 1.0f / scale;                // exact: powers of two
     const float lim = fminf(448.0f, 61440.0f * inv);
     uint8_t *page_at = (kv ? p.v_pool : p.k_pool) + ((size_t)(p.layer_page0 + blk) * B * H + h) * D;
+    // x / scale in fp16 when 1 / scale is one: exact but below 2^-14, far
+    // below half of e4m3's smallest, which is stored as 0 either way.
+    if (!bad && lim == 448.0f && inv <= 32768.0f) {
+        const __half2 by = __float2half2_rn(inv);
 #pragma unroll
-    for (int i = 0; i < S::VPT; ++i) {
-        const int e = i * S::GT + tg;
-        const int t = e / CPR, c = e % CPR;
-        if (t < lo || t >= hi) continue;
-        float f[8];
-        half8_to_float(x[i], f);
-        if (bad || lim < 448.0f) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = f[k] != f[k] ? 0.0f : fminf(fmaxf(f[k], -lim * scale), lim * scale);
+        for (int i = 0; i < S::VPT; ++i) {
+            const int e = i * S::GT + tg;
+            const int t = e / CPR, c = e % CPR;
+            if (t < lo || t >= hi) continue;
+            *reinterpret_cast<uint2 *>(page_at + (size_t)t * H * D + c * 8) =
+                make_uint2(scaled_e4m3x2(x[i].x, by) | (scaled_e4m3x2(x[i].y, by) << 16),
+                           scaled_e4m3x2(x[i].z, by) | (scaled_e4m3x2(x[i].w, by) << 16));
         }
-        const uint2 code = make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
-                                      e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
-        *reinterpret_cast<uint2 *>(page_at + (size_t)t * H * D + c * 8) = code;
+    } else {
+#pragma unroll
+        for (int i = 0; i < S::VPT; ++i) {
+            const int e = i * S::GT + tg;
+            const int t = e / CPR, c = e % CPR;
+            if (t < lo || t >= hi) continue;
+            float f[8];
+            half8_to_float(x[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = f[k] != f[k] ? 0.0f : fminf(fmaxf(f[k] * inv, -lim), lim);
+            *reinterpret_cast<uint2 *>(page_at + (size_t)t * H * D + c * 8) =
+                make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+        }
     }
     if (lo == 0 || scale > old) {
         if (tg == 0) *scale_at = scale;
