@@ -20,12 +20,14 @@
 //                      128-byte swizzle, by TMA boxes of up to a page (block
 //                      size 16 and up; each warp every other box) or 16-byte
 //                      cp.async per token (block size 1);
-//   warp 12            issues the scores S_g = Q_g K_j^T (A and B in shared
-//                      memory) and owns the tensor memory;
-//   warp 13            issues the products O_g += P_g V_j (P in tensor
-//                      memory, V in shared memory); warps 14-15 idle.
-// The softmax warpgroups run with 200 registers a thread, the others with
-// 56 (setmaxnreg after the setup barrier).
+//   warp 12            one elected thread issues the scores S_g = Q_g K_j^T (A
+//                      and B in shared memory); owns the tensor memory;
+//   warp 13            one elected thread issues the products O_g += P_g V_j
+//                      (P in tensor memory, V in shared memory);
+//   warp 14            zeroes the V rows past the last position (fp16 pools);
+//                      warp 15 idles.
+// The softmax warpgroups run with more registers a thread than the others
+// (setmaxnreg after the setup barrier).
 // The softmax threads read their row of S, apply the causal limit, keep a
 // running maximum per row (raised only past 2^8, log2 domain, so O is
 // rescaled rarely), add their weights to the row sum in fp32 and write them,
@@ -69,16 +71,22 @@ constexpr int QT = 128;          // rows per query tile (the MMA's M)
 constexpr int SOFTMAX_WARPS = 8;  // warpgroups 0 and 1
 constexpr int LOAD_WARP0 = 8;     // warpgroup 2: K loaders (warps 8, 9), V loaders (10, 11)
 constexpr int MMA_S_WARP = 12;    // warpgroup 3: issues the scores; owns the tensor memory
-constexpr int MMA_PV_WARP = 13;   // issues the products (warps 14 and 15 idle)
+constexpr int MMA_PV_WARP = 13;   // issues the products
+constexpr int CLEAN_WARP = 14;    // zeroes V rows past the end (warp 15 idles)
 constexpr int NTHREADS = 512;
 // Registers: launched at 128 a thread (512 threads, one CTA per SM); the
-// loader and MMA warpgroups then give theirs down to REG_OTHER and the
-// softmax warpgroups take REG_SOFTMAX.  Each SM sub-partition holds one warp
-// of every warpgroup, so the split must also fit its 16K registers.
-constexpr int REG_SOFTMAX = 200;
-constexpr int REG_OTHER = 56;
-static_assert(2 * 128 * REG_SOFTMAX + 2 * 128 * REG_OTHER == NTHREADS * 128, "the split is the launch's registers");
-static_assert(32 * (2 * REG_SOFTMAX + 2 * REG_OTHER) <= 16384, "a sub-partition's registers");
+// loader and MMA warpgroups then give some of theirs to the softmax
+// warpgroups, which at head_dim 64 hold 128 scores and their weights a row (64
+// at 128: the loaders of e4m3 tiles keep more).  Each SM sub-partition holds
+// one warp of every warpgroup, so the split must also fit its 16K registers.
+template <int D>
+struct Regs {
+    static constexpr int SOFTMAX = D == 64 ? 200 : 152;
+    static constexpr int OTHER = 256 - SOFTMAX;
+    static_assert(SOFTMAX % 8 == 0 && 2 * 128 * (SOFTMAX + OTHER) == NTHREADS * 128, "the split is the launch's registers");
+    static_assert(32 * (2 * SOFTMAX + 2 * OTHER) <= 16384, "a sub-partition's registers");
+};
+constexpr int kOrderSeqs = NTHREADS;   // a thread per sequence
 constexpr int kRawStages = 3;    // e4m3: raw K/V stages
 constexpr int TMEM_COLS = 512;
 constexpr float kRescaleLog2 = 8.0f;
@@ -125,7 +133,9 @@ struct Params {
     int max_new;
     int n_blocks;
     int block_size;
+    int block_shift;  // log2 of block_size
     int box_rows;     // rows of one TMA box (block size 16 and up)
+    int n_seqs;
     int n_items;      // sequences x kv-heads
     int n_qp;         // 256-row tiles of the longest (sequence, kv-head)
     long long layer_row0;
@@ -144,6 +154,8 @@ struct Bars {
     unsigned long long p_full[2];
     unsigned long long o_done[2];
     unsigned long long mma_done[2];
+    unsigned long long v_last;       // the last V tile has landed
+    unsigned long long v_clean;      // its rows past the end are zeros
     uint32_t tmem_base;
 };
 
@@ -153,10 +165,22 @@ struct Bars {
 // 128 bytes, 8-row groups 1024 bytes apart (the stride field), 16-byte chunk
 // c of row t stored at chunk c ^ (t mod 8).  The start address advances by
 // 32 bytes per 16-element K step inside a 64-element half; every block
-// starts on a 1024-byte boundary, so the base-offset field stays 0.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// starts on a 1024-byte boundary, so the base-offset field stays 0.  `lead`
+// (the leading field) is the distance of neighbouring 64-element halves of an
+// MN-major operand wider than 64.  Addresses are below 2^18, so a descriptor
+// of the same layout `bytes` further is the sum with bytes / 16.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lead = 16) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// True on one lane of the (converged) warp.  What that thread does alone,
+// descriptors included, then runs on the warp's uniform registers: with
+// `lane == 0` instead, an MMA took 80 to 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, fp16 A and B, A
@@ -308,10 +332,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __shared__ Bars bars;
     uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
-    // work item: the longest query tiles first
+    // Work item, the longest first.  Causal: the last query tiles.  Cross: the
+    // longest contexts -- with blocks taken in the order of the sequences, four
+    // prompts' 384 blocks on 152 SMs left 40 % of the time idle behind the long
+    // ones (batches of up to kOrderSeqs: each block ranks the lengths itself).
     const int b = (int)blockIdx.x;
-    const int qp = p.n_qp - 1 - b / p.n_items;
-    const int item = b - (b / p.n_items) * p.n_items;
+    int qp = p.n_qp - 1 - b / p.n_items;
+    int item = b - (b / p.n_items) * p.n_items;
+    if constexpr (!CAUSAL) {
+        const int per = p.n_kv_heads * p.n_qp;
+        int seq = b / per;
+        if (p.n_seqs > 1 && p.n_seqs <= kOrderSeqs) {
+            __shared__ int len_of[kOrderSeqs];
+            __shared__ int picked;
+            const int u = (int)threadIdx.x;
+            const int mine = u < p.n_seqs ? p.lens[u] : 0;
+            if (u < p.n_seqs) len_of[u] = mine;
+            __syncthreads();
+            if (u < p.n_seqs) {
+                int rank = 0;
+                for (int v = 0; v < p.n_seqs; ++v) rank += len_of[v] > mine || (len_of[v] == mine && v < u);
+                if (rank == seq) picked = u;
+            }
+            __syncthreads();
+            seq = picked;
+        }
+        qp = b % per / p.n_kv_heads;
+        item = seq * p.n_kv_heads + b % p.n_kv_heads;
+    }
     const int s = item / p.n_kv_heads;
     const int h = item - s * p.n_kv_heads;
     const int warp = (int)threadIdx.x / 32;
@@ -472,34 +520,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int k = 0; k < IDS; ++k) {
             const int tok = j * BN + tile_token(lane + 32 * k);
-            q_id[k] = tok <= p_max ? bt_row[tok / B] : -2;
+            q_id[k] = tok <= p_max ? bt_row[tok >> p.block_shift] : -2;
         }
     };
+    // this lane's chunk 0 in a raw stage, in the pool and in a swizzled stage;
+    // chunk i is 2 TPI tokens further (t mod 8, the swizzle, stays)
+    const int x0 = li * TPI + lane / CPR, c0 = lane % CPR;
+    const uint32_t raw_at = (uint32_t)(x0 * CPR + c0) * 16;
+    const uint32_t row_bytes = (uint32_t)p.n_kv_heads * D;
+    const uint8_t *codes = reinterpret_cast<const uint8_t *>(pool_base) + h * D + c0 * 16;
+    const uint32_t wide_at[2] = {swz(x0, 2 * c0, BN), swz(x0, 2 * c0 + 1, BN)};
     auto q8_copy = [&](int j) {                              // tile j into raw stage j mod kRawStages
         const uint32_t dst = raw + (uint32_t)(j % kRawStages) * C::RAW_BYTES;
         if (j < ntt) {
             int row[IDS];
+            bool whole = true;
 #pragma unroll
             for (int k = 0; k < IDS; ++k) {
-                int id = q_id[k];
-                const int lt = lane + 32 * k;
-                if (id != -2 && (id < 0 || id >= p.n_blocks)) {
-                    atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
-                    id = -2;
-                }
-                row[k] = id < 0 ? -1 : (int)(p.layer_row0 + (long long)id * B + (j * BN + tile_token(lt)) % B);
+                const int id = q_id[k], lt = lane + 32 * k;
+                const bool ok = (unsigned)id < (unsigned)p.n_blocks;
+                if (!ok && id != -2) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                row[k] = ok ? (int)p.layer_row0 + (id << p.block_shift) + ((j * BN + tile_token(lt)) & (B - 1)) : -1;
+                whole = whole && ok;
                 cp_async4_zfill(dst + BN * D + (li * TW + lt) * 4,
-                                scale_base + (id < 0 ? 0 : (size_t)(p.layer_page0 + id) * p.n_kv_heads + h),
-                                id < 0 ? 0u : 4u);
+                                scale_base + (ok ? (size_t)(unsigned)((int)p.layer_page0 + id) * p.n_kv_heads + h : 0),
+                                ok ? 4u : 0u);
             }
-            const uint8_t *codes = reinterpret_cast<const uint8_t *>(pool_base);
+            if (__all_sync(FULL, whole)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int lt = i * TPI + lane / CPR;
-                const int r8 = __shfl_sync(FULL, row[i * TPI / 32], lt % 32);
-                cp_async16_zfill(dst + (tile_token(lt) * CPR + lane % CPR) * 16,
-                                 codes + (r8 < 0 ? 0 : ((size_t)r8 * p.n_kv_heads + h) * D + lane % CPR * 16),
-                                 r8 < 0 ? 0u : 16u);
+                for (int i = 0; i < 8; ++i) {
+                    const int r8 = __shfl_sync(FULL, row[i * TPI / 32], i * TPI % 32 + lane / CPR);
+                    cp_async16_cg(dst + raw_at + i * 2 * TPI * CPR * 16, codes + (size_t)(unsigned)r8 * row_bytes);
+                }
+            } else {                                          // the end, or bad ids: zeros
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r8 = __shfl_sync(FULL, row[i * TPI / 32], i * TPI % 32 + lane / CPR);
+                    cp_async16_zfill(dst + raw_at + i * 2 * TPI * CPR * 16,
+                                     codes + (r8 < 0 ? 0 : (size_t)(unsigned)r8 * row_bytes), r8 < 0 ? 0u : 16u);
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -511,28 +570,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int st = j % NS;
         const uint32_t dst = s_base + st * C::KV_BYTES;
         if (j >= NS && !wait_lanes(bar(empty[st]), ((j / NS) - 1) & 1, p.status)) return false;
+        constexpr int AT_ONCE = D == 64 ? 2 : 4;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int lt = i * TPI + lane / CPR;
-            const int tk = tile_token(lt), c = lane % CPR;
-            uint32_t w[4];
-            float f;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(src + (tk * CPR + c) * 16));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(src + BN * D + (li * TW + lt) * 4));
-            const __half2 f2 = __float2half2_rn(f);
+        for (int i0 = 0; i0 < 8; i0 += AT_ONCE) {
+            uint4 w[AT_ONCE];
+            float f[AT_ONCE];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t x[4];
+            for (int i = 0; i < AT_ONCE; ++i) {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                             : "r"(src + raw_at + (i0 + i) * 2 * TPI * CPR * 16));
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(f[i])
+                             : "r"(src + BN * D + (li * TW + (i0 + i) * TPI + lane / CPR) * 4));
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 v = __hmul2(widen_e4m3(w[2 * k + e / 2] >> (16 * (e & 1))), f2);
-                    x[e] = *reinterpret_cast<const uint32_t *>(&v);
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const __half2 f2 = __float2half2_rn(f[i]);
+                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 v = __hmul2(widen_e4m3(in[2 * k + e / 2] >> (16 * (e & 1))), f2);
+                        x[e] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + wide_at[k] + (i0 + i) * 2 * TPI * 128),
+                                 "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                                 : "memory");
                 }
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + swz(tk, 2 * c + k, BN)), "r"(x[0]),
-                             "r"(x[1]), "r"(x[2]), "r"(x[3])
-                             : "memory");
             }
         }
         fence_proxy_async_shared();
@@ -579,6 +646,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             mbar_init(bar(bars.mma_done[0]), 1);
             mbar_init(bar(bars.mma_done[1]), 1);
+            mbar_init(bar(bars.v_last), 1);
+            mbar_init(bar(bars.v_clean), 1);
             mbar_init_fence();
         }
         __syncwarp();
@@ -592,8 +661,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = bars.tmem_base;
-    if (warp >= SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
+    if (warp >= SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::OTHER));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D>::SOFTMAX));
 
     if (warp < SOFTMAX_WARPS) {
         // ---------------------------------------------------------- softmax
@@ -741,80 +810,91 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else if (warp == MMA_S_WARP) {
         // ------------------------------------------------- MMA: S = Q K^T
         constexpr uint32_t ID_S = idesc_f16(QT, BN, false);
-        const uint32_t s_q = smem_addr(sm);
-        bool ok = true;
-        for (int j = 0; ok && j < ntt; ++j) {
-            const int st = j % NS;
-            if (!wait_lanes(bar(bars.k_full[st]), (j / NS) & 1, p.status)) break;
-            for (int g = 0; g < 2; ++g) {
-                if (j >= nt[g]) continue;
-                // S of this query tile has been read (its previous tile)
-                if (j > 0 && !wait_lanes(bar(bars.s_free[g]), (j - 1) & 1, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_after_sync();
-                if (lane == 0) {
-                    const uint32_t a0 = s_q + g * C::Q_BYTES;
-                    const uint32_t b0 = s_k + st * C::KV_BYTES;
+        if (elect_one()) {
+            const uint64_t dq = sdesc(smem_addr(sm)), dk = sdesc(s_k);
+            bool ok = true;
+            int st = 0, phase = 0;
+            for (int j = 0; ok && j < ntt; ++j) {
+                if (!mbar_wait(bar(bars.k_full[st]), phase, p.status)) break;
+                for (int g = 0; g < 2; ++g) {
+                    if (j >= nt[g]) continue;
+                    // S of this query tile has been read (its previous tile)
+                    if (j > 0 && !mbar_wait(bar(bars.s_free[g]), (j - 1) & 1, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_after_sync();
+                    const uint64_t a = dq + g * (C::Q_BYTES / 16), b = dk + st * (C::KV_BYTES / 16);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        umma(tmem + g * BN, sdesc(a0 + (kk / 4) * QT * 128 + (kk % 4) * 32),
-                             sdesc(b0 + (kk / 4) * BN * 128 + (kk % 4) * 32), ID_S, kk > 0);
+                        umma(tmem + g * BN, a + (kk / 4) * (QT * 128 / 16) + (kk % 4) * 2,
+                             b + (kk / 4) * (BN * 128 / 16) + (kk % 4) * 2, ID_S, kk > 0);
                     umma_commit(bar(bars.s_full[g]));
                 }
+                if (ok) umma_commit(bar(bars.k_empty[st]));
+                if (++st == NS) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
-            if (ok && lane == 0) umma_commit(bar(bars.k_empty[st]));
+            // every MMA issued has completed before tensor memory is released
+            umma_commit(bar(bars.mma_done[0]));
         }
-        // every MMA issued has completed before tensor memory is released
-        if (lane == 0) umma_commit(bar(bars.mma_done[0]));
+        __syncwarp();
         wait_lanes(bar(bars.mma_done[0]), 0, p.status);
     } else if (warp == MMA_PV_WARP) {
         // ------------------------------------------------ MMA: O += P V
-        constexpr uint32_t ID_PV = idesc_f16(QT, 64, true);
-        bool ok = true;
-        for (int j = 0; ok && j < ntt; ++j) {
-            const int st = j % NS;
-            if (!wait_lanes(bar(bars.v_full[st]), (j / NS) & 1, p.status)) break;
-            if (!Q8 && j == ntt - 1 && p_max - j * BN < BN - 1) {
-                // V rows past the CTA's last position: zeros (a zero weight
-                // times a non-finite value would not vanish)
-                uint8_t *vt = sm + C::OFF_V + st * C::KV_BYTES;
-                const int first = p_max - j * BN + 1;
-                for (int e = lane; e < (BN - first) * 8 * C::HALVES; e += 32) {
-                    const int row = first + e / (8 * C::HALVES);
-                    const int rest = e % (8 * C::HALVES);
-                    *reinterpret_cast<uint4 *>(vt + ((rest / 8) * BN + row) * 128 + (rest % 8) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+        constexpr uint32_t ID_PV = idesc_f16(QT, D, true);
+        if (elect_one()) {
+            const uint64_t dv = sdesc(s_v, BN * 128);
+            bool ok = true;
+            int st = 0, phase = 0;
+            for (int j = 0; ok && j < ntt; ++j) {
+                if (!mbar_wait(bar(bars.v_full[st]), phase, p.status)) break;
+                if (!Q8 && j == ntt - 1) {
+                    mbar_arrive(bar(bars.v_last));
+                    if (!mbar_wait(bar(bars.v_clean), 0, p.status)) break;
                 }
-                fence_proxy_async_shared();
-                __syncwarp();
-            }
-            for (int g = 0; g < 2; ++g) {
-                if (j >= nt[g]) continue;
-                if (!wait_lanes(bar(bars.p_full[g]), j & 1, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_after_sync();
-                if (lane == 0) {
-                    const uint32_t a0 = tmem + C::COL_P + g * (BN / 2);
-                    const uint32_t v0 = s_v + st * C::KV_BYTES;
-                    const uint32_t to = tmem + C::COL_O + g * D;
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk) {
-#pragma unroll
-                        for (int hf = 0; hf < C::HALVES; ++hf)
-                            umma_ts(to + hf * 64, a0 + kk * 8, sdesc(v0 + hf * BN * 128 + kk * 2048), ID_PV,
-                                    j > 0 || kk > 0);
+                for (int g = 0; g < 2; ++g) {
+                    if (j >= nt[g]) continue;
+                    if (!mbar_wait(bar(bars.p_full[g]), j & 1, p.status)) {
+                        ok = false;
+                        break;
                     }
+                    tc_after_sync();
+                    const uint64_t b = dv + st * (C::KV_BYTES / 16);
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        umma_ts(tmem + C::COL_O + g * D, tmem + C::COL_P + g * (BN / 2) + kk * 8, b + kk * (2048 / 16),
+                                ID_PV, j > 0 || kk > 0);
                     umma_commit(bar(bars.o_done[g]));
                 }
+                if (ok) umma_commit(bar(bars.v_empty[st]));
+                if (++st == NS) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
-            if (ok && lane == 0) umma_commit(bar(bars.v_empty[st]));
+            umma_commit(bar(bars.mma_done[1]));
         }
-        if (lane == 0) umma_commit(bar(bars.mma_done[1]));
+        __syncwarp();
         wait_lanes(bar(bars.mma_done[1]), 0, p.status);
+    } else if (!Q8 && warp == CLEAN_WARP) {
+        // V rows past the CTA's last position: zeros (a zero weight times a
+        // non-finite value would not vanish)
+        if (wait_lanes(bar(bars.v_last), 0, p.status)) {
+            uint8_t *vt = sm + C::OFF_V + (ntt - 1) % NS * C::KV_BYTES;
+            const int first = p_max - (ntt - 1) * BN + 1;
+            for (int e = lane; e < (BN - first) * 8 * C::HALVES; e += 32) {
+                const int row = first + e / (8 * C::HALVES);
+                const int rest = e % (8 * C::HALVES);
+                *reinterpret_cast<uint4 *>(vt + ((rest / 8) * BN + row) * 128 + (rest % 8) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bars.v_clean));
+        }
     }
 
     tc_before_sync();
@@ -924,7 +1004,10 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     p.max_new = a.max_new;
     p.n_blocks = pool->n_blocks;
     p.block_size = pool->block_size;
+    p.block_shift = 0;
+    while ((1 << p.block_shift) < pool->block_size) ++p.block_shift;
     p.box_rows = box_rows;
+    p.n_seqs = a.n_seqs;
     p.n_items = (int)n_items;
     p.n_qp = (int)n_qp;
     p.layer_page0 = (long long)a.layer * pool->n_blocks;
