@@ -59,6 +59,7 @@
 
 #include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "internal.h"
@@ -129,6 +130,7 @@ struct Params {
     int n_q_heads;
     int n_kv_heads;
     int gh;
+    int gh_magic;     // 65536 / gh, rounded up
     int max_blocks;
     int max_new;
     int n_blocks;
@@ -419,23 +421,32 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t s_v = smem_addr(sm + C::OFF_V);
     auto bar = [](unsigned long long &x) { return smem_addr(&x); };
 
-    // Softmax threads: their row, and the query row into shared memory
-    // (zeros past the last row) before the setup barrier, which then orders
-    // it before the first MMA.
+    // Row r0 + d of the CTA: its new token, and where it lies in q and out.
+    // d + r0 mod gh is below 272, where the product with 65536 / gh (rounded
+    // up) gives the quotient.
+    const int i0 = r0 / p.gh, rem0 = r0 - i0 * p.gh;
+    auto token_of = [&](int d) { return i0 + (((rem0 + d) * p.gh_magic) >> 16); };
+    auto row_at = [&](int d) {
+        const int i = token_of(d);
+        return ((size_t)(q0 + i) * p.n_q_heads + (size_t)h * p.gh + (rem0 + d - (i - i0) * p.gh)) * D;
+    };
+    // Softmax threads: the query rows into shared memory (zeros past the last
+    // row), 16 bytes each and neighbouring lanes neighbouring chunks, before
+    // the setup barrier, which then orders them before the first MMA.
     const int g = (warp / 4) & 1;
     const int t = (int)threadIdx.x % 128;                    // row of the tile = tensor-memory lane
-    const int r = r0 + g * QT + t;
-    const bool valid = warp < SOFTMAX_WARPS && r < r_end;
-    const int i = valid ? r / p.gh : 0;
-    const int lim = CAUSAL && valid ? base + i : pmax[g];      // last position this row sees
-    const size_t ob = valid ? ((size_t)(q0 + i) * p.n_q_heads + (size_t)h * p.gh + (r - i * p.gh)) * D : 0;
+    const bool valid = warp < SOFTMAX_WARPS && r0 + g * QT + t < r_end;
+    const int lim = CAUSAL && valid ? base + token_of(g * QT + t) : pmax[g];   // last position this row sees
     if (warp < SOFTMAX_WARPS) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ob);
+        constexpr int CH = D / 8;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(sm + g * C::Q_BYTES + swz(t, c, QT)) = x;
+        for (int it = 0; it < CH; ++it) {
+            const int d = it * (256 / CH) + (int)threadIdx.x / CH, c = (int)threadIdx.x % CH;
+            const bool ok = r0 + d < r_end;
+            cp_async16_zfill(smem_addr(sm) + (d / QT) * C::Q_BYTES + swz(d % QT, c, QT),
+                             p.q + (ok ? row_at(d) + c * 8 : 0), ok ? 16u : 0u);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_shared();
     }
     // Loaders: block id of box `lane` of tile j (pages of 16 tokens and
@@ -621,8 +632,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");   // the loader warps: barriers initialised
         if constexpr (Q8) {
             q8_look_up(0);
-#pragma unroll
-            for (int j = 0; j < kRawStages - 1; ++j) q8_copy(j);
         } else {
             prefetch_tensormap(map);
             id0 = raw_id(0);
@@ -658,9 +667,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_before_sync();
-    __syncthreads();
+    // The loaders need nothing that the others set up: they only arrive.
+    __syncwarp();
+    if (loader) asm volatile("bar.arrive 2, %0;" ::"n"(NTHREADS) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(NTHREADS) : "memory");
     tc_after_sync();
-    const uint32_t tmem = bars.tmem_base;
+    const uint32_t tmem = loader ? 0u : bars.tmem_base;
     if (warp >= SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::OTHER));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D>::SOFTMAX));
 
@@ -758,36 +770,62 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (ok && nt[g] > 0 && wait_lanes(bar(bars.o_done[g]), (nt[g] - 1) & 1, p.status)) {
             tc_after_sync();
             const float inv = 1.0f / l;
+            // The warp's 32 rows, 128 bytes of each at a time, through its own
+            // rows of the query tile (whose MMAs are done): stored by rows
+            // straight from tensor memory, 16 bytes per lane and row, the
+            // output took 5,000 cycles.
+            const uint32_t stage = smem_addr(sm) + g * C::Q_BYTES;
+            const int t0 = (warp % 4) * 32;
+            auto store = [&](auto f32_c) {
+                constexpr bool F32 = decltype(f32_c)::value;
+                constexpr int DP = F32 ? 32 : 64;            // dims of 128 bytes
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += DP) {
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16(t_o + c0, o);
-                tmem_ld_wait();
-                if (valid) {
-                    if (p.out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + ob + c0);
+                    for (int part = 0; part < DP / 32; ++part) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + c0 + part * 32, o);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                                 __uint_as_float(o[4 * e + 2]) * inv,
-                                                 __uint_as_float(o[4 * e + 3]) * inv);
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + ob + c0);
+                        for (int e = 0; e < (F32 ? 8 : 4); ++e) {
+                            uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            dst[e] = make_uint4(
-                                pack_half2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
-                                pack_half2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
-                                pack_half2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
-                                pack_half2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
+                            for (int k = 0; k < 4; ++k) {
+                                if constexpr (F32) w[k] = __float_as_uint(__uint_as_float(o[4 * e + k]) * inv);
+                                else w[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                       __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                            }
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             stage + swz(t0 + lane, part * 4 + e, QT)),
+                                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                         : "memory");
                         }
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int it = 0; it < 8; ++it) {
+                        const int row = t0 + it * 4 + lane / 8, c = lane % 8, d = g * QT + row;
+                        uint4 w;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(stage + swz(row, c, QT)));
+                        if (r0 + d < r_end) {
+                            const size_t at = row_at(d) + c0;
+                            if constexpr (F32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at + c * 4) = w;
+                            else *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + at + c * 8) = w;
+                        }
+                    }
+                    __syncwarp();
                 }
-            }
+            };
+            if (p.out_f32) store(std::true_type());
+            else store(std::false_type());
         }
     } else if (loader) {
         // ---------------------------------------------------------- loaders
         if constexpr (Q8) {
+#pragma unroll 1
+            for (int j = 0; j < kRawStages - 1; ++j) q8_copy(j);
             for (int j = 0; j < ntt; ++j) {
                 __syncwarp();                                  // the raw stage of tile j - 1 has been read
                 q8_copy(j + kRawStages - 1);
@@ -1000,6 +1038,7 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     p.n_q_heads = a.n_q_heads;
     p.n_kv_heads = pool->n_kv_heads;
     p.gh = gh;
+    p.gh_magic = (65536 + gh - 1) / gh;
     p.max_blocks = a.max_blocks;
     p.max_new = a.max_new;
     p.n_blocks = pool->n_blocks;
