@@ -88,6 +88,7 @@ struct Regs {
     static_assert(32 * (2 * SOFTMAX + 2 * OTHER) <= 16384, "a sub-partition's registers");
 };
 constexpr int kOrderSeqs = NTHREADS;   // a thread per sequence
+constexpr int kOrderContext = 1024;
 constexpr int kRawStages = 3;    // e4m3: raw K/V stages
 constexpr int TMEM_COLS = 512;
 constexpr float kRescaleLog2 = 8.0f;
@@ -337,14 +338,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // Work item, the longest first.  Causal: the last query tiles.  Cross: the
     // longest contexts -- with blocks taken in the order of the sequences, four
     // prompts' 384 blocks on 152 SMs left 40 % of the time idle behind the long
-    // ones (batches of up to kOrderSeqs: each block ranks the lengths itself).
+    // ones (batches of up to kOrderSeqs with room for long contexts: each block
+    // ranks the lengths itself, which takes it about a microsecond).
     const int b = (int)blockIdx.x;
     int qp = p.n_qp - 1 - b / p.n_items;
     int item = b - (b / p.n_items) * p.n_items;
     if constexpr (!CAUSAL) {
         const int per = p.n_kv_heads * p.n_qp;
         int seq = b / per;
-        if (p.n_seqs > 1 && p.n_seqs <= kOrderSeqs) {
+        if (p.n_seqs > 1 && p.n_seqs <= kOrderSeqs && p.max_blocks * p.block_size >= kOrderContext) {
             __shared__ int len_of[kOrderSeqs];
             __shared__ int picked;
             const int u = (int)threadIdx.x;
@@ -367,6 +369,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int warp = (int)threadIdx.x / 32;
     const int lane = (int)threadIdx.x % 32;
     const int maxctx = p.max_blocks * p.block_size;
+
+    // Loaders: the block ids of their first tiles (what of the table row that
+    // needs, whatever it holds), on the way together with the lengths.
+    const bool loader = warp >= LOAD_WARP0 && warp < LOAD_WARP0 + 4;
+    const bool is_v = warp >= LOAD_WARP0 + 2;
+    const int li = (warp - LOAD_WARP0) & 1;                  // this warp's boxes: lane % 2 == li
+    const int32_t *bt_row = p.bt + (size_t)s * p.max_blocks;
+    constexpr int CPR = D / 16;                              // e4m3: chunks of a row of codes
+    constexpr int TPI = 32 / CPR;                            // tokens of a warp per chunk index
+    constexpr int TW = BN / 2;                               // tokens of a warp
+    constexpr int IDS = TW / 32;
+    auto tile_token = [&](int lt) { return lt / TPI * (2 * TPI) + li * TPI + lt % TPI; };
+    int first_id[2] = {0, 0};
+    if (loader) {
+        const int page = p.block_size >= 16 ? p.block_shift : 0;
+#pragma unroll
+        for (int k = 0; k < (Q8 ? IDS : 2); ++k) {
+            const int tok = Q8 ? tile_token(lane + 32 * k) : k * BN + lane * p.box_rows;
+            first_id[k] = bt_row[min(tok >> page, p.max_blocks - 1)];
+        }
+    }
 
     // lengths and new-token counts, clamped (and flagged) to what the table
     // and the call allow
@@ -452,7 +475,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // Loaders: block id of box `lane` of tile j (pages of 16 tokens and
     // more; boxes past the CTA's last position are not loaded), read two
     // tiles ahead of its use and range-checked only when used.
-    const int32_t *bt_row = p.bt + (size_t)s * p.max_blocks;
     const int box = p.box_rows;
     auto n_boxes = [&](int j) { return min(BN / box, (p_max - j * BN) / box + 1); };
     auto raw_id = [&](int j) {
@@ -463,9 +485,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // it -- the scores for K, the products for V -- are done).  They set up
     // their barriers and stage tile 0 before the setup barrier, so the first
     // tiles arrive while the query rows load.
-    const bool loader = warp >= LOAD_WARP0 && warp < LOAD_WARP0 + 4;
-    const bool is_v = warp >= LOAD_WARP0 + 2;
-    const int li = (warp - LOAD_WARP0) & 1;                  // this warp's boxes: lane % 2 == li
     const CUtensorMap *map = is_v ? &tmv : &tmk;
     unsigned long long *full = is_v ? bars.v_full : bars.k_full;
     unsigned long long *empty = is_v ? bars.v_empty : bars.k_empty;
@@ -519,14 +538,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // tensor's two warps; chunk i of a lane is of token 2 TPI i + TPI li +
     // lane / CPR.  Lane l looks up the block ids (one tile ahead of their
     // copy) and copies the scales of the warp's tokens l, l + 32 (in order).
-    constexpr int CPR = D / 16;                              // chunks of a row of codes
-    constexpr int TPI = 32 / CPR;                            // tokens of a warp per chunk index
-    constexpr int TW = BN / 2;                               // tokens of a warp
-    constexpr int IDS = TW / 32;
     const uint32_t raw = smem_addr(sm + C::OFF_RAW) + (is_v ? kRawStages * C::RAW_BYTES : 0);
     const float *scale_base = is_v ? p.v_scale : p.k_scale;
     int q_id[IDS];                                           // raw ids of the next tile to copy (-2: no token)
-    auto tile_token = [&](int lt) { return lt / TPI * (2 * TPI) + li * TPI + lt % TPI; };
     auto q8_look_up = [&](int j) {
 #pragma unroll
         for (int k = 0; k < IDS; ++k) {
@@ -630,18 +644,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init_fence();
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");   // the loader warps: barriers initialised
+        // They need nothing that the other warps set up, which wait for these
+        // barriers: they pass the setup barrier without waiting.
+        __syncwarp();
+        asm volatile("bar.arrive 2, %0;" ::"n"(NTHREADS) : "memory");
         if constexpr (Q8) {
-            q8_look_up(0);
+#pragma unroll
+            for (int k = 0; k < IDS; ++k) q_id[k] = tile_token(lane + 32 * k) <= p_max ? first_id[k] : -2;
         } else {
             prefetch_tensormap(map);
-            id0 = raw_id(0);
-            id1 = raw_id(1);
-        }
-        if (!Q8 && B >= 16) {
-            const int id = id0;
-            id0 = id1;
-            id1 = raw_id(2);
-            load_tile(0, id);
+            id0 = first_id[0];
+            id1 = first_id[1];
+            if (B >= 16) {
+                const int id = id0;
+                id0 = id1;
+                id1 = raw_id(2);
+                load_tile(0, id);
+            }
         }
     }
 
@@ -667,10 +686,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_before_sync();
-    // The loaders need nothing that the others set up: they only arrive.
-    __syncwarp();
-    if (loader) asm volatile("bar.arrive 2, %0;" ::"n"(NTHREADS) : "memory");
-    else asm volatile("bar.sync 2, %0;" ::"n"(NTHREADS) : "memory");
+    if (!loader) asm volatile("bar.sync 2, %0;" ::"n"(NTHREADS) : "memory");
     tc_after_sync();
     const uint32_t tmem = loader ? 0u : bars.tmem_base;
     if (warp >= SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::OTHER));
