@@ -46,7 +46,9 @@
 //   the others' flags, merges the parts with the log-sum-exp rule and clears
 //   the flags (a captured launch has the same stamp every time it is
 //   replayed).  The parts waited for belong to earlier spans, whose warps wait
-//   for nothing but still earlier ones, and the wait is bounded (1 s).
+//   for nothing but still earlier ones, and the wait is bounded (1 s).  Where
+//   pairs are cut into many parts (few long contexts), the teams of a CTA merge
+//   theirs first, behind a CTA barrier, and the CTAs' records are the parts.
 #pragma once
 
 #include <type_traits>
@@ -68,6 +70,15 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kPairCost = 2;
 // Least units per span: shorter ones cost more in merges than they bring.
 constexpr int kMinSpan = 4;
+// A pair of n stages in spans of x takes x stages, then the merge of n / x
+// parts, each kPartCost stages per 128 values of its rows: least at x =
+// sqrt(kPartCost * values / 128 * n).
+// (Measured with 0, 1/8, 1/4, 1/2: 6 sequences of 2,700 tokens, 4 rows, 128
+// dims 28.6, 26.6, 29.8, 34.6 us; 14 of 1,600, 16 rows, 64 dims 24.6, 23.9,
+// 25.5, 29.8.)
+constexpr float kPartCost = 0.125f;
+// More parts than this per longest pair: merged in two levels.
+constexpr float kMaxParts = 12.0f;
 // A cut inside a pair of at most this many stages moves to the pair's nearer
 // edge: such pairs stay whole and need no merge.
 constexpr int kWhole = 4;
@@ -127,6 +138,7 @@ struct Shape {
 // W is below 2^31: the host bounds it by the tables.
 struct Spans {
     unsigned n, q, r;
+    unsigned T;   // teams that merge their parts of a pair before the others see them (1 or a CTA's)
     __device__ __forceinline__ unsigned start(unsigned j) const { return j * q + min(j, r); }
     // the span that holds unit x
     __device__ __forceinline__ unsigned owner(unsigned x) const {
@@ -262,6 +274,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     __shared__ unsigned pre[kMaxSeqs + 1];   // units before sequence s
     __shared__ int len_sh[kMaxSeqs];
     __shared__ unsigned warp_sum[32];
+    __shared__ int warp_max[32];
     __shared__ Spans span_sh;
 
     const int warp = (int)threadIdx.x / 32;
@@ -286,9 +299,11 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         const int s0 = min((int)threadIdx.x * per, p.n_seqs);
         const int s1 = min(s0 + per, p.n_seqs);
         unsigned mine = 0;
+        int longest = 0;
         for (int s = s0; s < s1; ++s) {
             const int L = context_length(p, s, blockIdx.x == 0);
             len_sh[s] = L;
+            longest = max(longest, L);
             if (L > 0) mine += ((unsigned)(L + ST - 1) / ST + kPairCost) * p.n_groups;
         }
         unsigned incl = mine;
@@ -297,7 +312,11 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
             const unsigned x = __shfl_up_sync(FULL, incl, o);
             if (lane >= o) incl += x;
         }
-        if (lane == 31) warp_sum[warp] = incl;
+        longest = __reduce_max_sync(FULL, longest);
+        if (lane == 31) {
+            warp_sum[warp] = incl;
+            warp_max[warp] = longest;
+        }
         __syncthreads();
         unsigned at = __reduce_add_sync(FULL, lane < warp ? warp_sum[lane] : 0u) + incl - mine;
         for (int s = s0; s < s1; ++s) {
@@ -305,10 +324,25 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
             const int L = len_sh[s];
             if (L > 0) at += ((unsigned)(L + ST - 1) / ST + kPairCost) * p.n_groups;
         }
-        if (threadIdx.x == NTHREADS - 1) {
-            pre[p.n_seqs] = at;
-            const unsigned n = max(1u, min(gridDim.x * (NW / p.hg), at / kMinSpan));
-            span_sh = Spans{n, at / n, at % n};
+        if (warp == NW - 1) {
+            longest = __reduce_max_sync(FULL, lane < NW ? warp_max[lane] : 0);
+            if (lane == 31) {
+                pre[p.n_seqs] = at;
+                // few pairs: no more parts than pay (kPartCost)
+                const float n_long = (float)((longest + ST - 1) / ST);
+                const float cost = kPartCost * (float)((p.rows * D + 127) / 128) * n_long;
+                const unsigned in_cta = NW / p.hg, teams = gridDim.x * in_cta;
+                auto cut = [&](float c) {
+                    const unsigned least = max((unsigned)kMinSpan, (unsigned)sqrtf(c));
+                    return max(1u, min(teams, at / least));
+                };
+                unsigned n = cut(cost), T = 1;
+                if (in_cta > 1 && n_long * (float)n > kMaxParts * (float)at) {
+                    T = in_cta;
+                    n = cut(cost / (float)T);
+                }
+                span_sh = Spans{n, at / n, at % n, T};
+            }
         }
         __syncthreads();
     }
@@ -520,8 +554,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     constexpr int SLOT8 = Q8 ? 2 : 8;    // SLOT8 further
     constexpr int KS = D / 16;           // k-steps of the scores
     const size_t rec_row = (size_t)p.rows * REC;
-    int2 cut = make_int2(-1, 0);   // (sequence, group) of the pair whose last part this span has
-    unsigned flag_slots = 0;       // the slots of its other parts
+    int2 cut = make_int2(-1, 0);   // (sequence, group) of the pair that began in an earlier span
+    bool goes_on = false;          // the last pair goes on in the next span
     int stage = 0;
     while (cur.s < p.n_seqs) {
         const int s = cur.s;
@@ -814,8 +848,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
             // A part: its record (slot 1 of the team for the pair's first part).
             const int slot = first == 0 ? 1 : 0;
             float *rec = p.recs + (((size_t)team * 2 + slot) * p.hg + hl) * rec_row;
-            if (last == n_tiles) cut = make_int2(s, cur.g);   // the last part: merges
-            else flag_slots |= 1u << slot;
+            if (slot == 0) cut = make_int2(s, cur.g);
+            else goes_on = true;
             float f[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) f[nt][0] = f[nt][1] = vs;
@@ -837,32 +871,54 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
-    if (flag_slots) {
+    const bool group_end = team % sp.T == sp.T - 1;
+    unsigned ub = 0, team0 = 0;          // the pair that began earlier: first stage's unit, first team
+    bool ends = false;                   // its last part is here
+    if (cut.x >= 0) {
+        const unsigned n_tiles = (unsigned)(len_sh[cut.x] + ST - 1) / ST;
+        ub = pre[cut.x] + (unsigned)cut.y * (n_tiles + kPairCost) + kPairCost;
+        ends = ub + n_tiles <= u_hi;
+    }
+    auto flag_parts = [&](bool slot0, bool slot1) {   // these records are for others to read
+        if (!slot0 && !slot1) return;
         __syncwarp();
         if (lane == 0) {
             fence_acq_rel_gpu();
-            for (int slot = 0; slot < 2; ++slot)
-                if (flag_slots >> slot & 1) st_relaxed(p.flags + (team * 2 + slot) * p.hg + hl, p.stamp);
+            if (slot0) st_relaxed(p.flags + team * 2 * p.hg + hl, p.stamp);
+            if (slot1) st_relaxed(p.flags + (team * 2 + 1) * p.hg + hl, p.stamp);
         }
-    }
-    if (cut.x < 0) return;
+    };
+    flag_parts(sp.T == 1 && cut.x >= 0 && !ends, goes_on && group_end);
+    if (sp.T > 1) __syncthreads();       // the CTA's records are written
+    if (cut.x < 0 || (!ends && (sp.T == 1 || !group_end))) return;   // (!ends: the CTA's last team merges it)
 
-    // Merge the pair whose last part this span has.  What another SM wrote
+    // The pair that began in an earlier span: merge its parts, first the
+    // CTA's, when this is the last of them, then, when this is the pair's last
+    // part, the CTAs' (T = 1: there is no first step).  What another SM wrote
     // takes about 1.2 us to arrive and a lone warp issues an instruction every
     // few cycles, so the loads of a step go out together and few instructions
     // lie between: a lane takes ITEMS (row, four dims) items of AHEAD parts, 16
     // loads in all.
     __syncwarp();
-    const int n_tiles = (len_sh[cut.x] + ST - 1) / ST;
-    const unsigned team0 = sp.owner(pre[cut.x] + (unsigned)cut.y * (n_tiles + kPairCost) + kPairCost);
-    const int n_parts = (int)(team - team0) + 1;
+    team0 = sp.owner(ub);
+    const unsigned from0 = sp.T == 1 ? team : max(team0, team - team % sp.T);
+    const unsigned group0 = sp.T == 1 ? team0 : team0 / sp.T, group = sp.T == 1 ? team : team / sp.T;
     const int h = cut.y * p.hg + hl;
     const int q0 = p.cu_q ? p.cu_q[cut.x] : cut.x;
     const int nq = p.cu_q ? min(p.cu_q[cut.x + 1] - q0, p.rows / p.gh) : 1;
     const int n_rows = nq * p.gh;
-    // part k: slot 0 of team0 + k, but for the first one, its team's slot 1
-    auto place = [&](int k) { return ((team0 + k) * 2 + (k == 0 ? 1 : 0)) * p.hg + hl; };
-    {
+#pragma unroll 1
+    for (int level = from0 == team ? 1 : 0; level < 2; ++level) {   // (one part of the CTA: as it is)
+    // Part k of this level lies with this team (teams from0 .. this one, or the
+    // last team of each CTA that has a part): in slot 1 of the pair's first.
+    const int n_parts = (int)(level == 0 ? team - from0 : group - group0) + 1;
+    const unsigned u0 = level == 0 ? from0 : group0 * sp.T + sp.T - 1, step = level == 0 ? 1 : sp.T;
+    auto place = [&](int k) {
+        const unsigned u = min(team, u0 + k * step);
+        return (u * 2 + (u == team0 ? 1 : 0)) * p.hg + hl;
+    };
+    const bool last_level = level == 1 || (ends && from0 == team0);
+    if (level == 1) {
         unsigned long long since = 0;
         for (int k0 = 0; k0 < n_parts - 1; k0 += 32) {
             unsigned *flag = p.flags + place(min(k0 + lane, n_parts - 2));
@@ -979,6 +1035,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                     s4 = acc[i];
                     continue;
                 }
+                if (!last_level) {       // in place of the last part's (whose items no other lane reads)
+                    *reinterpret_cast<float4 *>(p.recs + place(n_parts - 1) * rec_row + row[i] * REC + d4) = acc[i];
+                    continue;
+                }
                 const int j = nq > 1 ? row[i] / p.gh : 0;
                 const float f = 1.0f / sum_l[row[i]];
                 const size_t o = ((size_t)(q0 + j) * p.n_q_heads + (size_t)h * p.gh + row[i] - j * p.gh) * D + d4;
@@ -994,6 +1054,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         if (items <= 32) combine(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
         else combine(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
         __syncwarp();
+    }
+    if (last_level) return;
+    if (lane < n_rows)
+        *reinterpret_cast<float2 *>(p.recs + place(n_parts - 1) * rec_row + lane * REC + D) =
+            make_float2(sum_l[16 + lane], sum_l[lane]);
+    __syncwarp();
+    if (!ends) {
+        flag_parts(true, false);
+        return;
+    }
     }
 }
 

@@ -117,3 +117,61 @@ def test_flags(pkv, cuda_dev):
         bad[1, 1] = 10 ** 6
         pkv.pf_paged_cross_attention(c.pool, 0, q, dev(bad, cuda_dev), c.lens_dev, cu, 3, 0.125, out, work)
         assert pkv.pf_device_status(reset=True) == pkv.PF_DEV_BAD_BLOCK_ID
+
+
+@pytest.mark.parametrize("hq,d,tokens", [(1, 64, 1 << 20), (16, 128, 1 << 19), (3, 128, 40000)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_very_long_context(pkv, cuda_dev, hq, d, tokens, f32):
+    """One long context over all SMs, its parts merged by CTA and then over the
+    CTAs: a table that names the same eight pages over and over, so the result
+    is that of those pages once."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [8 * 256], hq, 1, d, 256)
+    reps = tokens // (8 * 256)
+    table = np.tile(c.bt, (1, reps))
+    lens = dev(np.array([reps * 8 * 256], np.int32), cuda_dev)
+    q = np.random.default_rng(1).standard_normal((1, hq, d)).astype(np.float16)
+    out = torch.empty((1, hq, d), dtype=torch.float32 if f32 else torch.float16, device=cuda_dev)
+    ws = pkv.make_cross_workspace(c.pool, 1, hq, table.shape[1], 1)
+    scale = float(np.float32(d ** -0.5))
+    table, cu = dev(table, cuda_dev), dev(np.array([0, 1], np.int32), cuda_dev)
+    t = np.arange(8 * 256)
+    k, v = (x[0][c.bt[0][t // 256], t % 256] for x in (c.k_host, c.v_host))
+    want, tol = attention64(q, k, v, scale, False, 2.0 ** -21 if f32 else F16, F32 if f32 else F16)
+    # sums over `tokens` terms, not over the eight pages': a warp adds its stages' products to its part in
+    # order (at most 2^9 of them here, each step off by 2^-23 of the sum), then 2^8 parts at most
+    tol = tol + np.abs(v.astype(np.float64)).mean() * 2 * (2.0 ** 9 + 2.0 ** 8) * 2.0 ** -23
+    for _ in range(2):
+        pkv.pf_paged_cross_attention(c.pool, 0, dev(q, cuda_dev), table, lens, cu, 1, scale, out, ws)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out), want, tol)
+
+
+@pytest.mark.parametrize("lens,new,ws", [([3000, 700], [2, 1], True), ([300, 64], [140, 130], False)])
+def test_captured_and_replayed(pkv, cuda_dev, lens, new, ws):
+    """Two captured calls that share a workspace, replayed in turn on new inputs."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, lens, 4, 2, 64, 16)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    cu = dev(offs, cuda_dev)
+    work = pkv.make_cross_workspace(c.pool, 2, 4, c.bt.shape[1], max(new)) if ws else None
+    q = torch.zeros((int(offs[-1]), 4, 64), dtype=torch.float16, device=cuda_dev)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    call = lambda o: pkv.pf_paged_cross_attention(c.pool, 0, q, c.bt_dev, c.lens_dev, cu, max(new), 0.125, o, work)   # noqa: E731
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call(outs[0])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            call(o)
+    rng = np.random.default_rng(2)
+    rows = [[x[0][c.bt[s][np.arange(L) // 16], np.arange(L) % 16] for x in (c.k_host, c.v_host)] for s, L in enumerate(lens)]
+    for i in range(4):
+        qn = rng.standard_normal(tuple(q.shape)).astype(np.float16)
+        q.copy_(dev(qn, cuda_dev))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        got = [attention64(qn[offs[s]:offs[s + 1]], *rows[s], 0.125, False, F16, F16) for s in range(2)]
+        assert_within(host(outs[i % 2]), np.concatenate([o for o, _ in got]), np.concatenate([t for _, t in got]))
