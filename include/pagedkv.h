@@ -499,7 +499,7 @@ PF_API int pf_paged_decode_attention_noalloc(const pf_pool *pool, int layer,
                                              void *stream);
 
 /* Testing hook for the bounded waits (no counterpart on the pages): block 0
- * of the next decode-attention launch in this process
+ * of the next decode-attention launch over an fp16 pool in this process
  * (pf_paged_decode_attention, pf_decode_step, the noalloc variant, or the
  * decode-kernel path of pf_paged_prefill_attention) leaves the first stage of
  * its copy ring unfilled.  Every wait in the library gives up after 1 s: the

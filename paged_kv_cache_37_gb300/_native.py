@@ -352,6 +352,8 @@ def pf_copy_blocks(pool, src_ids, dst_ids, stream=None):
     n = src_ids.numel()
     if dst_ids.numel() != n:
         raise PagedKVError(PF_ERR_INVALID, "src_ids and dst_ids must have the same length")
+    if pool.k_scale is not None:
+        _on_current_device(pool, (src_ids, dst_ids))
     _check(lib().pf_copy_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32),
                                 _dev_ptr(dst_ids, "dst_ids", torch.int32), n, _stream_ptr(stream)))
 
@@ -506,6 +508,8 @@ def pf_gather_kv(pool, layer, block_tables, context_lens, cu_off, k_out, v_out, 
     n = context_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != n or cu_off.numel() < n:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_off needs n_seqs entries")
+    if pool.k_scale is not None:
+        _on_current_device(pool, (block_tables, context_lens, cu_off, k_out, v_out))
     _check(lib().pf_gather_kv(pool.handle, layer, _dev_ptr(block_tables, "block_tables", torch.int32),
                               block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
                               _dev_ptr(cu_off, "cu_off", torch.int64), n,
