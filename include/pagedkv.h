@@ -420,7 +420,8 @@ PF_API int pf_decode_step(const pf_pool *pool, int layer, const void *q,
  * (165 KB of shared memory at head_dim 64, 197 KB at 128, and all 512
  * tensor-memory columns).
  * 8-bit pools (rows written by pf_append_kv): with a workspace and rows <= 16
- * on any page size, a kernel that reads every K/V byte once; otherwise the
+ * on any page size, a kernel that reads every K/V byte once, or with fp16
+ * output and small batches of short tables the tcgen05 kernel; otherwise the
  * tcgen05 kernel, its loaders widening the codes. */
 PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
                                       const void *q,
@@ -455,7 +456,8 @@ PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
  * once with pf_decode_workspace_init, not shared by overlapping calls) and at
  * most 16 query rows (tokens x q-heads) per kv-head, a kernel that cuts long
  * contexts over the SMs, fp32 output with the weights to about 22 bits;
- * otherwise the tcgen05 kernel, the weights rounded to fp16. */
+ * otherwise, and for fp16 output of small batches with short tables, the
+ * tcgen05 kernel, the weights rounded to fp16. */
 PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
                              int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q,
                              int n_seqs, int max_q_tokens, int n_q_heads, float scale, void *out, int out_dtype,
@@ -476,7 +478,8 @@ PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_
  * exits).  Nothing is allocated.
  * - A batch whose scratch need (pf_decode_workspace_bytes) exceeds 8 MiB is
  *   rejected with PF_ERR_INVALID; split the batch or pass a workspace to
- *   pf_paged_decode_attention.
+ *   pf_paged_decode_attention.  (8-bit pools, whose need does not depend on
+ *   the batch: the call runs on as many SMs as the scratch serves.)
  * - The first call on a device looks up the array's device address (once
  *   per device, with that device current); make that first call before any
  *   stream capture.

@@ -320,18 +320,50 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
     return PF_OK;
 }
 
+// Whether a call of few rows takes the prompt kernel, whose blocks (one per
+// sequence and kv-head) need no partition and no merge, instead of a cut over
+// all SMs.  A wave of its blocks takes about 4 + steps microseconds, steps of
+// 128 tokens (64 at head_dim 128; twice as many where fp16 pages hold one
+// token each) at the table's longest context.  Measured, 8 kv-heads, few-rows
+// kernel / prompt kernel in microseconds:
+//   4 sequences, 1 row x 64 values, fp16: 100 tokens 10.9 / 5.8, 1024 tokens
+//   14.4 / 12.3, 1536 tokens 14.9 / 15.9; x 128, e4m3: 512 tokens 14.7 / 12.1,
+//   1024 tokens 17.0 / 19.2; 16 rows x 128, fp16: 512 tokens 31.8 / 11.1, 1024
+//   tokens 36.0 / 17.9, 8192 tokens 59.6 / 109;
+//   38 sequences (two waves), 1 row x 64, e4m3: 128 tokens 10.4 / 12.5; 16 rows
+//   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1.
+// fp32 results stay with the few-rows kernel, which does not round its weights
+// to fp16.
+static bool prompt_kernel_pays(const pkv::RowsArgs &a) {
+    if (a.out_dtype != PF_F16) return false;
+    const long long items = (long long)a.n_seqs * a.pool->n_kv_heads;
+    const long long waves = (items + a.plan.sms - 1) / a.plan.sms;
+    const int step = a.pool->head_dim == 64 ? 128 : 64;
+    long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
+    if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
+    const bool wide = a.rows * a.pool->head_dim > 512;   // parts cost the few-rows kernel most
+    return waves <= (wide ? 2 : 1) && waves * (4 + steps) <= (wide ? 20 : 12);
+}
+
 // The few-rows kernel with a checked workspace (decode and short appends over
-// PF_E4M3 pools, short cross attention).
-static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const char *fn, void *stream) {
+// PF_E4M3 pools, short cross attention), or for small calls the prompt kernel.
+static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const char *fn, void *stream,
+                     bool fit = false) {
     if (!aligned16(workspace))
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace must be 16-byte aligned");
     if (a.max_blocks <= 0 || (long long)a.max_blocks * a.pool->block_size > (1ll << 30))
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad max_blocks_per_seq");
-    int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan);
+    int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan, fit ? ws_bytes : SIZE_MAX);
     if (rc) return rc;
     if (ws_bytes < a.plan.bytes)
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
                                                   " bytes, needs " + std::to_string(a.plan.bytes));
+    if (prompt_kernel_pays(a)) {
+        pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
+                           a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
+                           a.causal && a.cu_q};
+        return pkv::launch_prefill_tc(b, static_cast<cudaStream_t>(stream));
+    }
     a.workspace = workspace;
     return pkv::launch_rows(a, static_cast<cudaStream_t>(stream));
 }
@@ -341,7 +373,7 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
 static int decode_call(const pf_pool *pool, int layer, const void *q, const void *k_new, const void *v_new,
                        bool overlap_previous, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
                        int n_seqs, int n_q_heads, float scale, void *out, int out_dtype, int split_tokens,
-                       void *workspace, size_t ws_bytes, void *stream) {
+                       void *workspace, size_t ws_bytes, void *stream, bool fit = false) {
     int rc = check_pool(pool, layer, "pf_paged_decode_attention");
     if (rc) return rc;
     if (n_seqs < 0) return pkv::set_error(PF_ERR_INVALID, "pf_paged_decode_attention: negative n_seqs");
@@ -370,7 +402,7 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
             return pkv::set_error(PF_ERR_UNSUPPORTED,
                                   "pf_paged_decode_attention: PF_E4M3 pools take split_tokens = 0");
         pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, nullptr, n_seqs, n_q_heads,
-                        group, true, scale, out, out_dtype, {}, nullptr};
+                        group, true, scale, out, out_dtype, {}, nullptr, false};
         if (k_new) {
             // the append first: a launch of its own, since a page's new scale is needed before any of its rows
             pkv::AppendArgs w{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, nullptr,
@@ -385,8 +417,9 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: bad max_blocks_per_seq");
             rc = pkv::launch_append(w, static_cast<cudaStream_t>(stream));
             if (rc) return rc;
+            a.after_append = true;
         }
-        return rows_call(a, workspace, ws_bytes, "pf_paged_decode_attention", stream);
+        return rows_call(a, workspace, ws_bytes, "pf_paged_decode_attention", stream, fit);
     }
     pkv::AttnPlan plan;
     // host-only checks first (no device query), then the device-sized plan
@@ -497,7 +530,7 @@ int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, co
     const int rows = append_rows(pool, n_q_heads, max_new_tokens);
     if (workspace != nullptr && rows > 0 && pool->dtype == PF_E4M3) {
         pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
-                        rows, true, scale, out, out_dtype, {}, nullptr};
+                        rows, true, scale, out, out_dtype, {}, nullptr, false};
         return rows_call(a, workspace, ws_bytes, "pf_paged_prefill_attention", stream);
     }
     if (workspace != nullptr && rows > 0) {
@@ -571,7 +604,7 @@ int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, cons
     const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
     if (workspace != nullptr && rows > 0) {
         pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
-                        rows, false, scale, out, out_dtype, {}, nullptr};
+                        rows, false, scale, out, out_dtype, {}, nullptr, false};
         return rows_call(a, workspace, ws_bytes, "pf_paged_cross_attention", stream);
     }
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_q_tokens,
@@ -599,3 +632,14 @@ int pf_device_status(int *status_out, int reset, void *stream) {
 }
 
 }  // extern "C"
+
+namespace pkv {
+
+int decode_on_scratch(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables, int max_blocks,
+                      const int32_t *context_lens, int n_seqs, int n_q_heads, float scale, void *out, int out_dtype,
+                      int split_tokens, void *scratch, size_t bytes, void *stream) {
+    return decode_call(pool, layer, q, nullptr, nullptr, false, block_tables, max_blocks, context_lens, n_seqs,
+                       n_q_heads, scale, out, out_dtype, split_tokens, scratch, bytes, stream, true);
+}
+
+}  // namespace pkv

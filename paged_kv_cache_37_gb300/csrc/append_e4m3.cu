@@ -16,7 +16,9 @@
 // Rows of inf or NaN are flagged; inf is stored as the largest magnitude, NaN
 // as 0, and neither counts for the scale.
 //
-// Append: 2 bytes read and 1 written per value, HBM bound.  One group of
+// Append: 2 bytes read and 1 written per value, HBM bound: 8192 tokens of 40
+// heads x 128 take 39.7 us, 6.35 TB/s; one token each for 128 sequences 3.1 us,
+// a launch and three dependent loads.  One group of
 // threads takes one (page, kv-head, K or V) and keeps all its new rows in
 // registers between the maximum and the rounding, so they are read once; the
 // group is a warp for 16-token pages (4 or 8 16-byte loads in flight per
@@ -79,6 +81,7 @@ __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t w, __half2 by) {
 template <int B, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
     using S = AppendShape<B, D>;
+    griddep_launch();   // the attention of a fused step sets out; it waits for this grid's end before it reads a page
     constexpr int CPR = D / 8;                     // chunks of a row
     __shared__ uint32_t warp_max[kThreads / 32];
     const int s = blockIdx.x / p.blocks_per_seq;

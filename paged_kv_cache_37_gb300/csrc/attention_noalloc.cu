@@ -55,7 +55,8 @@ extern "C" int pf_paged_decode_attention_noalloc(const pf_pool *pool, int layer,
     if (!pool) return pkv::set_error(PF_ERR_INVALID, "pf_paged_decode_attention_noalloc: pool is null");
     const size_t need = pf_decode_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens);
     if (need == 0) return PF_ERR_INVALID;   // message set by pf_decode_workspace_bytes
-    if (need > pkv::kNoAllocScratchBytes)
+    const bool q8 = pool->dtype == PF_E4M3;   // its workspace grows with the SMs, not with the batch
+    if (need > pkv::kNoAllocScratchBytes && !q8)
         return pkv::set_error(PF_ERR_INVALID,
                               "pf_paged_decode_attention_noalloc: this batch needs " + std::to_string(need) +
                                   " bytes of scratch but the built-in scratch holds " +
@@ -68,6 +69,10 @@ extern "C" int pf_paged_decode_attention_noalloc(const pf_pool *pool, int layer,
     // back (merge jobs, span records) carries the epoch of the launch that
     // wrote it, so nothing left by an earlier call -- one that timed out
     // included -- is taken for this call's data, and nothing needs resetting.
+    // (8-bit pools: what a call writes to read back, it clears.)
+    if (q8)
+        return pkv::decode_on_scratch(pool, layer, q, block_tables, max_blocks_per_seq, context_lens, n_seqs, n_q_heads,
+                                      scale, out, out_dtype, split_tokens, ws, pkv::kNoAllocScratchBytes, stream);
     return pf_paged_decode_attention(pool, layer, q, block_tables, max_blocks_per_seq, context_lens, n_seqs,
                                      n_q_heads, scale, out, out_dtype, split_tokens, ws, pkv::kNoAllocScratchBytes,
                                      stream);

@@ -152,6 +152,7 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
 // A kernel launched as a programmatic dependent waits here for the kernels
 // before it (complete, their writes visible).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 1-D bulk copy global -> shared, completing `bytes` on the mbarrier.
 // Both addresses 16-byte aligned, bytes a multiple of 16.

@@ -127,7 +127,7 @@ struct PrefillArgs {
     const int32_t *block_tables;
     int max_blocks;
     const int32_t *context_lens;
-    const int32_t *cu_q;
+    const int32_t *cu_q;   // null (not causal): one query per sequence, row s
     int n_seqs;
     int max_new;
     int n_q_heads;
@@ -162,11 +162,19 @@ unsigned next_epoch();
 // rows; the workspace holds the parts of cut sequences.
 constexpr int kMaxRows = 16;
 struct RowsPlan {
+    int sms;
     int grid;
     size_t flag_bytes;
     size_t bytes;   // of the workspace
 };
-int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan);
+// With as many CTAs as the device has SMs, or fewer whose workspace fits into
+// `most` bytes.
+int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan, size_t most = SIZE_MAX);
+// pf_paged_decode_attention over an 8-bit pool on as many SMs as a scratch of
+// `bytes` serves (abi.cpp).
+int decode_on_scratch(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables, int max_blocks,
+                      const int32_t *context_lens, int n_seqs, int n_q_heads, float scale, void *out, int out_dtype,
+                      int split_tokens, void *scratch, size_t bytes, void *stream);
 struct RowsArgs {
     const pf_pool *pool;
     int layer;
@@ -184,6 +192,7 @@ struct RowsArgs {
     int out_dtype;
     RowsPlan plan;
     void *workspace;
+    bool after_append;     // the stream's previous kernel is this call's append
 };
 int launch_rows(const RowsArgs &a, cudaStream_t stream);
 

@@ -36,17 +36,17 @@
 // other; with four stages the scores of the next tiles are computed while
 // the softmax threads exponentiate.
 //
-// Measured bounds (GB300, clock64 traces and single-CTA microbenchmarks of
-// tcgen05.mma kind::f16, M = 128, K = 16): one MMA costs about 100 cycles
-// with A and B in shared memory at N = 128 and about 71 with A in tensor
-// memory at N = 64 or 128 -- so P lives in tensor memory and the row sums
-// are summed on the CUDA cores rather than by another MMA over P.  A K/V
-// step of head_dim 64 (24 MMAs) then takes about 2,400 cycles.  TMA boxes
-// issued from one warp arrive at a few hundred cycles each whatever their
-// size, and the rate grows with the number of issuing warps (measured: 1, 2,
-// 4 warps -> 11.8, 23.4, 44 bytes a cycle per SM on 8 KB boxes), hence two
-// loader warps per tensor; 16-byte cp.async from the loader warps was several
-// times slower than TMA.
+// Measured (GB300; 4 prompts of 2048 tokens): 12 heads x 64 46 us, 32 q-heads
+// over 8 kv-heads x 128 142 us, over an e4m3 pool 144 us.  What bounds it (clock64
+// traces): of a K/V step's 2,400 cycles at head_dim 64 the exponentials of two
+// query tiles take 2,050 on the MUFU pipe -- so P lives in tensor memory, the
+// row sums are summed on the CUDA cores rather than by another MMA over P, and
+// nothing else of a step may wait.  At head_dim 128 MMAs and softmax share it.
+// TMA boxes issued from one warp arrive at a few hundred cycles each whatever
+// their size, and the rate grows with the number of issuing warps (measured:
+// 1, 2, 4 warps -> 11.8, 23.4, 44 bytes a cycle per SM on 8 KB boxes), hence
+// two loader warps per tensor; 16-byte cp.async from the loader warps was
+// several times slower than TMA.
 //
 // e4m3 pools (Q8): the loader warps bring each tile's codes into a ring of
 // raw stages by 16-byte cp.async (a lane copies the chunks that it widens
@@ -57,6 +57,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 #include <string>
 #include <type_traits>
@@ -399,8 +400,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (flagger) atomicOr(p.status, PF_DEV_BAD_LENGTH);
         L = L < 0 ? 0 : maxctx;
     }
-    const int q0 = p.cu_q[s];
-    int n = p.cu_q[s + 1] - q0;
+    const int q0 = CAUSAL || p.cu_q ? p.cu_q[s] : s;
+    int n = CAUSAL || p.cu_q ? p.cu_q[s + 1] - q0 : 1;
     if (n < 0 || (CAUSAL && n > L) || n > p.max_new) {
         if (flagger) atomicOr(p.status, PF_DEV_BAD_LENGTH);
         n = n < 0 ? 0 : min(CAUSAL ? min(n, L) : n, p.max_new);
@@ -1073,8 +1074,14 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
         D == 64 ? prefill_tc::pick<64>(a.causal, q8) : prefill_tc::pick<128>(a.causal, q8);
     const int smem = D == 64 ? (q8 ? prefill_tc::Cfg<64, true>::SMEM : prefill_tc::Cfg<64, false>::SMEM)
                              : (q8 ? prefill_tc::Cfg<128, true>::SMEM : prefill_tc::Cfg<128, false>::SMEM);
-    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: cudaFuncSetAttribute");
+    // once per device and kernel (setting it twice does no harm)
+    static std::atomic<bool> ready[kMaxDevices][8];
+    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * a.causal + 4 * q8];
+    if (!done.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: cudaFuncSetAttribute");
+        done.store(true, std::memory_order_release);
+    }
     fn<<<(unsigned)(n_items * n_qp), prefill_tc::NTHREADS, smem, stream>>>(pool->tmap_pf_k[dev], pool->tmap_pf_v[dev],
                                                                            p);
     e = cudaGetLastError();

@@ -27,7 +27,7 @@ rows::Kernel kernel_for(const pf_pool *pool, int n_rows, bool f32) {
 
 }  // namespace
 
-int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan) {
+int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan, size_t most) {
     static std::atomic<int> known[kMaxDevices];   // SMs per device, 0: not asked yet
     int sms = 0, dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -41,11 +41,16 @@ int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan)
         if (need_device) return cuda_error(e, "attention: SM count");
         sms = kSmsNoDevice;
     }
-    plan->grid = sms;
+    plan->sms = sms;
     const int hg = heads_per_team(pool->n_kv_heads);
-    const size_t warps = (size_t)plan->grid * (kernel_for(pool, n_rows, false).warps / hg) * hg;
-    plan->flag_bytes = (warps * 2 * sizeof(unsigned) + 255) / 256 * 256;
-    plan->bytes = kReserved + plan->flag_bytes + warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
+    const size_t warps = (size_t)(kernel_for(pool, n_rows, false).warps / hg) * hg;   // of a CTA
+    const size_t recs = warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
+    // (the flags of all SMs, rounded up, come first)
+    plan->flag_bytes = (sms * warps * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    const size_t front = kReserved + plan->flag_bytes;
+    plan->grid = most < front + sms * recs ? (int)(most < front ? 0 : (most - front) / recs) : sms;
+    if (plan->grid == 0) return set_error(PF_ERR_INVALID, "attention: the scratch holds no block's records");
+    plan->bytes = front + plan->grid * recs;
     return PF_OK;
 }
 
@@ -108,6 +113,7 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
         p.cu_q = a.cu_q ? a.cu_q + s0 : nullptr;
         p.n_seqs = a.n_seqs - s0 < step ? a.n_seqs - s0 : step;
         p.stamp = next_epoch() | 0x80000000u;
+        p.after_append = a.after_append && s0 == 0;
         // a programmatic dependent of the kernel before it: its blocks take
         // their SMs as that kernel's leave them, and then wait for its end
         cudaLaunchConfig_t cfg = {};

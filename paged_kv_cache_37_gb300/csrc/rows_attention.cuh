@@ -1,6 +1,7 @@
 // rows_attention.cuh -- attention of a few query rows per (sequence, kv-head)
 // over the paged cache: decode and short appends over an e4m3 pool, short
-// cross attention over either pool type.
+// cross attention over either pool type.  (fp16 results of small batches with
+// short tables come from the prompt kernel, which needs no partition.)
 //
 // For a (sequence s, kv-head h) with L tokens and at most 16 query rows (its
 // query tokens x its gh q-heads, row r = i * gh + g of token i):
@@ -9,7 +10,10 @@
 // k_scale[page][h], V_t = code * v_scale[page][h].
 //
 // Bound: every K and V byte of the context is read once and used for at most
-// 16 rows, so HBM bounds it; the rest is kept below that.
+// 16 rows, so HBM bounds it; the rest is kept below that.  Measured on GB300:
+// 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 24.1 us, of
+// which about 10 are the way to the first rows and the last merge; 16 x 2048
+// tokens, 40 heads x 128, fp32 results (336 MB) 64 us, 5.3 TB/s.
 // * Work: stages of ST tokens (a 4 KB piece of K and V for one head at 64-
 //   and 128-byte rows).  The stages of all (sequence, group of HG kv-heads)
 //   pairs are cut into equal spans, one per team of HG warps; warp hl of a
@@ -66,10 +70,18 @@ constexpr float kNoScore = -1.0e30f; // m before any score
 constexpr unsigned FULL = 0xffffffffu;
 
 // Cost of a (sequence, group) pair in the partition, in stages: entering one
-// costs a q load, a merge of lanes and a store.
+// costs a q load, a merge of lanes and a store.  (Measured with 1, 2, 4: the
+// mixed batch of 128 sequences, 12 heads x 64, e4m3, 25.8, 24.1, 25.0 us.)
 constexpr int kPairCost = 2;
 // Least units per span: shorter ones cost more in merges than they bring.
-constexpr int kMinSpan = 4;
+// (Measured with 1, 2, 4, 8: 512 sequences of 32 tokens, 4 heads x 64, 7.6,
+// 7.6, 9.9, 13.5 us; one of 2048 tokens, 40 heads x 128, 17.2, 17.1, 18.1,
+// 21.4; 32 of up to 512 tokens, 4 rows, 13.6, 13.7, 13.4, 15.9.)
+constexpr int kMinSpan = 2;
+// With two levels.  (Measured with 2, 4, 6: 4 sequences of up to 4000 tokens, 8
+// heads x 128, 20.0, 19.4, 20.3 us and, other lengths, 21.9, 18.4; 8 sequences,
+// 4 rows x 64, 17.2, 18.3, 20.1.)
+constexpr int kMinSpan2 = 4;
 // A pair of n stages in spans of x takes x stages, then the merge of n / x
 // parts, each kPartCost stages per 128 values of its rows: least at x =
 // sqrt(kPartCost * values / 128 * n).
@@ -77,10 +89,15 @@ constexpr int kMinSpan = 4;
 // dims 28.6, 26.6, 29.8, 34.6 us; 14 of 1,600, 16 rows, 64 dims 24.6, 23.9,
 // 25.5, 29.8.)
 constexpr float kPartCost = 0.125f;
-// More parts than this per longest pair: merged in two levels.
+// More parts than this per longest pair: merged in two levels.  (Measured with
+// 6, 12, 24 and one level only: 32 sequences of up to 512 tokens, 4 rows, 14.7,
+// 13.4, 13.3, 13.4 us; 6 of 2,700 tokens, 4 rows x 128, 21.1, 21.0, 26.6, 26.6;
+// one of 65,536 tokens, 4 rows x 128, 37.3, 37.4, 37.4, 88.6.)
 constexpr float kMaxParts = 12.0f;
 // A cut inside a pair of at most this many stages moves to the pair's nearer
-// edge: such pairs stay whole and need no merge.
+// edge: such pairs stay whole and need no merge.  (Measured with 0, 4, 8 and
+// spans of at least 4: 4 sequences of up to 100 tokens, 12 heads x 64, 11.7,
+// 10.2, 10.3 us; larger batches the same within 1 %.)
 constexpr int kWhole = 4;
 
 struct Params {
@@ -109,6 +126,7 @@ struct Params {
     int n_groups;
     int rows;               // rows per kv-head the call allows
     int causal;
+    int after_append;       // the previous kernel wrote pages only: set out before it ends
     int out_f32;
     long long layer_row0;   // layer * n_blocks * block_size
     long long layer_page0;  // layer * n_blocks
@@ -281,8 +299,9 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     const int lane = (int)threadIdx.x % 32;
 
     // Launched as a programmatic dependent: everything below may read what the
-    // stream's previous kernel wrote.
-    griddep_wait();
+    // stream's previous kernel wrote, or after a step's own append (which was
+    // launched when everything before it had ended) the pages only.
+    if (!p.after_append) griddep_wait();
 
     // The front of every table row into L2, shared out over the grid: the
     // lengths are not known yet.
@@ -332,14 +351,14 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                 const float n_long = (float)((longest + ST - 1) / ST);
                 const float cost = kPartCost * (float)((p.rows * D + 127) / 128) * n_long;
                 const unsigned in_cta = NW / p.hg, teams = gridDim.x * in_cta;
-                auto cut = [&](float c) {
-                    const unsigned least = max((unsigned)kMinSpan, (unsigned)sqrtf(c));
+                auto cut = [&](float c, int least_span) {
+                    const unsigned least = max((unsigned)least_span, (unsigned)sqrtf(c));
                     return max(1u, min(teams, at / least));
                 };
-                unsigned n = cut(cost), T = 1;
+                unsigned n = cut(cost, kMinSpan), T = 1;
                 if (in_cta > 1 && n_long * (float)n > kMaxParts * (float)at) {
                     T = in_cta;
-                    n = cut(cost / (float)T);
+                    n = cut(cost / (float)T, kMinSpan2);
                 }
                 span_sh = Spans{n, at / n, at % n, T};
             }
@@ -366,7 +385,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     const int hl = warp % p.hg;
     const unsigned team = blockIdx.x * (NW / p.hg) + warp / p.hg;
     const Spans sp = span_sh;
-    if (warp / p.hg >= NW / p.hg || team >= sp.n || pre[p.n_seqs] == 0) return;
+    if (warp / p.hg >= NW / p.hg || team >= sp.n || pre[p.n_seqs] == 0) {
+        if (p.after_append) griddep_wait();   // this grid does not end before the append's
+        return;
+    }
     // The pair that holds unit x: its sequence and group, and x's distance from
     // the pair's first unit.
     auto pair_at = [&](unsigned x, int &s, int &g, unsigned &per) {
@@ -541,6 +563,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     for (int k = 0; k < PF; ++k) ahead[k].n = 0;
 #pragma unroll 1
     for (int k = 0; k < PF; ++k) look_further();
+    if (p.after_append) griddep_wait();
 #pragma unroll 1
     for (int k = 0; k < PF; ++k) {
         copy(k, ahead[0]);

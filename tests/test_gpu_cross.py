@@ -30,6 +30,17 @@ CASES = [
 @pytest.mark.parametrize("cache", ["f16", "e4m3"])
 @pytest.mark.parametrize("f32", [False, True])
 def test_cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32):
+    _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32, False)
+
+
+@pytest.mark.parametrize("lens,new,hq,h,d,page,ws", CASES[:6])
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+def test_cross_wide_table(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache):
+    """Tables with room for 4096 more tokens: fp16 results from the few-rows kernel as well."""
+    _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, False, True)
+
+
+def _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32, wide):
     import torch
     offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     rng = np.random.default_rng(9)
@@ -58,6 +69,8 @@ def test_cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32):
         pool, table, lens_dev = c.pool, c.table_dev, dev(c.lens, cuda_dev)
         want, tol = c.want(q, offs, False, step, F32 if f32 else F16)
         tol = tol + 2.0 ** -25 + 2 * 2.0 ** -25 * scale * np.abs(q.astype(np.float64)).sum(-1).max() * 64
+    if wide:
+        table = torch.nn.functional.pad(table, (0, 4096 // page), value=1 << 30)
     out = torch.full((int(offs[-1]) + 1, hq, d), 7.0, dtype=torch.float32 if f32 else torch.float16, device=cuda_dev)
     work = pkv.make_cross_workspace(pool, len(lens), hq, table.shape[1], max(new)) if ws else None
     assert (work is not None) == work_small

@@ -87,6 +87,22 @@ class Case:
                             self.scale(), causal, weight_step, out_step) for s, L in enumerate(self.lens)]
         return np.concatenate([o for o, _ in outs]), np.concatenate([t for _, t in outs])
 
+    def small_weights(self, offs):
+        """What want() leaves out: weights that the few-rows kernel stores as
+        subnormal fp16.  It stores 2^7 w / w_max (at least 2^7 for the largest
+        weight) times a V scale over the largest V scale S met, and takes it
+        times code * S.  Below 2^-14 the rounding is off by 2^-25 instead of
+        2^-11 relative, which moves the mean by at most
+        2^-25 / 2^7 * |code| * S for each token, sum w / w_max being at least 1."""
+        out = []
+        for s, L in enumerate(self.lens):
+            t = np.arange(L)
+            blk = self.table[s][t // self.B]
+            top = self.vm.scale[blk].max(0)[:, None] if L else 0.0                      # [H, 1]
+            x = 2.0 ** -32 * np.abs(self.vm.code[blk, t % self.B]).sum(0) * top           # [H, D]
+            out.append(np.broadcast_to(np.repeat(x, self.Hq // self.H, 0), (offs[s + 1] - offs[s], self.Hq, self.D)))
+        return np.concatenate(out)
+
     def scale(self):
         return float(np.float32(1.0 / np.sqrt(self.D)))
 
@@ -184,6 +200,72 @@ def test_decode(pkv, cuda_dev, lens, hq, h, d, page, f32):
     assert bool((out[-1] == 7.0).all())      # the row behind the last sequence
 
 
+def wide_table(c):
+    """The table with room for 4096 more tokens, whose entries name no block:
+    fp16 results then come from the few-rows kernel as well."""
+    return np.pad(c.table, ((0, 0), (0, 4096 // c.B)), constant_values=1 << 30)
+
+
+@pytest.mark.parametrize("lens,hq,h,d,page", CASES)
+def test_decode_wide_table(pkv, cuda_dev, lens, hq, h, d, page):
+    import torch
+    c = Case(pkv, cuda_dev, lens, hq, h, d, page, width=max(si.pages_for(max(lens), page), 2))
+    c.fill()
+    table = dev(wide_table(c), cuda_dev)
+    q = c.rng.standard_normal((len(lens), hq, d)).astype(np.float16)
+    out = torch.full((len(lens) + 1, hq, d), 7.0, dtype=torch.float16, device=cuda_dev)
+    ws = pkv.make_workspace(c.pool, len(lens), hq, table.shape[1], 0)
+    pkv.pf_device_status(reset=True)
+    for _ in range(2):
+        pkv.pf_paged_decode_attention(c.pool, 1, dev(q, cuda_dev), table, dev(c.lens, cuda_dev), c.scale(),
+                                      out[:-1], 0, ws)
+        assert pkv.pf_device_status(reset=True) == 0
+        want, tol = c.want(q, np.arange(len(lens) + 1), False, F16, F16)
+        assert_within(host(out)[:-1], want, tol + c.small_weights(np.arange(len(lens) + 1)))
+    assert bool((out[-1] == 7.0).all())
+
+
+@pytest.mark.parametrize("lens,hq,h,d,page", [([100, 0, 300], 12, 12, 64, 16), ([1, 2000], 8, 2, 128, 64),
+                                                ([900, 3, 0], 16, 1, 128, 16)])   # 122 and 41 blocks' records
+def test_decode_noalloc(pkv, cuda_dev, lens, hq, h, d, page):
+    """Without a workspace, tight table and wide: both kernels, the built-in scratch used twice."""
+    import torch
+    c = Case(pkv, cuda_dev, lens, hq, h, d, page)
+    c.fill()
+    q = c.rng.standard_normal((len(lens), hq, d)).astype(np.float16)
+    want, tol = c.want(q, np.arange(len(lens) + 1), False, F16, F16)
+    for table in (c.table, wide_table(c), wide_table(c)):
+        out = torch.full((len(lens), hq, d), 7.0, dtype=torch.float16, device=cuda_dev)
+        pkv.pf_paged_decode_attention_noalloc(c.pool, 1, dev(q, cuda_dev), dev(table, cuda_dev), dev(c.lens, cuda_dev),
+                                              c.scale(), out, 0)
+        assert_within(host(out), want, tol)
+
+
+def test_decode_step_wide_table(pkv, cuda_dev):
+    """Steps whose attention sets out while the append runs, then contexts that are all empty."""
+    import torch
+    lens = [33, 1, 16, 900, 0, 2000]
+    c = Case(pkv, cuda_dev, lens, 8, 4, 128, 16)
+    c.append(np.maximum(c.lens - 1, 0))
+    table, n = wide_table(c), len(lens)
+    q = c.rng.standard_normal((n, 8, 128)).astype(np.float16)
+    out = torch.empty((n, 8, 128), dtype=torch.float16, device=cuda_dev)
+    ws = pkv.make_workspace(c.pool, n, 8, table.shape[1], 0)
+    k, v = c.rows(n), c.rows(n)
+    args = (dev(q, cuda_dev), dev(k, cuda_dev), dev(v, cuda_dev), dev(table, cuda_dev))
+    pkv.pf_decode_step(c.pool, 1, *args, dev(c.lens, cuda_dev), c.scale(), out, 0, ws)
+    one = np.concatenate([[0], np.cumsum(c.lens > 0)])     # the empty context takes no row
+    c.km.append(k[c.lens > 0], c.table, c.lens, one)
+    c.vm.append(v[c.lens > 0], c.table, c.lens, one)
+    c.check_pool()
+    want, tol = c.want(q, np.arange(n + 1), False, F16, F16)
+    assert_within(host(out), want, tol + c.small_weights(np.arange(n + 1)))
+    pkv.pf_decode_step(c.pool, 1, *args, dev(np.zeros(n, np.int32), cuda_dev), c.scale(), out, 0, ws)
+    assert not host(out).any()
+    c.check_pool()
+    assert pkv.pf_device_status(reset=True) == 0
+
+
 @pytest.mark.parametrize("lens,new,hq,h,d,page,ws", [
     ([40, 17, 3, 300], [3, 1, 3, 0], 12, 12, 64, 16, True),
     ([40, 500, 16], [2, 2, 1], 14, 2, 64, 64, True),          # 14 rows per kv-head
@@ -217,7 +299,32 @@ def test_append_attention(pkv, cuda_dev, lens, new, hq, h, d, page, ws, f32):
     assert bool((out[-1] == 7.0).all())
 
 
-def test_wide_range_of_value_scales(pkv, cuda_dev):
+@pytest.mark.parametrize("lens,new,hq,h,d,page", [
+    ([40, 17, 3, 300], [3, 1, 3, 0], 12, 12, 64, 16),
+    ([40, 500, 16], [2, 2, 1], 14, 2, 64, 64),                # 14 rows per kv-head
+    ([100, 33], [16, 2], 5, 5, 128, 1),
+    ([1000, 16], [4, 4], 8, 2, 128, 256),
+])
+def test_append_attention_wide_table(pkv, cuda_dev, lens, new, hq, h, d, page):
+    import torch
+    c = Case(pkv, cuda_dev, lens, hq, h, d, page)
+    c.fill()
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = c.rng.standard_normal((int(offs[-1]), hq, d)).astype(np.float16)
+    out = torch.full((int(offs[-1]) + 1, hq, d), 7.0, dtype=torch.float16, device=cuda_dev)
+    table = dev(wide_table(c), cuda_dev)
+    work = pkv.make_prefill_workspace(c.pool, len(lens), hq, table.shape[1], max(new))
+    pkv.pf_device_status(reset=True)
+    pkv.pf_paged_prefill_attention(c.pool, 1, dev(q, cuda_dev), table, dev(c.lens, cuda_dev), dev(offs, cuda_dev),
+                                   max(new), c.scale(), out[:-1], work)
+    assert pkv.pf_device_status(reset=True) == 0
+    want, tol = c.want(q, offs, True, F16, F16)
+    assert_within(host(out)[:-1], want, tol + c.small_weights(offs))
+    assert bool((out[-1] == 7.0).all())
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_wide_range_of_value_scales(pkv, cuda_dev, wide):
     """Pages whose V scales differ by 2^20: an outlier page of little weight
     must not cost the others their precision."""
     import torch
@@ -232,8 +339,10 @@ def test_wide_range_of_value_scales(pkv, cuda_dev):
     q[:, :, 0] = 1.0
     for f32 in (False, True):
         out = torch.empty((1, 1, 64), dtype=torch.float32 if f32 else torch.float16, device=cuda_dev)
-        ws = pkv.make_workspace(c.pool, 1, 1, c.table.shape[1], 0)
-        pkv.pf_paged_decode_attention(c.pool, 1, dev(q, cuda_dev), c.table_dev, dev(c.lens, cuda_dev), c.scale(), out, 0, ws)
+        table = wide_table(c) if wide else c.table
+        ws = pkv.make_workspace(c.pool, 1, 1, table.shape[1], 0)
+        pkv.pf_paged_decode_attention(c.pool, 1, dev(q, cuda_dev), dev(table, cuda_dev), dev(c.lens, cuda_dev),
+                                      c.scale(), out, 0, ws)
         want, tol = c.want(q, [0, 1], False, 2.0 ** -21 if f32 else F16, F32 if f32 else F16)
         assert_within(host(out), want, tol)
 
