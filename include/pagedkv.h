@@ -421,8 +421,10 @@ PF_API int pf_decode_step(const pf_pool *pool, int layer, const void *q,
  * tensor-memory columns).
  * 8-bit pools (rows written by pf_append_kv): with a workspace and rows <= 16
  * on any page size, a kernel that reads every K/V byte once, or with fp16
- * output and small batches of short tables the tcgen05 kernel; otherwise the
- * tcgen05 kernel, its loaders widening the codes. */
+ * output and small batches the tcgen05 kernel; otherwise the tcgen05 kernel,
+ * its loaders widening the codes.  With a workspace the tcgen05 kernel cuts
+ * long contexts of few blocks over the SMs and merges the parts in a second
+ * launch. */
 PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
                                       const void *q,
                                       const int32_t *block_tables,
@@ -436,7 +438,9 @@ PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
 /* Workspace bytes of pf_paged_prefill_attention's decode-kernel path for
  * these sizes, or 0 when that path does not apply (more than 16 rows per
  * kv-head, or 8 on pages of fewer than 16 tokens; the call then needs no
- * workspace) or on bad arguments. */
+ * workspace) or on bad arguments.  8-bit pools: also what the tcgen05 kernel
+ * takes to cut these sizes' contexts over the SMs (a call without a workspace
+ * does not cut them; one with fewer bytes is refused). */
 PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
                                          int n_q_heads, int max_blocks_per_seq,
                                          int max_new_tokens);
@@ -456,14 +460,17 @@ PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
  * once with pf_decode_workspace_init, not shared by overlapping calls) and at
  * most 16 query rows (tokens x q-heads) per kv-head, a kernel that cuts long
  * contexts over the SMs, fp32 output with the weights to about 22 bits;
- * otherwise, and for fp16 output of small batches with short tables, the
- * tcgen05 kernel, the weights rounded to fp16. */
+ * otherwise, and for fp16 output of small batches, the tcgen05 kernel, the
+ * weights rounded to fp16; with a workspace it cuts long contexts of few
+ * blocks over the SMs and merges the parts in a second launch. */
 PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
                              int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q,
                              int n_seqs, int max_q_tokens, int n_q_heads, float scale, void *out, int out_dtype,
                              void *workspace, size_t ws_bytes, void *stream);
 /* Workspace bytes of pf_paged_cross_attention for these sizes, or 0 when it
- * needs none (more than 16 rows per kv-head) or on bad arguments. */
+ * needs none (more than 16 rows per kv-head and contexts that are not worth
+ * cutting) or on bad arguments.  The call takes no less; NULL instead runs on
+ * the tcgen05 kernel, uncut. */
 PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                 int max_q_tokens);
 

@@ -1,6 +1,7 @@
 // abi.cpp -- C ABI entry points of libpagedkv.so that are not the allocator:
 // error reporting, pool descriptors, host-side argument validation and the
 // dispatch of the device calls to their launchers.
+#include <algorithm>
 #include <cstdio>
 #include <cstring>
 #include <new>
@@ -288,6 +289,15 @@ int pf_swap_in(const pf_pool *pool, const void *host_src, const int32_t *ids, in
     return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
 }
 
+// Workspace bytes of a call of `rows` rows per kv-head on either kernel.
+static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_seqs, int n_q_heads, int max_blocks,
+                                   bool causal) {
+    pkv::RowsPlan plan;
+    if (pkv::rows_plan(pool, rows, false, &plan) != PF_OK) return 0;
+    return std::max(plan.bytes, pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks,
+                                                            rows / (n_q_heads / pool->n_kv_heads)));
+}
+
 size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                  int split_tokens) {
     pkv::clear_error();
@@ -303,8 +313,7 @@ size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads,
                                                "at most 16 q-heads per kv-head");
             return 0;
         }
-        pkv::RowsPlan rows;
-        return pkv::rows_plan(pool, group, false, &rows) == PF_OK ? rows.bytes : 0;
+        return rows_workspace_bytes(pool, group, n_seqs, n_q_heads, max_blocks_per_seq, false);
     }
     pkv::AttnPlan plan;
     if (pkv::attention_plan(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens, false, &plan)) return 0;
@@ -328,12 +337,17 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
 // kernel / prompt kernel in microseconds:
 //   4 sequences, 1 row x 64 values, fp16: 100 tokens 10.9 / 5.8, 1024 tokens
 //   14.4 / 12.3, 1536 tokens 14.9 / 15.9; x 128, e4m3: 512 tokens 14.7 / 12.1,
-//   1024 tokens 17.0 / 19.2; 16 rows x 128, fp16: 512 tokens 31.8 / 11.1, 1024
-//   tokens 36.0 / 17.9, 8192 tokens 59.6 / 109;
+//   1024 tokens 17.0 / 19.2; 16 rows x 128, fp16: 512 tokens 31.8 / 11.1, 2048
+//   tokens 47.7 / 30.8 (cut into parts 16.2), 8192 tokens 59.6 / 109 (36.5); 9
+//   rows x 64: 2048 tokens 23.2 / 19.6 (13.7);
 //   38 sequences (two waves), 1 row x 64, e4m3: 128 tokens 10.4 / 12.5; 16 rows
 //   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1.
 // fp32 results stay with the few-rows kernel, which does not round its weights
 // to fp16.
+static int prompt_splits_of(const pkv::RowsArgs &a) {
+    return pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
+                              a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms);
+}
 static bool prompt_kernel_pays(const pkv::RowsArgs &a) {
     if (a.out_dtype != PF_F16) return false;
     const long long items = (long long)a.n_seqs * a.pool->n_kv_heads;
@@ -341,8 +355,10 @@ static bool prompt_kernel_pays(const pkv::RowsArgs &a) {
     const int step = a.pool->head_dim == 64 ? 128 : 64;
     long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
-    const bool wide = a.rows * a.pool->head_dim > 512;   // parts cost the few-rows kernel most
-    return waves <= (wide ? 2 : 1) && waves * (4 + steps) <= (wide ? 20 : 12);
+    if (a.rows * a.pool->head_dim <= 512) return waves == 1 && steps <= 8;
+    // wide rows: the few-rows kernel's parts cost it most
+    if (waves == 1) return steps <= 32 || prompt_splits_of(a) > 1;
+    return waves == 2 && steps <= 6;
 }
 
 // The few-rows kernel with a checked workspace (decode and short appends over
@@ -355,13 +371,15 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad max_blocks_per_seq");
     int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan, fit ? ws_bytes : SIZE_MAX);
     if (rc) return rc;
-    if (ws_bytes < a.plan.bytes)
+    const size_t need = fit ? a.plan.bytes
+                            : rows_workspace_bytes(a.pool, a.rows, a.n_seqs, a.n_q_heads, a.max_blocks, a.causal && a.cu_q);
+    if (ws_bytes < need)
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
-                                                  " bytes, needs " + std::to_string(a.plan.bytes));
+                                                  " bytes, needs " + std::to_string(need));
     if (prompt_kernel_pays(a)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
-                           a.causal && a.cu_q};
+                           a.causal && a.cu_q, workspace, ws_bytes};
         return pkv::launch_prefill_tc(b, static_cast<cudaStream_t>(stream));
     }
     a.workspace = workspace;
@@ -407,12 +425,11 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
             // the append first: a launch of its own, since a page's new scale is needed before any of its rows
             pkv::AppendArgs w{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, nullptr,
                               n_seqs, 1};
-            pkv::RowsPlan plan8;
-            rc = pkv::rows_plan(pool, group, true, &plan8);
-            if (rc) return rc;
-            if (ws_bytes < plan8.bytes)   // nothing is launched by a call that fails
+            const size_t need8 = rows_workspace_bytes(pool, group, n_seqs, n_q_heads, max_blocks_per_seq, false);
+            if (need8 == 0) return PF_ERR_CUDA;   // message set
+            if (ws_bytes < need8)   // nothing is launched by a call that fails
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: workspace has " + std::to_string(ws_bytes) +
-                                                          " bytes, needs " + std::to_string(plan8.bytes));
+                                                          " bytes, needs " + std::to_string(need8));
             if ((long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: bad max_blocks_per_seq");
             rc = pkv::launch_append(w, static_cast<cudaStream_t>(stream));
@@ -469,6 +486,21 @@ int pf_decode_step(const pf_pool *pool, int layer, const void *q, const void *k_
                        n_q_heads, scale, out, out_dtype, split_tokens, workspace, ws_bytes, stream);
 }
 
+// Hands the prompt kernel the workspace that its sizes ask for, if any was given.
+static int prompt_workspace(pkv::PrefillArgs &a, void *workspace, size_t ws_bytes, const char *fn) {
+    const size_t need =
+        workspace ? pkv::prompt_workspace_bytes(a.pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new) : 0;
+    if (need == 0) return PF_OK;
+    if (!aligned16(workspace))
+        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace must be 16-byte aligned");
+    if (ws_bytes < need)
+        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
+                                                  " bytes, needs " + std::to_string(need));
+    a.workspace = workspace;
+    a.ws_bytes = ws_bytes;
+    return PF_OK;
+}
+
 // Rows per kv-head when an append takes the decode kernel (its query tokens
 // x its q-heads), or 0 when they do not fit (the standalone kernel then).
 // Rows per kv-head of an append on the decode kernel (query tokens x
@@ -489,10 +521,10 @@ size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads
         return 0;
     }
     const int rows = append_rows(pool, n_q_heads, max_new_tokens);
-    if (rows == 0) return 0;   // the call takes the kernel that needs no workspace
+    if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
+        return pkv::prompt_workspace_bytes(pool, true, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens);
     if (pool->dtype == PF_E4M3) {
-        pkv::RowsPlan plan8;
-        return pkv::rows_plan(pool, rows, false, &plan8) == PF_OK ? plan8.bytes : 0;
+        return rows_workspace_bytes(pool, rows, n_seqs, n_q_heads, max_blocks_per_seq, true);
     }
     pkv::AttnPlan plan;
     // sized like pf_decode_workspace_bytes: by the resident grid, or by a
@@ -553,6 +585,7 @@ int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, co
     }
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_new_tokens,
                        n_q_heads, scale, out, out_dtype, true};
+    if ((rc = prompt_workspace(a, workspace, ws_bytes, "pf_paged_prefill_attention")) != PF_OK) return rc;
     return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -571,9 +604,9 @@ size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, 
         return 0;
     }
     const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
-    if (rows == 0) return 0;   // the call takes the kernel that needs no workspace
-    pkv::RowsPlan plan;
-    return pkv::rows_plan(pool, rows, false, &plan) == PF_OK ? plan.bytes : 0;
+    if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
+        return pkv::prompt_workspace_bytes(pool, false, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens);
+    return rows_workspace_bytes(pool, rows, n_seqs, n_q_heads, max_blocks_per_seq, false);
 }
 
 int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
@@ -609,6 +642,7 @@ int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, cons
     }
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_q_tokens,
                        n_q_heads, scale, out, out_dtype, false};
+    if ((rc = prompt_workspace(a, workspace, ws_bytes, "pf_paged_cross_attention")) != PF_OK) return rc;
     return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
 }
 

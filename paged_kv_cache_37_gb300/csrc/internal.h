@@ -135,7 +135,13 @@ struct PrefillArgs {
     void *out;
     int out_dtype;
     bool causal;   // the queries are the context's last tokens
+    void *workspace = nullptr;   // for the parts of contexts cut over the SMs, or null: not cut
+    size_t ws_bytes = 0;
 };
+// Parts that the prompt kernel cuts contexts of these sizes into (1: none).
+int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms);
+// Bytes of that workspace, 0 if these sizes are not cut (or causal fp16).
+size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new);
 int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu (causal, fp16 pools)
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);   // prefill_tc.cu
 
@@ -156,6 +162,9 @@ int launch_gather_e4m3(const GatherArgs &a, cudaStream_t stream);
 // Stamp of each launch that leaves records of cut work in a workspace (never
 // 0, so a zeroed workspace holds none of any launch).
 unsigned next_epoch();
+
+// SMs of the current device; without one an error, or a bound for sizing.
+int device_sms(bool need_device, int *sms);
 
 // Attention of at most kMaxRows query rows per (sequence, kv-head):
 // rows_attention.cuh.  Every schedule detail follows from the device and the

@@ -54,9 +54,17 @@
 // the product falls below fp16's smallest normal, then off by at most 2^-25)
 // and store them into the swizzled stage that the MMAs read; rows past the
 // last position are zero-filled.
+//
+// Contexts cut over the SMs (SPLIT: few blocks, long contexts, a workspace): a
+// block (sequence, kv-head, query rows) is one CTA per part of its context.  A
+// part's CTA counts positions and tiles from its first token and leaves O, not
+// yet divided, with each row's maximum and sum of weights in the workspace;
+// merge_parts_kernel joins them.  A block whose context fills one part only
+// writes its output itself.  (prompt_splits has the rule and both sides.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <string>
@@ -90,6 +98,10 @@ struct Regs {
 };
 constexpr int kOrderSeqs = NTHREADS;   // a thread per sequence
 constexpr int kOrderContext = 1024;
+// Long contexts of few blocks are cut into parts of at least kMinTiles tiles,
+// at most kMaxParts of them (a lane each in the merge).
+constexpr int kMinTiles = 4;
+constexpr int kMaxParts = 32;
 constexpr int kRawStages = 3;    // e4m3: raw K/V stages
 constexpr int TMEM_COLS = 512;
 constexpr float kRescaleLog2 = 8.0f;
@@ -146,7 +158,14 @@ struct Params {
     long long layer_page0;   // layer * n_blocks
     int out_f32;
     float scale_log2;
+    // contexts cut: the parts of block (item, qp), part after part
+    int splits;       // parts at most
+    float2 *part_ml;  // [block][part][2 QT]: a row's reference maximum (log2) and sum of weights
+    float *part_o;    // [block][part][2 QT][D]: its sum of weighted values
 };
+
+// Tiles of a part when a block's n tiles are cut into at most `splits`.
+__device__ __forceinline__ int part_tiles(int n, int splits) { return max(kMinTiles, (n + splits - 1) / splits); }
 
 struct Bars {
     unsigned long long k_full[4];
@@ -325,7 +344,7 @@ __device__ __forceinline__ void cp_async4_zfill(uint32_t smem, const void *gmem,
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
 }
 
-template <int D, bool CAUSAL, bool Q8>
+template <int D, bool CAUSAL, bool Q8, bool SPLIT>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const Params p) {
@@ -341,7 +360,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // prompts' 384 blocks on 152 SMs left 40 % of the time idle behind the long
     // ones (batches of up to kOrderSeqs with room for long contexts: each block
     // ranks the lengths itself, which takes it about a microsecond).
-    const int b = (int)blockIdx.x;
+    const int part = SPLIT ? (int)blockIdx.x % p.splits : 0;
+    const int b = SPLIT ? (int)blockIdx.x / p.splits : (int)blockIdx.x;
     int qp = p.n_qp - 1 - b / p.n_items;
     int item = b - (b / p.n_items) * p.n_items;
     if constexpr (!CAUSAL) {
@@ -383,14 +403,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr int IDS = TW / 32;
     auto tile_token = [&](int lt) { return lt / TPI * (2 * TPI) + li * TPI + lt % TPI; };
     int first_id[2] = {0, 0};
-    if (loader) {
+    auto first_look = [&](int from) {
         const int page = p.block_size >= 16 ? p.block_shift : 0;
 #pragma unroll
         for (int k = 0; k < (Q8 ? IDS : 2); ++k) {
-            const int tok = Q8 ? tile_token(lane + 32 * k) : k * BN + lane * p.box_rows;
+            const int tok = from + (Q8 ? tile_token(lane + 32 * k) : k * BN + lane * p.box_rows);
             first_id[k] = bt_row[min(tok >> page, p.max_blocks - 1)];
         }
-    }
+    };
+    if (!SPLIT && loader) first_look(0);
 
     // lengths and new-token counts, clamped (and flagged) to what the table
     // and the call allow
@@ -410,6 +431,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int r0 = qp * 2 * QT;
     if (r0 >= rows) return;                  // the whole CTA: no row here
     const int r_end = min(r0 + 2 * QT, rows);
+    if (SPLIT && L == 0 && part > 0) return;
     if (!CAUSAL && L == 0) {                 // nothing to attend to: zeros
         const size_t o0 = ((size_t)q0 * p.n_q_heads + (size_t)h * p.gh) * D;
         for (int e = threadIdx.x; e < (r_end - r0) * (D / 8); e += NTHREADS) {
@@ -438,8 +460,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             nt[g] = pmax[g] / BN + 1;
         }
     }
-    const int p_max = max(pmax[0], pmax[1]);
-    const int ntt = max(nt[0], nt[1]);
+    int p_max = max(pmax[0], pmax[1]);
+    int ntt = max(nt[0], nt[1]);
+    // This CTA's part of the context: tokens tok0 .. tok0 + p_max; positions
+    // and tiles count from tok0.
+    int tok0 = 0, n_parts = 1;
+    if constexpr (SPLIT) {
+        const int per = part_tiles(ntt, p.splits);
+        n_parts = (ntt + per - 1) / per;
+        if (part >= n_parts) return;
+        tok0 = part * per * BN;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            pmax[g] = min(pmax[g], tok0 + per * BN - 1) - tok0;
+            nt[g] = nt[g] == 0 || pmax[g] < 0 ? 0 : pmax[g] / BN + 1;
+        }
+        p_max = max(pmax[0], pmax[1]);
+        ntt = max(nt[0], nt[1]);
+        if (loader) first_look(tok0);
+    }
 
     const uint32_t s_k = smem_addr(sm + C::OFF_K);
     const uint32_t s_v = smem_addr(sm + C::OFF_V);
@@ -460,7 +499,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int g = (warp / 4) & 1;
     const int t = (int)threadIdx.x % 128;                    // row of the tile = tensor-memory lane
     const bool valid = warp < SOFTMAX_WARPS && r0 + g * QT + t < r_end;
-    const int lim = CAUSAL && valid ? base + token_of(g * QT + t) : pmax[g];   // last position this row sees
+    const int lim = CAUSAL && valid ? base + token_of(g * QT + t) - tok0 : pmax[g];   // last position this row sees
     if (warp < SOFTMAX_WARPS) {
         constexpr int CH = D / 8;
 #pragma unroll
@@ -479,7 +518,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int box = p.box_rows;
     auto n_boxes = [&](int j) { return min(BN / box, (p_max - j * BN) / box + 1); };
     auto raw_id = [&](int j) {
-        return (!Q8 && p.block_size >= 16 && j < ntt && lane < n_boxes(j)) ? bt_row[(j * BN + lane * box) / p.block_size] : 0;
+        return (!Q8 && p.block_size >= 16 && j < ntt && lane < n_boxes(j)) ? bt_row[(tok0 + j * BN + lane * box) / p.block_size] : 0;
     };
     // Loaders (two warps for K, two for V, each issuing every other page
     // box of a tile; a stage is refilled once the MMAs of the tile that used
@@ -508,7 +547,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar(full[st]), (uint32_t)((nb + 1 - li) / 2) * box * D * 2);
             __syncwarp();
             if (mine) {
-                const int row = (int)(p.layer_row0 + (long long)id * B + (j * BN + lane * box) % B);
+                const int row = (int)(p.layer_row0 + (long long)id * B + (tok0 + j * BN + lane * box) % B);
 #pragma unroll
                 for (int hf = 0; hf < C::HALVES; ++hf)
                     tma_load_4d_plain(dst + (uint32_t)(hf * BN + lane * box) * 128u, map, 0, row, hf, h, bar(full[st]));
@@ -519,7 +558,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int tk = lane + 32 * li; tk < BN; tk += 64) {
                 const int tok = j * BN + tk;
                 if (tok > p_max) break;
-                int bid = bt_row[tok];
+                int bid = bt_row[tok0 + tok];
                 if (bid < 0 || bid >= p.n_blocks) {
                     atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
                     bid = 0;
@@ -546,7 +585,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int k = 0; k < IDS; ++k) {
             const int tok = j * BN + tile_token(lane + 32 * k);
-            q_id[k] = tok <= p_max ? bt_row[tok >> p.block_shift] : -2;
+            q_id[k] = tok <= p_max ? bt_row[(tok0 + tok) >> p.block_shift] : -2;
         }
     };
     // this lane's chunk 0 in a raw stage, in the pool and in a swizzled stage;
@@ -566,7 +605,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int id = q_id[k], lt = lane + 32 * k;
                 const bool ok = (unsigned)id < (unsigned)p.n_blocks;
                 if (!ok && id != -2) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
-                row[k] = ok ? (int)p.layer_row0 + (id << p.block_shift) + ((j * BN + tile_token(lt)) & (B - 1)) : -1;
+                row[k] = ok ? (int)p.layer_row0 + (id << p.block_shift) + ((tok0 + j * BN + tile_token(lt)) & (B - 1)) : -1;
                 whole = whole && ok;
                 cp_async4_zfill(dst + BN * D + (li * TW + lt) * 4,
                                 scale_base + (ok ? (size_t)(unsigned)((int)p.layer_page0 + id) * p.n_kv_heads + h : 0),
@@ -786,7 +825,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (ok && nt[g] > 0 && wait_lanes(bar(bars.o_done[g]), (nt[g] - 1) & 1, p.status)) {
             tc_after_sync();
-            const float inv = 1.0f / l;
+            const bool whole = !SPLIT || n_parts == 1;       // else a part: unscaled, fp32
+            const float inv = whole ? 1.0f / l : 1.0f;
+            const size_t part_row = SPLIT ? (((size_t)item * p.n_qp + qp) * p.splits + part) * (2 * QT) : 0;
+            if (!whole) p.part_ml[part_row + g * QT + t] = make_float2(m, l);
             // The warp's 32 rows, 128 bytes of each at a time, through its own
             // rows of the query tile (whose MMAs are done): stored by rows
             // straight from tensor memory, 16 bytes per lane and row, the
@@ -826,7 +868,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                                      : "r"(stage + swz(row, c, QT)));
-                        if (r0 + d < r_end) {
+                        if (SPLIT && !whole) {
+                            if (F32 && r0 + d < r_end)
+                                *reinterpret_cast<uint4 *>(p.part_o + (part_row + d) * D + c0 + c * 4) = w;
+                        } else if (r0 + d < r_end) {
                             const size_t at = row_at(d) + c0;
                             if constexpr (F32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at + c * 4) = w;
                             else *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + at + c * 8) = w;
@@ -835,7 +880,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                 }
             };
-            if (p.out_f32) store(std::true_type());
+            if (p.out_f32 || !whole) store(std::true_type());
             else store(std::false_type());
         }
     } else if (loader) {
@@ -961,6 +1006,70 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
 }
 
+// The rows of cut blocks from their parts: with M the largest reference
+// maximum m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts
+// that the row sees.  A warp per row; lane i holds part i's m and l.
+constexpr int kMergeWarps = 8;
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_parts_kernel(const Params p) {
+    constexpr int BN = Cfg<D, false>::BN;
+    constexpr int V = D / 32;                // values of a lane
+    const int blk = (int)blockIdx.x;
+    const int item = blk / p.n_qp, qp = blk - item * p.n_qp;
+    const int s = item / p.n_kv_heads, h = item - s * p.n_kv_heads;
+    const int lane = (int)threadIdx.x % 32;
+    const int d = (int)blockIdx.y * kMergeWarps + (int)threadIdx.x / 32;   // row of the block
+    griddep_wait();
+    const int L = min(max(p.lens[s], 0), p.max_blocks * p.block_size);
+    const int q0 = CAUSAL || p.cu_q ? p.cu_q[s] : s;
+    int n = CAUSAL || p.cu_q ? max(p.cu_q[s + 1] - q0, 0) : 1;
+    n = min(CAUSAL ? min(n, L) : n, p.max_new);
+    const int rows = n * p.gh, r0 = qp * 2 * QT, r = r0 + d;
+    if (r >= rows || L == 0) return;
+    // the block's tiles and parts, as the main kernel counts them
+    const int base = L - n;
+    const int last = CAUSAL ? base + (min(r0 + 2 * QT, rows) - 1) / p.gh : L - 1;
+    const int ntt = last / BN + 1, per = part_tiles(ntt, p.splits);
+    if (ntt <= per) return;                  // one part: written by the main kernel
+    const int parts = (CAUSAL ? base + r / p.gh : L - 1) / (per * BN) + 1;   // that the row sees
+    const size_t row = ((size_t)blk * p.splits) * (2 * QT) + d;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < parts) ml = p.part_ml[row + (size_t)lane * (2 * QT)];
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    const float w = ex2(ml.x - top);
+    float l = w * ml.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+    float acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    const float *at = p.part_o + row * D + lane * V;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+        const float wi = __shfl_sync(FULL, w, i);
+        float x[V];
+        if constexpr (V == 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(at + (size_t)i * (2 * QT) * D);
+            x[0] = v.x, x[1] = v.y;
+        } else {
+            const float4 v = *reinterpret_cast<const float4 *>(at + (size_t)i * (2 * QT) * D);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(wi, x[k], acc[k]);
+    }
+    const float inv = 1.0f / l;
+    const int i = r / p.gh;
+    const size_t out = ((size_t)(q0 + i) * p.n_q_heads + (size_t)h * p.gh + (r - i * p.gh)) * D + lane * V;
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+        if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + out + k) = make_float2(acc[k] * inv, acc[k + 1] * inv);
+        else *reinterpret_cast<__half2 *>(static_cast<__half *>(p.out) + out + k) = __floats2half2_rn(acc[k] * inv, acc[k + 1] * inv);
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1005,14 +1114,54 @@ namespace {
 
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, Params);
 
-template <int D>
+template <int D, bool SPLIT>
 KernelFn pick(bool causal, bool q8) {
-    if (q8) return causal ? prefill_tc_kernel<D, true, true> : prefill_tc_kernel<D, false, true>;
-    return causal ? prefill_tc_kernel<D, true, false> : prefill_tc_kernel<D, false, false>;
+    if (q8) return causal ? prefill_tc_kernel<D, true, true, SPLIT> : prefill_tc_kernel<D, false, true, SPLIT>;
+    if constexpr (SPLIT) return prefill_tc_kernel<D, false, false, true>;   // (causal fp16 contexts are not cut)
+    else return causal ? prefill_tc_kernel<D, true, false, false> : prefill_tc_kernel<D, false, false, false>;
+}
+
+// Workspace of a block's part.
+size_t part_bytes(int D) { return (size_t)(2 * QT) * (D + 2) * sizeof(float); }
+
+long long blocks_of(const pf_pool *pool, int n_seqs, int n_q_heads, int max_new) {
+    return (long long)n_seqs * pool->n_kv_heads *
+           (((long long)max_new * (n_q_heads / pool->n_kv_heads) + 2 * QT - 1) / (2 * QT));
 }
 
 }  // namespace
 }  // namespace prefill_tc
+
+// Parts that contexts are cut into: as many as give every SM a block, of at
+// least kMinTiles tiles at the table's longest context, if that pays.  In
+// microseconds a tile takes 0.9; the second launch 4, and the parts' way
+// through L2 their bytes at 5 TB/s.  (Measured uncut / cut, 8 kv-heads: fp16 x
+// 64, 32 rows, 4 x 2048 tokens 19.8 / 13.7, 1 x 65,536 tokens 456 / 37; 1 x 1024
+// tokens 12.0 / 13.0; e4m3 x 128, 32 rows, 4 x 8192 tokens 115 / 37; 512 rows, 4
+// x 2048 tokens 36.2 / 29.9, 4 x 1024 tokens 21.6 / 22.7.)
+int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms) {
+    const long long blocks = prefill_tc::blocks_of(pool, n_seqs, n_q_heads, max_new);
+    if ((causal && pool->dtype == PF_F16) || blocks <= 0) return 1;
+    const int BN = pool->head_dim == 64 ? prefill_tc::Cfg<64, false>::BN : prefill_tc::Cfg<128, false>::BN;
+    const long long tiles = ((long long)max_blocks * pool->block_size + BN - 1) / BN;
+    const long long n =
+        std::min(std::min(sms / blocks, tiles / prefill_tc::kMinTiles), (long long)prefill_tc::kMaxParts);
+    if (n < 2) return 1;
+    const long long rows = std::min((long long)max_new * (n_q_heads / pool->n_kv_heads), 2ll * prefill_tc::QT);
+    const double bytes = 2.0 * (double)(blocks * n * rows) * pool->head_dim * sizeof(float);
+    return 0.9 * (double)(tiles - (tiles + n - 1) / n) > 4.0 + bytes / 5e6 ? (int)n : 1;
+}
+
+size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new) {
+    int sms = 0;
+    if (n_seqs <= 0 || max_new <= 0 || n_q_heads <= 0 || n_q_heads % pool->n_kv_heads || max_blocks <= 0 ||
+        device_sms(false, &sms) != PF_OK)
+        return 0;
+    const int splits = prompt_splits(pool, causal, n_seqs, n_q_heads, max_blocks, max_new, sms);
+    return splits == 1 ? 0
+                       : (size_t)prefill_tc::blocks_of(pool, n_seqs, n_q_heads, max_new) * splits *
+                             prefill_tc::part_bytes(pool->head_dim);
+}
 
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     int *status = device_status_ptr();
@@ -1070,22 +1219,56 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
     p.layer_row0 = p.layer_page0 * pool->block_size;
     p.out_f32 = a.out_dtype == PF_F32;
     p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.splits = 1;
+    p.part_ml = nullptr;
+    p.part_o = nullptr;
+    const long long blocks = n_items * n_qp;
+    if (a.workspace) {
+        int sms = 0;
+        const int rc = device_sms(true, &sms);
+        if (rc) return rc;
+        p.splits = prompt_splits(pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new, sms);
+        // (fewer where the workspace is a fixed scratch)
+        const size_t fit = a.ws_bytes / ((size_t)blocks * prefill_tc::part_bytes(D));
+        if (fit < (size_t)p.splits) p.splits = fit < 2 ? 1 : (int)fit;
+        p.part_ml = static_cast<float2 *>(a.workspace);
+        p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * 2 * prefill_tc::QT);
+    }
+    const bool split = p.splits > 1;
     const prefill_tc::KernelFn fn =
-        D == 64 ? prefill_tc::pick<64>(a.causal, q8) : prefill_tc::pick<128>(a.causal, q8);
+        D == 64 ? (split ? prefill_tc::pick<64, true>(a.causal, q8) : prefill_tc::pick<64, false>(a.causal, q8))
+                : (split ? prefill_tc::pick<128, true>(a.causal, q8) : prefill_tc::pick<128, false>(a.causal, q8));
     const int smem = D == 64 ? (q8 ? prefill_tc::Cfg<64, true>::SMEM : prefill_tc::Cfg<64, false>::SMEM)
                              : (q8 ? prefill_tc::Cfg<128, true>::SMEM : prefill_tc::Cfg<128, false>::SMEM);
     // once per device and kernel (setting it twice does no harm)
-    static std::atomic<bool> ready[kMaxDevices][8];
-    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * a.causal + 4 * q8];
+    static std::atomic<bool> ready[kMaxDevices][16];
+    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * a.causal + 4 * q8 + 8 * split];
     if (!done.load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: cudaFuncSetAttribute");
         done.store(true, std::memory_order_release);
     }
-    fn<<<(unsigned)(n_items * n_qp), prefill_tc::NTHREADS, smem, stream>>>(pool->tmap_pf_k[dev], pool->tmap_pf_v[dev],
-                                                                           p);
+    fn<<<(unsigned)(blocks * p.splits), prefill_tc::NTHREADS, smem, stream>>>(pool->tmap_pf_k[dev],
+                                                                              pool->tmap_pf_v[dev], p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: launch");
+    if (split) {
+        cudaLaunchConfig_t cfg = {};
+        const long long most = std::min((long long)a.max_new * gh, 2ll * prefill_tc::QT);   // rows of a block
+        cfg.gridDim = dim3((unsigned)blocks, (unsigned)((most + prefill_tc::kMergeWarps - 1) / prefill_tc::kMergeWarps));
+        cfg.blockDim = dim3(32 * prefill_tc::kMergeWarps);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = D == 64 ? (a.causal ? cudaLaunchKernelEx(&cfg, prefill_tc::merge_parts_kernel<64, true>, p)
+                                : cudaLaunchKernelEx(&cfg, prefill_tc::merge_parts_kernel<64, false>, p))
+                    : (a.causal ? cudaLaunchKernelEx(&cfg, prefill_tc::merge_parts_kernel<128, true>, p)
+                                : cudaLaunchKernelEx(&cfg, prefill_tc::merge_parts_kernel<128, false>, p));
+        if (e != cudaSuccess) return cuda_error(e, "pf_paged_prefill_attention: merge launch");
+    }
     return PF_OK;
 }
 

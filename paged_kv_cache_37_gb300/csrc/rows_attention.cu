@@ -27,7 +27,7 @@ rows::Kernel kernel_for(const pf_pool *pool, int n_rows, bool f32) {
 
 }  // namespace
 
-int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan, size_t most) {
+int device_sms(bool need_device, int *out) {
     static std::atomic<int> known[kMaxDevices];   // SMs per device, 0: not asked yet
     int sms = 0, dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -41,6 +41,14 @@ int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan,
         if (need_device) return cuda_error(e, "attention: SM count");
         sms = kSmsNoDevice;
     }
+    *out = sms;
+    return PF_OK;
+}
+
+int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan, size_t most) {
+    int sms = 0;
+    const int rc = device_sms(need_device, &sms);
+    if (rc) return rc;
     plan->sms = sms;
     const int hg = heads_per_team(pool->n_kv_heads);
     const size_t warps = (size_t)(kernel_for(pool, n_rows, false).warps / hg) * hg;   // of a CTA

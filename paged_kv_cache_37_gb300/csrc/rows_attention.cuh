@@ -1,7 +1,7 @@
 // rows_attention.cuh -- attention of a few query rows per (sequence, kv-head)
 // over the paged cache: decode and short appends over an e4m3 pool, short
 // cross attention over either pool type.  (fp16 results of small batches with
-// short tables come from the prompt kernel, which needs no partition.)
+// short tables, or with many rows, come from the prompt kernel.)
 //
 // For a (sequence s, kv-head h) with L tokens and at most 16 query rows (its
 // query tokens x its gh q-heads, row r = i * gh + g of token i):

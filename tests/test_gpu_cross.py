@@ -33,11 +33,28 @@ def test_cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32):
     _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32, False)
 
 
-@pytest.mark.parametrize("lens,new,hq,h,d,page,ws", CASES[:6])
+MANY = [([3 + 7 * i % 90 for i in range(40)], [1 + i % 3 for i in range(40)], 25, 5, 64, 16, True),
+        ([3 + 7 * i % 90 for i in range(40)], [1 + i % 3 for i in range(40)], 20, 5, 128, 1, True)]
+
+
+@pytest.mark.parametrize("lens,new,hq,h,d,page,ws", CASES[:6] + MANY)
 @pytest.mark.parametrize("cache", ["f16", "e4m3"])
 def test_cross_wide_table(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache):
     """Tables with room for 4096 more tokens: fp16 results from the few-rows kernel as well."""
     _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, False, True)
+
+
+@pytest.mark.parametrize("lens,new,hq,h,d,page", [
+    ([5000, 0, 600, 63], [33, 40, 17, 3], 2, 1, 128, 16),       # a part per context, several, none
+    ([9000], [300], 4, 2, 64, 64),                             # two blocks of rows, the last one short
+    ([1, 1024, 2047], [20, 20, 19], 3, 3, 64, 256),
+    ([700, 1300], [6, 9], 12, 4, 128, 1),
+])
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_cross_cut_contexts(pkv, cuda_dev, lens, new, hq, h, d, page, cache, f32):
+    """Few blocks of many rows over long contexts: cut into parts, which are merged."""
+    _cross(pkv, cuda_dev, lens, new, hq, h, d, page, True, cache, f32, False)
 
 
 def _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32, wide):
@@ -73,7 +90,11 @@ def _cross(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache, f32, wide):
         table = torch.nn.functional.pad(table, (0, 4096 // page), value=1 << 30)
     out = torch.full((int(offs[-1]) + 1, hq, d), 7.0, dtype=torch.float32 if f32 else torch.float16, device=cuda_dev)
     work = pkv.make_cross_workspace(pool, len(lens), hq, table.shape[1], max(new)) if ws else None
-    assert (work is not None) == work_small
+    step_tokens = 128 if d == 64 else 64
+    blocks = len(lens) * h * -(-max(new) * (hq // h) // 256)
+    cut = ws and min(torch.cuda.get_device_properties(cuda_dev).multi_processor_count // blocks,
+                     -(-table.shape[1] * page // step_tokens) // 4) >= 2
+    assert (work is not None) == (work_small or cut)
     pkv.pf_device_status(reset=True)
     for _ in range(2):
         pkv.pf_paged_cross_attention(pool, 1, dev(q, cuda_dev), table, lens_dev, dev(offs, cuda_dev), max(new), scale,
