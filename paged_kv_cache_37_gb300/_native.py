@@ -121,14 +121,17 @@ def _check(rc):
 
 # --------------------------------------------------------------- helpers
 
-def _dev_ptr(t, name, dtype=None):
-    """Address of a contiguous CUDA tensor (an int: what ctypes takes for a
-    pointer argument without a wrapper object)."""
+def _dev_ptr(t, name, dtype=None, dev=None):
+    """Address of a contiguous CUDA tensor, on device dev if given (an int: what
+    ctypes takes for a pointer argument without a wrapper object)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
+    if dev is None or t.get_device() != dev:
+        if not t.is_cuda:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
+        if dev is not None:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} is on {t.device}, the current device is cuda:{dev}")
     if not t.is_contiguous():
         raise PagedKVError(PF_ERR_INVALID, f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -150,14 +153,14 @@ def _stream_ptr(stream):
     return stream.cuda_stream
 
 
-def _on_current_device(pool, tensors):
-    """The pool and these tensors lie on torch's current device (whose current
-    stream the call takes by default)."""
+def _pool_device(pool):
+    """The device that a call's tensors have to lie on: torch's current one
+    (whose current stream the call takes by default), and the pool's."""
     import torch
     dev = torch.cuda.current_device()
-    for t in (pool.k_pool, *tensors):
-        if t is not None and t.get_device() != dev:
-            raise PagedKVError(PF_ERR_INVALID, f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if pool.device != dev:
+        raise PagedKVError(PF_ERR_INVALID, f"the pool is on cuda:{pool.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _host_i32(a, name):
@@ -192,6 +195,7 @@ class Pool:
         self.v_pool = v_pool
         self.k_scale = k_scale
         self.v_scale = v_scale
+        self.device = k_pool.get_device()
         self.n_layers, self.n_blocks, self.block_size, self.n_kv_heads, self.head_dim = k_pool.shape
 
     def __del__(self):
@@ -352,10 +356,9 @@ def pf_copy_blocks(pool, src_ids, dst_ids, stream=None):
     n = src_ids.numel()
     if dst_ids.numel() != n:
         raise PagedKVError(PF_ERR_INVALID, "src_ids and dst_ids must have the same length")
-    if pool.k_scale is not None:
-        _on_current_device(pool, (src_ids, dst_ids))
-    _check(lib().pf_copy_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32),
-                                _dev_ptr(dst_ids, "dst_ids", torch.int32), n, _stream_ptr(stream)))
+    dev = None if pool.k_scale is None else _pool_device(pool)
+    _check(lib().pf_copy_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32, dev),
+                                _dev_ptr(dst_ids, "dst_ids", torch.int32, dev), n, _stream_ptr(stream)))
 
 
 def pf_compact_blocks(pool, src_ids, dst_ids, block_map, block_tables, context_lens, stream=None):
@@ -369,12 +372,12 @@ def pf_compact_blocks(pool, src_ids, dst_ids, block_map, block_tables, context_l
         raise PagedKVError(PF_ERR_INVALID, "block_map must have n_blocks entries")
     if block_tables.dim() != 2 or context_lens.numel() != block_tables.shape[0]:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_rows, max_blocks]; context_lens [n_rows]")
-    _on_current_device(pool, (src_ids, dst_ids, block_map, block_tables, context_lens))
-    _check(lib().pf_compact_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32),
-                                   _dev_ptr(dst_ids, "dst_ids", torch.int32), n,
-                                   _dev_ptr(block_map, "block_map", torch.int32),
-                                   _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[0],
-                                   block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
+    dev = _pool_device(pool)
+    _check(lib().pf_compact_blocks(pool.handle, _dev_ptr(src_ids, "src_ids", torch.int32, dev),
+                                   _dev_ptr(dst_ids, "dst_ids", torch.int32, dev), n,
+                                   _dev_ptr(block_map, "block_map", torch.int32, dev),
+                                   _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[0],
+                                   block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32, dev),
                                    _stream_ptr(stream)))
 
 
@@ -392,7 +395,8 @@ def pf_swap_out(pool, ids, host_dst, stream=None):
     import torch
     n = ids.numel()
     ptr = _pinned_ptr(host_dst, "host_dst", n * pf_block_image_bytes(pool))
-    _check(lib().pf_swap_out(pool.handle, _dev_ptr(ids, "ids", torch.int32), n, ptr, _stream_ptr(stream)))
+    dev = None if pool.k_scale is None else _pool_device(pool)
+    _check(lib().pf_swap_out(pool.handle, _dev_ptr(ids, "ids", torch.int32, dev), n, ptr, _stream_ptr(stream)))
 
 
 def pf_swap_in(pool, host_src, ids, stream=None):
@@ -400,7 +404,8 @@ def pf_swap_in(pool, host_src, ids, stream=None):
     import torch
     n = ids.numel()
     ptr = _pinned_ptr(host_src, "host_src", n * pf_block_image_bytes(pool))
-    _check(lib().pf_swap_in(pool.handle, ptr, _dev_ptr(ids, "ids", torch.int32), n, _stream_ptr(stream)))
+    dev = None if pool.k_scale is None else _pool_device(pool)
+    _check(lib().pf_swap_in(pool.handle, ptr, _dev_ptr(ids, "ids", torch.int32, dev), n, _stream_ptr(stream)))
 
 
 def pf_prefill_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens):
@@ -420,17 +425,17 @@ def pf_paged_prefill_attention(pool, layer, q, block_tables, context_lens, cu_q,
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
     if tuple(out.shape) != tuple(q.shape) or q.shape[-1] != pool.head_dim:
         raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out must have the shape of q")
-    if pool.k_scale is not None:
-        _on_current_device(pool, (q, block_tables, context_lens, cu_q, out, workspace))
+    dev = None if pool.k_scale is None else _pool_device(pool)
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
     _check(lib().pf_paged_prefill_attention(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
-        _dev_ptr(cu_q, "cu_q", torch.int32), n, int(max_new_tokens), q.shape[1], float(scale),
-        _dev_ptr(out, "out"), out_dtype,
-        None if workspace is None else _dev_ptr(workspace, "workspace"),
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev),
+        _dev_ptr(cu_q, "cu_q", torch.int32, dev), n, int(max_new_tokens), q.shape[1], float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype,
+        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
 
 
@@ -453,15 +458,16 @@ def pf_paged_cross_attention(pool, layer, q, block_tables, context_lens, cu_q, m
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
-    _on_current_device(pool, (q, block_tables, context_lens, cu_q, out, workspace))
+    dev = _pool_device(pool)
     if q.numel() == 0:
         return
     _check(lib().pf_paged_cross_attention(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
-        _dev_ptr(cu_q, "cu_q", torch.int32), n, int(max_q_tokens), q.shape[1], float(scale),
-        _dev_ptr(out, "out"), out_dtype,
-        None if workspace is None else _dev_ptr(workspace, "workspace"),
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev),
+        _dev_ptr(cu_q, "cu_q", torch.int32, dev), n, int(max_q_tokens), q.shape[1], float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype,
+        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
 
 
@@ -477,14 +483,14 @@ def pf_append_kv(pool, layer, k_new, v_new, block_tables, context_lens, cu_new, 
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
     if k_new.shape[0] != n if cu_new is None else cu_new.numel() != n + 1:
         raise PagedKVError(PF_ERR_INVALID, "cu_new must have n_seqs + 1 entries, or be None with one row per sequence")
-    _on_current_device(pool, (k_new, v_new, block_tables, context_lens, cu_new))
+    dev = _pool_device(pool)
     if k_new.numel() == 0:
         return
-    _check(lib().pf_append_kv(pool.handle, layer, _dev_ptr(k_new, "k_new", torch.float16),
-                              _dev_ptr(v_new, "v_new", torch.float16),
-                              _dev_ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-                              _dev_ptr(context_lens, "context_lens", torch.int32),
-                              None if cu_new is None else _dev_ptr(cu_new, "cu_new", torch.int32), n,
+    _check(lib().pf_append_kv(pool.handle, layer, _dev_ptr(k_new, "k_new", torch.float16, dev),
+                              _dev_ptr(v_new, "v_new", torch.float16, dev),
+                              _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+                              _dev_ptr(context_lens, "context_lens", torch.int32, dev),
+                              None if cu_new is None else _dev_ptr(cu_new, "cu_new", torch.int32, dev), n,
                               int(max_new_tokens), _stream_ptr(stream)))
 
 
@@ -508,12 +514,12 @@ def pf_gather_kv(pool, layer, block_tables, context_lens, cu_off, k_out, v_out, 
     n = context_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != n or cu_off.numel() < n:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_off needs n_seqs entries")
-    if pool.k_scale is not None:
-        _on_current_device(pool, (block_tables, context_lens, cu_off, k_out, v_out))
-    _check(lib().pf_gather_kv(pool.handle, layer, _dev_ptr(block_tables, "block_tables", torch.int32),
-                              block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
-                              _dev_ptr(cu_off, "cu_off", torch.int64), n,
-                              _dev_ptr(k_out, "k_out", torch.float16), _dev_ptr(v_out, "v_out", torch.float16),
+    dev = None if pool.k_scale is None else _pool_device(pool)
+    _check(lib().pf_gather_kv(pool.handle, layer, _dev_ptr(block_tables, "block_tables", torch.int32, dev),
+                              block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32, dev),
+                              _dev_ptr(cu_off, "cu_off", torch.int64, dev), n,
+                              _dev_ptr(k_out, "k_out", torch.float16, dev),
+                              _dev_ptr(v_out, "v_out", torch.float16, dev),
                               _stream_ptr(stream)))
 
 
@@ -537,8 +543,7 @@ def pf_paged_decode_attention(pool, layer, q, block_tables, context_lens, scale,
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; context_lens [n_seqs]")
     if tuple(out.shape) != (n, hq, d) or d != pool.head_dim:
         raise PagedKVError(PF_ERR_INVALID, "q must be [n_seqs, n_q_heads, head_dim], out must have the shape of q")
-    if pool.k_scale is not None:
-        _on_current_device(pool, (q, block_tables, context_lens, out, workspace))
+    dev = None if pool.k_scale is None else _pool_device(pool)
     if out.dtype == torch.float16:
         out_dtype = PF_F16
     elif out.dtype == torch.float32:
@@ -546,9 +551,10 @@ def pf_paged_decode_attention(pool, layer, q, block_tables, context_lens, scale,
     else:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
     _check(lib().pf_paged_decode_attention(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32), n, hq, float(scale),
-        _dev_ptr(out, "out"), out_dtype, split_tokens, _dev_ptr(workspace, "workspace"),
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev), n, hq, float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype, split_tokens, _dev_ptr(workspace, "workspace", None, dev),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
 
 
@@ -566,16 +572,15 @@ def pf_decode_step(pool, layer, q, k_new, v_new, block_tables, context_lens, sca
         raise PagedKVError(PF_ERR_INVALID, "k_new / v_new must be [n_seqs, n_kv_heads, head_dim]")
     if tuple(out.shape) != (n, hq, d) or d != pool.head_dim:
         raise PagedKVError(PF_ERR_INVALID, "q must be [n_seqs, n_q_heads, head_dim], out must have the shape of q")
-    if pool.k_scale is not None:
-        _on_current_device(pool, (q, k_new, v_new, block_tables, context_lens, out, workspace))
+    dev = None if pool.k_scale is None else _pool_device(pool)
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
     _check(lib().pf_decode_step(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(k_new, "k_new", torch.float16),
-        _dev_ptr(v_new, "v_new", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32), n, hq, float(scale),
-        _dev_ptr(out, "out"), out_dtype, split_tokens, _dev_ptr(workspace, "workspace"),
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev), _dev_ptr(k_new, "k_new", torch.float16, dev),
+        _dev_ptr(v_new, "v_new", torch.float16, dev), _dev_ptr(block_tables, "block_tables", torch.int32, dev),
+        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32, dev), n, hq, float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype, split_tokens, _dev_ptr(workspace, "workspace", None, dev),
         workspace.numel() * workspace.element_size(), int(flags), _stream_ptr(stream)))
 
 
@@ -592,10 +597,12 @@ def pf_paged_decode_attention_noalloc(pool, layer, q, block_tables, context_lens
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
+    dev = None if pool.k_scale is None else _pool_device(pool)
     _check(lib().pf_paged_decode_attention_noalloc(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16), _dev_ptr(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32), n, hq, float(scale),
-        _dev_ptr(out, "out"), out_dtype, split_tokens, _stream_ptr(stream)))
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev), n, hq, float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype, split_tokens, _stream_ptr(stream)))
 
 
 def pf_test_inject_wait_timeout():

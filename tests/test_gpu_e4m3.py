@@ -512,3 +512,27 @@ def test_workspace_shared_with_an_fp16_pool(pkv, cuda_dev):
         pkv.pf_paged_decode_attention(c.pool, 1, qd, c.table_dev, lens, c.scale(), out, 0, ws)
         assert_within(host(out), want, tol)
         assert_close_to_oracle(host(f.attention(0.125, ws=ws)), f.oracle(oracle, 0.125))
+
+
+def test_tensors_elsewhere_are_refused(pkv, cuda_dev):
+    """Tensors of the host, of another type or not contiguous: an error that names the argument, nothing launched."""
+    import torch
+    c = Case(pkv, cuda_dev, [33, 5], 4, 4, 64, 16)
+    c.fill()
+    q = torch.zeros((2, 4, 64), dtype=torch.float16, device=cuda_dev)
+    out, lens = torch.full_like(q, 7.0), dev(c.lens, cuda_dev)
+    ws = pkv.make_workspace(c.pool, 2, 4, c.table.shape[1], 0)
+    good = [q, c.table_dev, lens, c.scale(), out, 0, ws]
+    for i, bad, name in ((0, q.cpu(), "q"), (1, c.table_dev.cpu(), "block_tables"), (2, lens.long(), "context_lens"),
+                         (4, out.cpu(), "out"), (6, ws.cpu(), "workspace"),
+                         (0, q.transpose(0, 1).contiguous().transpose(0, 1), "q")):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(pkv.PagedKVError, match=name):
+            pkv.pf_paged_decode_attention(c.pool, 1, *args)
+    with pytest.raises(pkv.PagedKVError, match="k_new"):
+        pkv.pf_append_kv(c.pool, 1, q.cpu(), q, c.table_dev, lens, None)
+    with pytest.raises(pkv.PagedKVError, match="block_map"):
+        ids = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+        pkv.pf_compact_blocks(c.pool, ids, ids, torch.zeros(c.N, dtype=torch.int32), c.table_dev, lens)
+    assert bool((out == 7.0).all())
