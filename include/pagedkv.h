@@ -439,8 +439,8 @@ PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
  * these sizes, or 0 when that path does not apply (more than 16 rows per
  * kv-head, or 8 on pages of fewer than 16 tokens; the call then needs no
  * workspace) or on bad arguments.  8-bit pools: also what the tcgen05 kernel
- * takes to cut these sizes' contexts over the SMs (a call without a workspace
- * does not cut them; one with fewer bytes is refused). */
+ * takes to cut these sizes' contexts over the SMs (without a workspace the
+ * call does not cut them, with a smaller one into fewer parts). */
 PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
                                          int n_q_heads, int max_blocks_per_seq,
                                          int max_new_tokens);
@@ -469,8 +469,9 @@ PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *
                              void *workspace, size_t ws_bytes, void *stream);
 /* Workspace bytes of pf_paged_cross_attention for these sizes, or 0 when it
  * needs none (more than 16 rows per kv-head and contexts that are not worth
- * cutting) or on bad arguments.  The call takes no less; NULL instead runs on
- * the tcgen05 kernel, uncut. */
+ * cutting) or on bad arguments.  Smaller batches need no more.  Up to 16 rows
+ * take no less; above, contexts are cut into as many parts as fit, and not at
+ * all without a workspace. */
 PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                 int max_q_tokens);
 

@@ -289,12 +289,18 @@ int pf_swap_in(const pf_pool *pool, const void *host_src, const int32_t *ids, in
     return pkv::launch_block_copy(a, static_cast<cudaStream_t>(stream));
 }
 
-// Workspace bytes of a call of `rows` rows per kv-head on either kernel.
-static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_seqs, int n_q_heads, int max_blocks,
-                                   bool causal) {
+// Whether rows are many enough values that the few-rows kernel pays for its
+// parts more than the prompt kernel does.
+static bool wide_rows(const pf_pool *pool, int rows) { return rows * pool->head_dim > 512; }
+
+// Workspace bytes of a call of `rows` rows per kv-head on either kernel.  (The
+// prompt kernel's are asked for as for a single sequence: a workspace serves
+// smaller batches than its own.)
+static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads, int max_blocks, bool causal) {
     pkv::RowsPlan plan;
     if (pkv::rows_plan(pool, rows, false, &plan) != PF_OK) return 0;
-    return std::max(plan.bytes, pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks,
+    if (!wide_rows(pool, rows)) return plan.bytes;
+    return std::max(plan.bytes, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks,
                                                             rows / (n_q_heads / pool->n_kv_heads)));
 }
 
@@ -313,7 +319,7 @@ size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads,
                                                "at most 16 q-heads per kv-head");
             return 0;
         }
-        return rows_workspace_bytes(pool, group, n_seqs, n_q_heads, max_blocks_per_seq, false);
+        return rows_workspace_bytes(pool, group, n_q_heads, max_blocks_per_seq, false);
     }
     pkv::AttnPlan plan;
     if (pkv::attention_plan(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens, false, &plan)) return 0;
@@ -344,21 +350,18 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
 //   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1.
 // fp32 results stay with the few-rows kernel, which does not round its weights
 // to fp16.
-static int prompt_splits_of(const pkv::RowsArgs &a) {
-    return pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
-                              a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms);
-}
-static bool prompt_kernel_pays(const pkv::RowsArgs &a) {
+static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
     if (a.out_dtype != PF_F16) return false;
     const long long items = (long long)a.n_seqs * a.pool->n_kv_heads;
     const long long waves = (items + a.plan.sms - 1) / a.plan.sms;
     const int step = a.pool->head_dim == 64 ? 128 : 64;
     long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
-    if (a.rows * a.pool->head_dim <= 512) return waves == 1 && steps <= 8;
-    // wide rows: the few-rows kernel's parts cost it most
-    if (waves == 1) return steps <= 32 || prompt_splits_of(a) > 1;
-    return waves == 2 && steps <= 6;
+    if (!wide_rows(a.pool, a.rows)) return waves == 1 && steps <= 8;
+    if (waves > 1) return waves == 2 && steps <= 6;
+    const int parts = pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
+                                         a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes);
+    return steps <= 32 || parts > 1;
 }
 
 // The few-rows kernel with a checked workspace (decode and short appends over
@@ -372,11 +375,11 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
     int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan, fit ? ws_bytes : SIZE_MAX);
     if (rc) return rc;
     const size_t need = fit ? a.plan.bytes
-                            : rows_workspace_bytes(a.pool, a.rows, a.n_seqs, a.n_q_heads, a.max_blocks, a.causal && a.cu_q);
+                            : rows_workspace_bytes(a.pool, a.rows, a.n_q_heads, a.max_blocks, a.causal && a.cu_q);
     if (ws_bytes < need)
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
                                                   " bytes, needs " + std::to_string(need));
-    if (prompt_kernel_pays(a)) {
+    if (prompt_kernel_pays(a, ws_bytes)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
                            a.causal && a.cu_q, workspace, ws_bytes};
@@ -425,7 +428,7 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
             // the append first: a launch of its own, since a page's new scale is needed before any of its rows
             pkv::AppendArgs w{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, nullptr,
                               n_seqs, 1};
-            const size_t need8 = rows_workspace_bytes(pool, group, n_seqs, n_q_heads, max_blocks_per_seq, false);
+            const size_t need8 = rows_workspace_bytes(pool, group, n_q_heads, max_blocks_per_seq, false);
             if (need8 == 0) return PF_ERR_CUDA;   // message set
             if (ws_bytes < need8)   // nothing is launched by a call that fails
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: workspace has " + std::to_string(ws_bytes) +
@@ -486,16 +489,11 @@ int pf_decode_step(const pf_pool *pool, int layer, const void *q, const void *k_
                        n_q_heads, scale, out, out_dtype, split_tokens, workspace, ws_bytes, stream);
 }
 
-// Hands the prompt kernel the workspace that its sizes ask for, if any was given.
+// Hands the prompt kernel a workspace to cut contexts with, as many parts as fit.
 static int prompt_workspace(pkv::PrefillArgs &a, void *workspace, size_t ws_bytes, const char *fn) {
-    const size_t need =
-        workspace ? pkv::prompt_workspace_bytes(a.pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new) : 0;
-    if (need == 0) return PF_OK;
+    if (!workspace || (a.causal && a.pool->dtype == PF_F16)) return PF_OK;   // (causal fp16 contexts are not cut)
     if (!aligned16(workspace))
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace must be 16-byte aligned");
-    if (ws_bytes < need)
-        return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
-                                                  " bytes, needs " + std::to_string(need));
     a.workspace = workspace;
     a.ws_bytes = ws_bytes;
     return PF_OK;
@@ -524,7 +522,7 @@ size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads
     if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
         return pkv::prompt_workspace_bytes(pool, true, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens);
     if (pool->dtype == PF_E4M3) {
-        return rows_workspace_bytes(pool, rows, n_seqs, n_q_heads, max_blocks_per_seq, true);
+        return rows_workspace_bytes(pool, rows, n_q_heads, max_blocks_per_seq, true);
     }
     pkv::AttnPlan plan;
     // sized like pf_decode_workspace_bytes: by the resident grid, or by a
@@ -606,7 +604,7 @@ size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, 
     const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
     if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
         return pkv::prompt_workspace_bytes(pool, false, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens);
-    return rows_workspace_bytes(pool, rows, n_seqs, n_q_heads, max_blocks_per_seq, false);
+    return rows_workspace_bytes(pool, rows, n_q_heads, max_blocks_per_seq, false);
 }
 
 int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,

@@ -138,9 +138,12 @@ struct PrefillArgs {
     void *workspace = nullptr;   // for the parts of contexts cut over the SMs, or null: not cut
     size_t ws_bytes = 0;
 };
-// Parts that the prompt kernel cuts contexts of these sizes into (1: none).
-int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms);
-// Bytes of that workspace, 0 if these sizes are not cut (or causal fp16).
+// Parts that the prompt kernel cuts contexts of these sizes into with a
+// workspace of ws_bytes (1: none).
+int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms,
+                  size_t ws_bytes);
+// Bytes of that workspace for these sizes and for smaller batches, 0 if these
+// are not cut (or causal fp16).
 size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new);
 int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu (causal, fp16 pools)
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);   // prefill_tc.cu

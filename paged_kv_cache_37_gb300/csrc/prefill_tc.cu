@@ -1139,13 +1139,15 @@ long long blocks_of(const pf_pool *pool, int n_seqs, int n_q_heads, int max_new)
 // 64, 32 rows, 4 x 2048 tokens 19.8 / 13.7, 1 x 65,536 tokens 456 / 37; 1 x 1024
 // tokens 12.0 / 13.0; e4m3 x 128, 32 rows, 4 x 8192 tokens 115 / 37; 512 rows, 4
 // x 2048 tokens 36.2 / 29.9, 4 x 1024 tokens 21.6 / 22.7.)
-int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms) {
+int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms,
+                  size_t ws_bytes) {
     const long long blocks = prefill_tc::blocks_of(pool, n_seqs, n_q_heads, max_new);
     if ((causal && pool->dtype == PF_F16) || blocks <= 0) return 1;
     const int BN = pool->head_dim == 64 ? prefill_tc::Cfg<64, false>::BN : prefill_tc::Cfg<128, false>::BN;
     const long long tiles = ((long long)max_blocks * pool->block_size + BN - 1) / BN;
-    const long long n =
-        std::min(std::min(sms / blocks, tiles / prefill_tc::kMinTiles), (long long)prefill_tc::kMaxParts);
+    const long long room = (long long)(ws_bytes / prefill_tc::part_bytes(pool->head_dim));   // parts that fit
+    const long long n = std::min(std::min(std::min((long long)sms, room) / blocks, tiles / prefill_tc::kMinTiles),
+                                 (long long)prefill_tc::kMaxParts);
     if (n < 2) return 1;
     const long long rows = std::min((long long)max_new * (n_q_heads / pool->n_kv_heads), 2ll * prefill_tc::QT);
     const double bytes = 2.0 * (double)(blocks * n * rows) * pool->head_dim * sizeof(float);
@@ -1157,10 +1159,10 @@ size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int 
     if (n_seqs <= 0 || max_new <= 0 || n_q_heads <= 0 || n_q_heads % pool->n_kv_heads || max_blocks <= 0 ||
         device_sms(false, &sms) != PF_OK)
         return 0;
-    const int splits = prompt_splits(pool, causal, n_seqs, n_q_heads, max_blocks, max_new, sms);
-    return splits == 1 ? 0
-                       : (size_t)prefill_tc::blocks_of(pool, n_seqs, n_q_heads, max_new) * splits *
-                             prefill_tc::part_bytes(pool->head_dim);
+    // a part per SM, whatever the batch: a smaller one takes no more
+    return prompt_splits(pool, causal, n_seqs, n_q_heads, max_blocks, max_new, sms, SIZE_MAX) == 1
+               ? 0
+               : sms * prefill_tc::part_bytes(pool->head_dim);
 }
 
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
@@ -1227,10 +1229,7 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
         int sms = 0;
         const int rc = device_sms(true, &sms);
         if (rc) return rc;
-        p.splits = prompt_splits(pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new, sms);
-        // (fewer where the workspace is a fixed scratch)
-        const size_t fit = a.ws_bytes / ((size_t)blocks * prefill_tc::part_bytes(D));
-        if (fit < (size_t)p.splits) p.splits = fit < 2 ? 1 : (int)fit;
+        p.splits = prompt_splits(pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new, sms, a.ws_bytes);
         p.part_ml = static_cast<float2 *>(a.workspace);
         p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * 2 * prefill_tc::QT);
     }

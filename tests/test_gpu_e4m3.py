@@ -536,3 +536,62 @@ def test_tensors_elsewhere_are_refused(pkv, cuda_dev):
         ids = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
         pkv.pf_compact_blocks(c.pool, ids, ids, torch.zeros(c.N, dtype=torch.int32), c.table_dev, lens)
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("hq,h,new", [(16, 1, 1), (2, 2, 1), (2, 1, 4), (2, 1, 40)])
+def test_workspace_of_a_larger_batch(pkv, cuda_dev, hq, h, new):
+    """A workspace made for the largest batch serves smaller ones, whose contexts are cut further;
+    with one that is too small a call of many rows cuts less."""
+    import torch
+    c = Case(pkv, cuda_dev, [3000], hq, h, 128, 16)
+    c.fill()
+    offs = np.array([0, new], np.int32)
+    q = c.rng.standard_normal((new, hq, 128)).astype(np.float16)
+    want, tol = c.want(q, offs, True, F16, F16)
+    out = torch.empty((new, hq, 128), dtype=torch.float16, device=cuda_dev)
+    lens, table, qd = dev(c.lens, cuda_dev), c.table_dev, dev(q, cuda_dev)
+    for n in (500, 40, 1):
+        ws = pkv.make_prefill_workspace(c.pool, n, hq, table.shape[1], new)
+        pkv.pf_paged_prefill_attention(c.pool, 1, qd, table, lens, dev(offs, cuda_dev), new, c.scale(), out, ws)
+        assert_within(host(out), want, tol + c.small_terms(q, offs), f"made for {n}")
+        if new == 1:
+            ws = pkv.make_workspace(c.pool, n, hq, table.shape[1], 0)
+            pkv.pf_paged_decode_attention(c.pool, 1, qd, table, lens, c.scale(), out, 0, ws)
+            assert_within(host(out), want, tol + c.small_terms(q, offs), f"decode, made for {n}")
+    if new == 40:
+        for kb in (16, 600):                      # no part fits; four do
+            ws = torch.zeros(kb * 1024, dtype=torch.uint8, device=cuda_dev)
+            pkv.pf_paged_prefill_attention(c.pool, 1, qd, table, lens, dev(offs, cuda_dev), new, c.scale(), out, ws)
+            assert_within(host(out), want, tol + c.small_terms(q, offs), f"{kb} KiB")
+
+
+def test_cut_contexts_captured_and_replayed(pkv, cuda_dev):
+    """Two captured calls of cut contexts that share a workspace, replayed with other lengths and queries."""
+    import torch
+    c = Case(pkv, cuda_dev, [5000, 1500], 4, 2, 64, 16)
+    c.fill()
+    new, offs = [20, 30], np.array([0, 20, 50], np.int32)
+    ws = pkv.make_prefill_workspace(c.pool, 2, 4, c.table.shape[1], 30)
+    qd = torch.zeros((50, 4, 64), dtype=torch.float16, device=cuda_dev)
+    lens, cu = dev(c.lens, cuda_dev), dev(offs, cuda_dev)
+    outs = [torch.empty_like(qd) for _ in range(2)]
+    call = lambda o: pkv.pf_paged_prefill_attention(c.pool, 1, qd, c.table_dev, lens, cu, max(new), c.scale(), o, ws)   # noqa: E731
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call(outs[0])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            call(o)
+    full = c.lens
+    for i, now in enumerate(([5000, 1500], [400, 30], [2049, 1024], [20, 1500])):
+        q = c.rng.standard_normal((50, 4, 64)).astype(np.float16)
+        c.lens = np.array(now, np.int32)
+        qd.copy_(dev(q, cuda_dev))
+        lens.copy_(dev(c.lens, cuda_dev))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        want, tol = c.want(q, offs, True, F16, F16)
+        assert_within(host(outs[i % 2]), want, tol + c.small_terms(q, offs), f"replay {i}")
+    c.lens = full
