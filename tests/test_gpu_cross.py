@@ -49,6 +49,7 @@ def test_cross_wide_table(pkv, cuda_dev, lens, new, hq, h, d, page, ws, cache):
     ([9000], [300], 4, 2, 64, 64),                             # two blocks of rows, the last one short
     ([1, 1024, 2047], [20, 20, 19], 3, 3, 64, 256),
     ([700, 1300], [6, 9], 12, 4, 128, 1),
+    ([4100, 64, 65, 129], [129, 1, 128, 100], 1, 1, 64, 16),   # contexts of one and two tiles beside a cut one
 ])
 @pytest.mark.parametrize("cache", ["f16", "e4m3"])
 @pytest.mark.parametrize("f32", [False, True])

@@ -293,6 +293,7 @@ def test_decode_step_wide_table(pkv, cuda_dev):
     ([6000], [700], 2, 2, 64, 64, True),
     ([1100, 515], [1030, 20], 1, 1, 64, 256, True),
     ([900, 1], [300, 1], 4, 2, 128, 1, True),
+    ([2000, 130, 127, 128], [128, 128, 100, 33], 1, 1, 64, 16, True),
 ])
 @pytest.mark.parametrize("f32", [False, True])
 def test_append_attention(pkv, cuda_dev, lens, new, hq, h, d, page, ws, f32):
