@@ -347,7 +347,9 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
 //   tokens 47.7 / 30.8 (cut into parts 16.2), 8192 tokens 59.6 / 109 (36.5); 9
 //   rows x 64: 2048 tokens 23.2 / 19.6 (13.7);
 //   38 sequences (two waves), 1 row x 64, e4m3: 128 tokens 10.4 / 12.5; 16 rows
-//   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1.
+//   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1; 32
+//   sequences of 512 tokens, e4m3 x 128: 8 rows 22.5 / 23.8, 9 25.9 / 23.9;
+//   38 of 512 tokens, e4m3 x 64: 9 rows 18.2 / 19.0, 16 19.5 / 19.2.
 // fp32 results stay with the few-rows kernel, which does not round its weights
 // to fp16.
 static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
@@ -358,7 +360,7 @@ static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
     long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
     if (!wide_rows(a.pool, a.rows)) return waves == 1 && steps <= 8;
-    if (waves > 1) return waves == 2 && steps <= 6;
+    if (waves > 1) return waves == 2 && steps <= (a.rows * a.pool->head_dim > 1024 ? 8 : 4);
     const int parts = pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
                                          a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes);
     return steps <= 32 || parts > 1;
