@@ -30,10 +30,10 @@
 //   free, so a lane reads 16-byte chunks of K rows as they lie; V is transposed
 //   by ldmatrix.  e4m3 codes are widened to fp16 (exact) in between; V's
 //   transpose is by bytes, and the token order of a tile is chosen so that a
-//   lane's four tokens are two k pairs.  (mma.sync on e4m3 operands is not a
-//   way around the widening: it compiles to the same conversions and two fp16
-//   MMAs; scores from three e4m3 terms of q took 574 warp instructions per 4
-//   KB stage that way.)
+//   lane's four tokens are two k pairs.  (Scores by mma.sync on e4m3 operands,
+//   from three e4m3 terms of q, need no widening of K and were slower: 660
+//   executed warp instructions per 4 KB stage by smsp__inst_executed, 574 with
+//   the widening.)
 // * Softmax in the log2 domain on the S^T fragments, fp32.  The running
 //   maximum is raised only when a lane sees a score 2^8 above it, so its
 //   reduction over the lanes is off the common path; the row sums stay per
