@@ -484,10 +484,11 @@ PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_
  * without workspace / ws_bytes: the scratch is a fixed 8 MiB array inside
  * the library (held by every GPU that loads the library until the process
  * exits).  Nothing is allocated.
- * - A batch whose scratch need (pf_decode_workspace_bytes) exceeds 8 MiB is
- *   rejected with PF_ERR_INVALID; split the batch or pass a workspace to
- *   pf_paged_decode_attention.  (8-bit pools, whose need does not depend on
- *   the batch: the call runs on as many SMs as the scratch serves.)
+ * - A batch that needs more than 8 MiB of scratch (pf_decode_workspace_bytes,
+ *   less the workspace's first 33,280 bytes) is rejected with PF_ERR_INVALID;
+ *   split the batch or pass a workspace to pf_paged_decode_attention.  (8-bit
+ *   pools, whose need does not depend on the batch: the call runs on as many
+ *   SMs as the scratch serves.)
  * - The first call on a device looks up the array's device address (once
  *   per device, with that device current); make that first call before any
  *   stream capture.

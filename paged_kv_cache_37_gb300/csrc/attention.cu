@@ -245,8 +245,8 @@ int attention_plan(const pf_pool *pool, int n_seqs, int n_q_heads, int max_block
         rc = resident_grid(pool, n_q_heads, plan->spans, plan->cuda_cores, &plan->grid);
         if (rc) return rc;
     }
-    // [reserved: 256 B][records][merge jobs]
-    plan->counter_bytes = 256;
+    // [front][records][merge jobs]
+    plan->counter_bytes = kWorkspaceFront;
     const int ng = (pool->n_kv_heads + HG - 1) / HG;
     if (plan->spans) {
         plan->chunk = TB;

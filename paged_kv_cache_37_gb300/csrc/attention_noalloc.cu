@@ -15,9 +15,9 @@
 namespace pkv {
 namespace {
 
-// Scratch of the no-allocation variant: reserved bytes, partial records and
-// merge jobs of one call (the same layout as a caller's workspace).
-constexpr size_t kNoAllocScratchBytes = 8u << 20;   // 8 MiB per device
+// Scratch of the no-allocation variant: the same layout as a caller's
+// workspace, with 8 MiB for the partial records and merge jobs of one call.
+constexpr size_t kNoAllocScratchBytes = kWorkspaceFront + (8u << 20);
 static __device__ __align__(256) uint8_t g_noalloc_scratch[kNoAllocScratchBytes];
 
 // In host code g_noalloc_scratch names a host-side stand-in, not device

@@ -30,6 +30,16 @@ constexpr int kTileTokens = 16;
 // the tcgen05 kernel, fewer the warp-level MMA kernel.
 constexpr int kTcMinRows = 128;
 
+// Front of every attention workspace: kFlagOffset reserved bytes, then the
+// flags of the few-rows kernel (two per warp of up to kFlagSms CTAs of
+// kFlagWarps warps).  Records of every kernel lie behind it, so that whatever
+// calls share a workspace -- other kernels, shapes or pool types -- a flag word
+// only ever holds a stamp or zero.
+constexpr int kFlagSms = 256;
+constexpr int kFlagWarps = 16;
+constexpr size_t kFlagOffset = 512;
+constexpr size_t kWorkspaceFront = kFlagOffset + (size_t)kFlagSms * kFlagWarps * 2 * sizeof(unsigned);
+
 }  // namespace pkv
 
 // Non-owning description of caller-owned K and V pools.
@@ -176,11 +186,10 @@ constexpr int kMaxRows = 16;
 struct RowsPlan {
     int sms;
     int grid;
-    size_t flag_bytes;
     size_t bytes;   // of the workspace
 };
-// With as many CTAs as the device has SMs, or fewer whose workspace fits into
-// `most` bytes.
+// With as many CTAs as the device has SMs (at most kFlagSms), or fewer whose
+// workspace fits into `most` bytes.
 int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan, size_t most = SIZE_MAX);
 // pf_paged_decode_attention over an 8-bit pool on as many SMs as a scratch of
 // `bytes` serves (abi.cpp).
@@ -214,7 +223,7 @@ struct AttnPlan {
     bool cuda_cores;       // CUDA-core consumers (split_tokens != 0): fp32 scores and weights
     int chunk;             // chunk schedule: tokens per chunk
     int grid;              // persistent grid (0 when planned without a device)
-    size_t counter_bytes;  // reserved bytes at the front of the workspace (256 B)
+    size_t counter_bytes;  // the workspace's front (kWorkspaceFront)
     size_t partial_bytes;  // partial records (spans: epoch-tagged 64-bit words; chunks: fp32), then merge jobs
     size_t n_jobs;         // chunk schedule: merge job slots (0: no merge kernel)
 };

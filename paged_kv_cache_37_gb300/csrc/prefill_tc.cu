@@ -1145,7 +1145,7 @@ int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, i
     if ((causal && pool->dtype == PF_F16) || blocks <= 0) return 1;
     const int BN = pool->head_dim == 64 ? prefill_tc::Cfg<64, false>::BN : prefill_tc::Cfg<128, false>::BN;
     const long long tiles = ((long long)max_blocks * pool->block_size + BN - 1) / BN;
-    const long long room = (long long)(ws_bytes / prefill_tc::part_bytes(pool->head_dim));   // parts that fit
+    const long long room = ws_bytes < kWorkspaceFront ? 0 : (long long)((ws_bytes - kWorkspaceFront) / prefill_tc::part_bytes(pool->head_dim));   // parts that fit
     const long long n = std::min(std::min(std::min((long long)sms, room) / blocks, tiles / prefill_tc::kMinTiles),
                                  (long long)prefill_tc::kMaxParts);
     if (n < 2) return 1;
@@ -1162,7 +1162,7 @@ size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int 
     // a part per SM, whatever the batch: a smaller one takes no more
     return prompt_splits(pool, causal, n_seqs, n_q_heads, max_blocks, max_new, sms, SIZE_MAX) == 1
                ? 0
-               : sms * prefill_tc::part_bytes(pool->head_dim);
+               : kWorkspaceFront + sms * prefill_tc::part_bytes(pool->head_dim);
 }
 
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
@@ -1230,7 +1230,7 @@ int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
         const int rc = device_sms(true, &sms);
         if (rc) return rc;
         p.splits = prompt_splits(pool, a.causal, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new, sms, a.ws_bytes);
-        p.part_ml = static_cast<float2 *>(a.workspace);
+        p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceFront);
         p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * 2 * prefill_tc::QT);
     }
     const bool split = p.splits > 1;

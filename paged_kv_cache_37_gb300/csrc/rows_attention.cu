@@ -1,5 +1,6 @@
 // rows_attention.cu -- host side of rows_attention.cuh: the partition's grid,
 // the workspace and the launches.
+#include <algorithm>
 #include <atomic>
 
 #include "rows_attention.cuh"
@@ -9,7 +10,6 @@ namespace {
 
 // SMs assumed when no device can be queried (sizes a workspace only).
 constexpr int kSmsNoDevice = 256;
-constexpr size_t kReserved = 256;   // front of every workspace, unused
 
 // Warps per team: as many as 4 of the kv-heads, spread evenly over the groups
 // (5 heads: 3 + 2, so that one warp in six idles instead of three in eight).
@@ -53,12 +53,10 @@ int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan,
     const int hg = heads_per_team(pool->n_kv_heads);
     const size_t warps = (size_t)(kernel_for(pool, n_rows, false).warps / hg) * hg;   // of a CTA
     const size_t recs = warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
-    // (the flags of all SMs, rounded up, come first)
-    plan->flag_bytes = (sms * warps * 2 * sizeof(unsigned) + 255) / 256 * 256;
-    const size_t front = kReserved + plan->flag_bytes;
-    plan->grid = most < front + sms * recs ? (int)(most < front ? 0 : (most - front) / recs) : sms;
+    const size_t room = (most < kWorkspaceFront ? 0 : most - kWorkspaceFront) / recs;
+    plan->grid = (int)std::min(room, (size_t)std::min(sms, kFlagSms));
     if (plan->grid == 0) return set_error(PF_ERR_INVALID, "attention: the scratch holds no block's records");
-    plan->bytes = front + plan->grid * recs;
+    plan->bytes = kWorkspaceFront + plan->grid * recs;
     return PF_OK;
 }
 
@@ -87,8 +85,8 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
     p.status = status;
-    p.flags = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(a.workspace) + kReserved);
-    p.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kReserved + a.plan.flag_bytes);
+    p.flags = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(a.workspace) + kFlagOffset);
+    p.recs = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceFront);
     p.max_blocks = a.max_blocks;
     p.n_blocks = pool->n_blocks;
     p.block_size = pool->block_size;
@@ -120,7 +118,7 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
         p.lens = a.context_lens + s0;
         p.cu_q = a.cu_q ? a.cu_q + s0 : nullptr;
         p.n_seqs = a.n_seqs - s0 < step ? a.n_seqs - s0 : step;
-        p.stamp = next_epoch() | 0x80000000u;
+        p.stamp = next_epoch();
         p.after_append = a.after_append && s0 == 0;
         // a programmatic dependent of the kernel before it: its blocks take
         // their SMs as that kernel's leave them, and then wait for its end

@@ -113,7 +113,7 @@ struct Params {
     int *status;
     unsigned *flags;            // [team][2][head]: the stamp once that part's record is written
     float *recs;                // [team][2][head][rows][D + 4]: parts of cut pairs (acc, m, l)
-    unsigned stamp;             // this launch's; the top bit set, so no other content of a workspace has it
+    unsigned stamp;             // this launch's (the flags' part of a workspace holds stamps and zeros only)
     int n_seqs;
     int max_blocks;
     int n_blocks;
@@ -148,6 +148,7 @@ struct Shape {
     static constexpr int NST = RB == 256 ? 2 : 3;
     static constexpr int THREADS = 32 * NW;
     static constexpr int SMEM = NW * NST * (2 * KV + SC);
+    static_assert(NW <= kFlagWarps, "the workspace's flags");
 };
 
 // Work units in order (sequence, group, stage): a pair has kPairCost units

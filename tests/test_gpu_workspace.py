@@ -1,0 +1,61 @@
+"""One workspace under calls of every kind: the kernels share its layout, a
+front of 33,280 bytes (reserved bytes, then from byte 512 the few-rows
+kernel's flags) and records behind it."""
+import numpy as np
+import pytest
+
+from e4m3_util import assert_within, attention64
+from gpu_util import PagedCase, dev, host
+from test_gpu_e4m3 import F16, Case, wide_table
+
+pytestmark = pytest.mark.gpu
+
+FLAGS = slice(512, 33280)
+
+
+def test_flags_hold_nothing_but_flags(pkv, cuda_dev):
+    """A flag is a word equal to its launch's stamp, so no call may leave anything else there: calls of
+    both pool types, of 1, 3, 12 and 40 rows, fp16 and fp32 results, balanced and in fixed chunks, in
+    turn on one workspace.  Each gives its result and leaves every flag word zero."""
+    import torch
+    c = Case(pkv, cuda_dev, [3000, 700], 4, 4, 64, 16)
+    c.fill()
+    f = PagedCase(pkv, cuda_dev, [3000, 700], 4, 4, 64, 16)
+    table, lens = dev(wide_table(c), cuda_dev), dev(c.lens, cuda_dev)
+    sizes = [f.pkv.pf_decode_workspace_bytes(f.pool, 2, 4, f.bt.shape[1], split) for split in (0, 64)]
+    sizes += [pkv.pf_prefill_workspace_bytes(c.pool, 2, 4, table.shape[1], n) for n in (1, 3, 12, 40)]
+    sizes += [pkv.pf_cross_workspace_bytes(f.pool, 2, 4, f.bt.shape[1], n) for n in (1, 12, 40)]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device=cuda_dev)
+    pkv.pf_decode_workspace_init(ws)
+    kv = [[x[0][f.bt[s][np.arange(L) // 16], np.arange(L) % 16] for x in (f.k_host, f.v_host)]
+          for s, L in enumerate(f.lens)]
+
+    def e4m3(n, dtype):
+        offs = np.array([0, n, 2 * n], np.int32)
+        q = c.rng.standard_normal((2 * n, 4, 64)).astype(np.float16)
+        out = torch.empty((2 * n, 4, 64), dtype=dtype, device=cuda_dev)
+        pkv.pf_paged_prefill_attention(c.pool, 1, dev(q, cuda_dev), table, lens, dev(offs, cuda_dev), n, c.scale(), out, ws)
+        want, tol = c.want(q, offs, True, F16, F16)
+        assert_within(host(out), want, tol + c.small_terms(q, offs), f"e4m3 {n}")
+
+    def cross(n, dtype):
+        offs = np.array([0, n, 2 * n], np.int32)
+        q = c.rng.standard_normal((2 * n, 4, 64)).astype(np.float16)
+        out = torch.empty((2 * n, 4, 64), dtype=dtype, device=cuda_dev)
+        pkv.pf_paged_cross_attention(f.pool, 0, dev(q, cuda_dev), f.bt_dev, f.lens_dev, dev(offs, cuda_dev), n, 0.125, out, ws)
+        got = [attention64(q[offs[s]:offs[s + 1]], *kv[s], 0.125, False, F16, F16) for s in range(2)]
+        assert_within(host(out), np.concatenate([o for o, _ in got]), np.concatenate([t for _, t in got]), f"cross {n}")
+
+    def decode(split, dtype):
+        got = [attention64(f.q[s:s + 1], *kv[s], 0.125, False, F16, F16) for s in range(2)]
+        # (the fp16 pools' kernel sums the rounded weights: as far off again at most)
+        assert_within(host(f.attention(0.125, split=split, out_dtype=dtype, ws=ws)), np.concatenate([o for o, _ in got]),
+                      2 * np.concatenate([t for _, t in got]), f"decode {split}")
+
+    calls = [lambda t, n=n: e4m3(n, t) for n in (1, 3, 12, 40)] + [lambda t, n=n: cross(n, t) for n in (1, 12, 40)]
+    calls += [lambda t, s=s: decode(s, t) for s in (0, 64)]
+    for dtype in (torch.float16, torch.float32):
+        for i in np.random.default_rng(3).permutation(np.repeat(np.arange(len(calls)), 2)):
+            calls[i](dtype)
+            assert not host(ws[FLAGS]).any(), f"call {i}"
+    assert pkv.pf_device_status(reset=True) == 0
