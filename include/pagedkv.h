@@ -341,11 +341,11 @@ PF_API int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stre
  * cores.
  * workspace: device memory of at least pf_decode_workspace_bytes(...) bytes,
  * initialised once with pf_decode_workspace_init; calls sharing a workspace
- * must not overlap on the GPU.
+ * (of any kind, over either pool type, captured in graphs and replayed as
+ * often as wanted) must not overlap on the GPU.
  * 8-bit pools: split_tokens 0 only (any page size, up to 16 q-heads per
  * kv-head); K and V are code * scale, the products run on tensor cores as
- * above (codes are exact in fp16), and a workspace of this call may be used by
- * captured graphs as often as they are replayed. */
+ * above (codes are exact in fp16). */
 PF_API int pf_paged_decode_attention(const pf_pool *pool, int layer, const void *q,
                               const int32_t *block_tables,
                               int max_blocks_per_seq,

@@ -165,6 +165,9 @@ int kernel_for(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_cores, 
     return PF_OK;
 }
 
+// A captured launch is counted by its CTAs (attn::kLaunchStep).
+constexpr int kMaxGrid = (int)attn::kLaunchStep;
+
 // Persistent grid of the kernel on the current device: SMs x resident CTAs.
 int resident_grid(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_cores, int *grid) {
     KernelInfo ki;
@@ -193,15 +196,14 @@ int resident_grid(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_core
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return cuda_error(e, "attention: SM count");
         if (occ < 1) return set_error(PF_ERR_UNSUPPORTED, "attention: kernel does not fit on an SM");
-        sh.grid = sms * occ;
+        sh.grid = sms * occ < kMaxGrid ? sms * occ : kMaxGrid;
         sh.ready = true;
     }
     *grid = sh.grid;
     return PF_OK;
 }
 
-// Merge-job stamp of each main-kernel launch (never 0, so a zeroed
-// workspace holds no job of any launch).
+// Stamps of the attention launches, counted.
 std::atomic<unsigned> g_epoch{0};
 
 // Grid bound used to size span records when no device can be queried.
@@ -237,7 +239,7 @@ int attention_plan(const pf_pool *pool, int n_seqs, int n_q_heads, int max_block
     int rc = kernel_for(pool, n_q_heads, plan->spans, plan->cuda_cores, &ki, &HG, &mma);
     if (rc) return rc;
     // a record: the rows of the kernel instance x (D + 2) words (acc, m, l);
-    // fp32 for fixed chunks, 64-bit (value, epoch) for spans
+    // fp32 for fixed chunks, 64-bit (value, stamp) for spans
     const size_t rec_words = (size_t)ki.rows * (size_t)(pool->head_dim + 2);
     const int per_launch = n_seqs < attn::kMaxSeqsPerLaunch ? n_seqs : attn::kMaxSeqsPerLaunch;
     plan->grid = 0;
@@ -306,6 +308,11 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
     p.partials = reinterpret_cast<float *>(ws + plan.counter_bytes);
     p.span_recs = reinterpret_cast<unsigned long long *>(ws + plan.counter_bytes);
     p.jobs = reinterpret_cast<attn::Job *>(ws + plan.counter_bytes + rec_bytes);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(stream, &capture);
+    if (e != cudaSuccess) return cuda_error(e, "pf_paged_decode_attention: cudaStreamIsCapturing");
+    p.state = capture == cudaStreamCaptureStatusNone ? nullptr
+                                                     : reinterpret_cast<unsigned long long *>(ws + kStateOffset);
     p.status = status;
     p.max_blocks = a.max_blocks;
     p.n_q_heads = a.n_q_heads;
@@ -334,8 +341,8 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
     const size_t row = (size_t)a.n_q_heads * pool->head_dim;   // q / out elements per sequence
 
     // Sequences are independent: batches larger than one launch's share of
-    // shared memory run as consecutive launches on the stream; each launch
-    // stamps its merge jobs with a fresh epoch.
+    // shared memory run as consecutive launches on the stream, each with a
+    // stamp of its own.
     for (int s0 = 0; s0 < a.n_seqs; s0 += attn::kMaxSeqsPerLaunch) {
         const int n = a.n_seqs - s0 < attn::kMaxSeqsPerLaunch ? a.n_seqs - s0 : attn::kMaxSeqsPerLaunch;
         // decode: q and out rows are the sequences; append: cu_q holds
@@ -350,7 +357,7 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
         p.bt = a.block_tables + (size_t)s0 * a.max_blocks;
         p.lens = a.context_lens + s0;
         p.n_seqs = n;
-        p.epoch = next_epoch();
+        p.stamp = attn::host_stamp(next_epoch());
         if (a.overlap_previous) {
             // A programmatic dependent of the previous kernel on the stream:
             // resident while that kernel drains; the kernel waits for it

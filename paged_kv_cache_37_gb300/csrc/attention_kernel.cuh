@@ -45,16 +45,18 @@
 // * End of item: token groups merge by shuffles (and the WPH warps of a head
 //   through shared memory).  A whole pair writes `out`.  A part of a cut pair
 //   writes its record (acc[D], m, l per q-head).
-//   - Span schedule: every word of the record carries the launch's epoch
+//   - Span schedule: every word of the record carries the launch's stamp
 //     (one indivisible 64-bit store per value, no fence).  The pair's last
 //     span merges it: when its CTA has no items left, the head's warp loads
 //     the pair's records, polls until every word carries this launch's
-//     epoch (the other parts belong to earlier spans, whose CTAs never wait
+//     stamp (the other parts belong to earlier spans, whose CTAs never wait
 //     for anyone), combines them with the log-sum-exp rule and writes
 //     `out`.  Nothing needs resetting between calls.
-//   - Chunk schedule: chunk 0 of the pair also writes a merge job stamped
-//     with the call's epoch; merge_kernel, launched next on the stream as a
-//     programmatic dependent of this grid, merges every job of this epoch.
+//   - Chunk schedule: chunk 0 of the pair also writes a merge job with the
+//     launch's stamp; merge_kernel, launched next on the stream as a
+//     programmatic dependent of this grid, merges every job of this stamp.
+//   The stamp of a captured launch comes from a count in the workspace, not
+//   from the host, so that every replay has another one (launch_stamp).
 //   Only a merging warp waits for other CTAs, and only for parts that need
 //   nothing from it.
 // * Every wait is bounded (1 s) and parks the thread in hardware while it
@@ -99,7 +101,7 @@ struct ItemDesc {
 // the first span can use slot 1).
 struct Job {
     int s, h0, kind, first, z_first, n_parts;
-    unsigned epoch;
+    unsigned stamp;
     int pad;
 };
 
@@ -135,9 +137,10 @@ struct Params {
     float *partials;         // chunk schedule: fp32 records of the chunks of cut pairs
     struct Job *jobs;        // chunk schedule: merge jobs for merge_kernel
     // span schedule: records of the parts of cut pairs, 64-bit words
-    // (value, epoch) per float (see st_tagged)
+    // (value, stamp) per float (see st_tagged)
     unsigned long long *span_recs;
-    unsigned epoch;   // this launch's stamp for merge jobs and span records (never 0)
+    unsigned stamp;              // this launch's (launch_stamp)
+    unsigned long long *state;   // or the workspace's count of captured launches
     int *status;
     int n_seqs;
     int max_blocks;
@@ -247,6 +250,8 @@ struct __align__(128) Smem {
     uint64_t qfull[NQ];
     uint64_t qempty[NQ];
     uint64_t cbar;   // consumer-warps barrier (count NCW), used when WPH > 1
+    uint64_t stamped;   // stamp is there (captured launches)
+    unsigned stamp;
     PendPart pend[NCW][2];   // span schedule: this warp's cut parts (record slot 0 / 1)
     int warp_tot[NTHREADS / 32];
     // span schedule: pre[s] = units (per group: tiles + kPairCost, 0 for an
@@ -719,11 +724,11 @@ __device__ __forceinline__ void store_whole(const Params &p, const ItemDesc &d, 
 // Rows row0 .. row0 + R - 1 of the record of one part of a cut pair for head
 // hl (state as in store_whole, m and l the same in every lane).  Chunk
 // schedule: fp32 words, and the first part also writes the pair's job.  Span
-// schedule: words tagged with the launch's epoch, record ((span * 2 + slot)
+// schedule: words tagged with the launch's stamp, record ((span * 2 + slot)
 // * HG + hl).
 template <int D, int G, int HG, int R>
 __device__ __forceinline__ void write_part(const Params &p, const Smem<D, G, HG> &sm, const ItemDesc &d, int hl,
-                                           int lane, int row0, bool write_job, const float (&m)[R],
+                                           int lane, int row0, bool write_job, unsigned stamp, const float (&m)[R],
                                            const float (&l)[R], const float (&acc)[R][8]) {
     constexpr int LPT = D / 8;
     constexpr int REC = G * (D + 2);
@@ -737,10 +742,10 @@ __device__ __forceinline__ void write_part(const Params &p, const Smem<D, G, HG>
                 if (g >= G) continue;
                 unsigned long long *w = part + g * (D + 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) st_tagged(w + lane * 8 + i, acc[r][i], p.epoch);
+                for (int i = 0; i < 8; ++i) st_tagged(w + lane * 8 + i, acc[r][i], stamp);
                 if (lane == 0) {
-                    st_tagged(w + D, m[r], p.epoch);
-                    st_tagged(w + D + 1, l[r], p.epoch);
+                    st_tagged(w + D, m[r], stamp);
+                    st_tagged(w + D + 1, l[r], stamp);
                 }
             }
         }
@@ -772,7 +777,7 @@ __device__ __forceinline__ void write_part(const Params &p, const Smem<D, G, HG>
         jb.first = d.a;          // chunk 0 of the sequence
         jb.z_first = 0;
         jb.n_parts = d.c;
-        jb.epoch = p.epoch;
+        jb.stamp = stamp;
         p.jobs[(size_t)d.a * p.n_groups + d.h0 / HG] = jb;
     }
 }
@@ -853,13 +858,43 @@ __device__ __forceinline__ void merge_pair(const Params &p, int first, int n, in
     }
 }
 
+// The stamp of a launch marks what it leaves in the workspace.  A plain launch
+// brings its own (p.stamp, the host's count).  A captured one is the same every
+// time that it is replayed, so its stamp comes from a count in the workspace
+// (p.state, zero at first) to which it adds kLaunchStep in all: one from each CTA
+// and the rest from the first.  A CTA's first consumer warp reads the word at its
+// start and adds to it at its end, so until every CTA has read it, state /
+// kLaunchStep is what the launch found; the next launch over the workspace
+// starts after this one's end.  (Added to by every warp, or at the start, the
+// back-to-back steps of 32.3 us took 32.8; so, 32.5.)
+// The bits of a stamp are those of an fp32 NaN, an infinity or a number below
+// -2^65, 0xe... for the host's and 0xf... for the workspace's.  Neither a
+// record's finite values nor a job's integers are, so what other kinds of calls
+// left in a workspace is not taken for stamped.  It comes round after 2^28
+// launches.
+constexpr unsigned long long kLaunchStep = 1 << 16;
+__host__ __device__ constexpr unsigned host_stamp(unsigned count) { return 0xe0000000u | (count & 0x0fffffffu); }
+__device__ __forceinline__ unsigned state_stamp(unsigned long long launches) {
+    return 0xf0000000u | (unsigned)(launches & 0x0fffffffu);
+}
+
+template <typename S>
+__device__ __forceinline__ unsigned launch_stamp(const Params &p, S &sm) {
+    if (p.state == nullptr) return p.stamp;
+    mbar_wait(smem_addr(&sm.stamped), 0, p.status);
+    return sm.stamp;
+}
+
 // Consumer start: wait for the previous kernel on the stream (as in the
-// producer: it may still be writing `out`), then give empty (or invalid,
-// clamped to empty) sequences a zero output (decode: row s; append: its
-// query rows, when it has any).
-template <int D>
-__device__ __forceinline__ void zero_empty_outputs(const Params &p, int cw, int lane) {
+// producer: it may still be writing `out`), take the launch's stamp, and give
+// empty (or invalid, clamped to empty) sequences a zero output (decode: row s;
+// append: its query rows, when it has any).
+template <int D, typename S>
+__device__ __forceinline__ void consumer_start(const Params &p, S &sm, int cw, int lane) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool stamper = p.state != nullptr && cw == 0 && lane == 0;
+    unsigned long long state = 0;
+    if (stamper) state = ld_tagged(p.state);
     const int Hq = p.n_q_heads;
     for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
         if (p.lens[s] <= 0) {
@@ -872,6 +907,10 @@ __device__ __forceinline__ void zero_empty_outputs(const Params &p, int cw, int 
             }
         }
     }
+    if (stamper) {
+        sm.stamp = state_stamp(state / kLaunchStep + 1);
+        mbar_arrive(smem_addr(&sm.stamped));
+    }
 }
 
 // Span schedule: merge the n parts of a cut pair for kv-head h (head hl of
@@ -881,12 +920,12 @@ __device__ __forceinline__ void zero_empty_outputs(const Params &p, int cw, int 
 // lane loads one part's (m, l) and, in the same round trip, every part's acc
 // values of its own dims (D / 32 of them), PB parts at a time; a batch is
 // loaded again (after a short sleep) until every word carries this launch's
-// epoch.  The parts are written by CTAs of earlier spans (and this warp),
+// stamp.  The parts are written by CTAs of earlier spans (and this warp),
 // which wait for no one, so the words arrive; the wait is bounded all the
 // same and gives up with PF_DEV_WAIT_TIMEOUT.
 template <int D, int G, int HG>
-__device__ __forceinline__ bool merge_span_pair(const Params &p, int first, int z_first, int n, int qrow0, int nq,
-                                                int h, int hl, int lane) {
+__device__ __forceinline__ bool merge_span_pair(const Params &p, unsigned stamp, int first, int z_first, int n,
+                                                int qrow0, int nq, int h, int hl, int lane) {
     constexpr int REC = G * (D + 2);
     constexpr int DPL = D / 32;   // dims per lane
     constexpr int PB = 8;         // parts whose acc loads are in flight together
@@ -914,7 +953,7 @@ __device__ __forceinline__ bool merge_span_pair(const Params &p, int first, int 
                     if (j0 == 0 && i < n) {
                         const unsigned long long *pc = rec_of(i) + g * (D + 2);
                         const unsigned long long wm = ld_tagged(pc + D), wl = ld_tagged(pc + D + 1);
-                        have = tagged_epoch(wm) == p.epoch && tagged_epoch(wl) == p.epoch;
+                        have = tag_of(wm) == stamp && tag_of(wl) == stamp;
                         mi = tagged_value(wm);
                         li = tagged_value(wl);
                     }
@@ -925,7 +964,7 @@ __device__ __forceinline__ bool merge_span_pair(const Params &p, int first, int 
 #pragma unroll
                             for (int q = 0; q < DPL; ++q) {
                                 const unsigned long long w = ld_tagged(pc + lane + 32 * q);
-                                have = have && tagged_epoch(w) == p.epoch;
+                                have = have && tag_of(w) == stamp;
                                 v[jj][q] = tagged_value(w);
                             }
                         }
@@ -981,11 +1020,12 @@ __device__ __forceinline__ bool merge_span_pair(const Params &p, int first, int 
 // cut pair whose last part is its span's first segment (record slot 0, bit 0
 // of `pending`).  A part in slot 1 (a pair that starts inside the span and
 // runs past its end) is merged by a later span.
-template <int D, int G, int HG>
-__device__ __forceinline__ void merge_if_last(const Params &p, const PendPart &pp, int pending, int hl, int lane) {
+template <int D, int G, int HG, typename S>
+__device__ __forceinline__ void merge_if_last(const Params &p, S &sm, const PendPart &pp, int pending, int hl,
+                                              int lane) {
     if (!(pending & 1) || pp.first + pp.n_parts - 1 != (int)blockIdx.x) return;
     __syncwarp();
-    merge_span_pair<D, G, HG>(p, pp.first, pp.z_first, pp.n_parts, pp.qrow0, pp.nq, pp.h0 + hl, hl, lane);
+    merge_span_pair<D, G, HG>(p, launch_stamp(p, sm), pp.first, pp.z_first, pp.n_parts, pp.qrow0, pp.nq, pp.h0 + hl, hl, lane);
 }
 
 // Span schedule: note a finished cut part (lane 0; written to the warp's
@@ -1027,7 +1067,7 @@ __device__ __forceinline__ void consumers(const Params &p, Smem<D, G, HG> &sm, i
     const int row0 = RSPLIT ? part * R : 0;
     const int tok_base = RSPLIT ? 0 : part * TPT;
 
-    zero_empty_outputs<D>(p, cw, lane);
+    consumer_start<D>(p, sm, cw, lane);
 
     uint32_t st = 0;
     uint32_t cphase = 0;
@@ -1038,7 +1078,7 @@ __device__ __forceinline__ void consumers(const Params &p, Smem<D, G, HG> &sm, i
         if (!warp_wait(smem_addr(&sm.qfull[slot]), (k / NQ) & 1, p.status, lane)) return;
         const ItemDesc d = sm.desc[slot];
         if (d.s < 0) {
-            if (part == 0) merge_if_last<D, G, HG>(p, sm.pend[cw][0], pending, hl, lane);
+            if (part == 0) merge_if_last<D, G, HG>(p, sm, sm.pend[cw][0], pending, hl, lane);
             return;
         }
         const int h = d.h0 + hl;
@@ -1247,11 +1287,12 @@ __device__ __forceinline__ void consumers(const Params &p, Smem<D, G, HG> &sm, i
         } else if (leader) {
             if (d.kind == kChunk) {
                 // chunk 0 of the sequence also writes the merge job
-                write_part<D, G, HG, R>(p, sm, d, hl, lane, row0, d.b == 0 && hl == 0 && part == 0, m, l, acc);
+                write_part<D, G, HG, R>(p, sm, d, hl, lane, row0, d.b == 0 && hl == 0 && part == 0, launch_stamp(p, sm), m, l,
+                                            acc);
             } else {
                 // Span part: write the record and note the pair; the CTA
                 // of its last span merges it.
-                write_part<D, G, HG, R>(p, sm, d, hl, lane, row0, false, m, l, acc);
+                write_part<D, G, HG, R>(p, sm, d, hl, lane, row0, false, launch_stamp(p, sm), m, l, acc);
                 if (lane == 0) sm.pend[cw][d.c] = pending_part(p, sm.pre, d);
                 pending |= 1 << d.c;
             }
@@ -1304,7 +1345,7 @@ __device__ __forceinline__ void consumers_mma(const Params &p, Smem<D, G, HG, tr
     const int Hq = p.n_q_heads;
     constexpr bool hilo = HILO;   // fp32 output: weights as fp16 hi + lo parts
 
-    zero_empty_outputs<D>(p, cw, lane);
+    consumer_start<D>(p, sm, cw, lane);
 
     uint32_t st = 0;
     uint32_t cphase = 0;
@@ -1315,7 +1356,7 @@ __device__ __forceinline__ void consumers_mma(const Params &p, Smem<D, G, HG, tr
         if (!warp_wait(smem_addr(&sm.qfull[slot]), (k / NQ) & 1, p.status, lane)) return;
         const ItemDesc d = sm.desc[slot];
         if (d.s < 0) {
-            merge_if_last<D, G, HG>(p, sm.pend[cw][0], pending, hl, lane);
+            merge_if_last<D, G, HG>(p, sm, sm.pend[cw][0], pending, hl, lane);
             return;
         }
         const int h = d.h0 + hl;
@@ -1566,8 +1607,9 @@ __device__ __forceinline__ void consumers_mma(const Params &p, Smem<D, G, HG, tr
             }
         } else {
             // Span part: write the record ((span * 2 + slot) * HG + head),
-            // every word tagged with the launch's epoch, and note the pair;
+            // every word tagged with the launch's stamp, and note the pair;
             // the CTA of its last span merges it.
+            const unsigned stamp = launch_stamp(p, sm);
             unsigned long long *part_rec =
                 p.span_recs + (((size_t)d.span * 2 + d.c) * HG + hl) * (size_t)(G * (D + 2));
 #pragma unroll
@@ -1577,12 +1619,12 @@ __device__ __forceinline__ void consumers_mma(const Params &p, Smem<D, G, HG, tr
                 unsigned long long *rw = part_rec + g * (D + 2);
 #pragma unroll
                 for (int b = 0; b < NNB; ++b) {
-                    st_tagged(rw + b * 8 + 2 * tq, o[b][2 * r], p.epoch);
-                    st_tagged(rw + b * 8 + 2 * tq + 1, o[b][2 * r + 1], p.epoch);
+                    st_tagged(rw + b * 8 + 2 * tq, o[b][2 * r], stamp);
+                    st_tagged(rw + b * 8 + 2 * tq + 1, o[b][2 * r + 1], stamp);
                 }
                 if (tq == 0) {
-                    st_tagged(rw + D, m[r], p.epoch);
-                    st_tagged(rw + D + 1, l[r], p.epoch);
+                    st_tagged(rw + D, m[r], stamp);
+                    st_tagged(rw + D + 1, l[r], stamp);
                 }
             }
             if (lane == 0) sm.pend[cw][d.c] = pending_part(p, sm.pre, d);
@@ -1628,6 +1670,7 @@ __device__ __forceinline__ void decode_attention(const CUtensorMap &tmk, const C
             mbar_init(smem_addr(&sm.qempty[i]), NCW);
         }
         mbar_init(smem_addr(&sm.cbar), NCW);
+        mbar_init(smem_addr(&sm.stamped), 1);
         mbar_init_fence();
     }
     if (p.spans) {
@@ -1683,6 +1726,8 @@ __device__ __forceinline__ void decode_attention(const CUtensorMap &tmk, const C
     if (warp == 0) producer<D, G, HG, MMA>(&tmk, &tmv, p, sm, lane);
     else if constexpr (MMA) consumers_mma<D, G, HG, HILO>(p, sm, warp - 1, lane);
     else consumers<D, G, HG>(p, sm, warp - 1, lane);
+    if (p.state != nullptr && warp == 1 && lane == 0)
+        atomicAdd(p.state, blockIdx.x == 0 ? kLaunchStep - (unsigned long long)(gridDim.x - 1) : 1ull);
 }
 
 // Resident CTAs per SM are set by shared memory (3 at head_dim 64 with the
@@ -1729,20 +1774,21 @@ __global__ void __maxnreg__(128) paged_decode_kernel_mma_r128(const __grid_const
     decode_attention<D, G, HG, true, HILO>(tmk, tmv, p);
 }
 
-// Chunk schedule: merge the records of every job of this launch's epoch, one
+// Chunk schedule: merge the records of every job of this launch's stamp, one
 // warp per (job slot, head).  A head costs about two dependent memory round
 // trips (the job, then its records).
 template <int D, int G, int HG>
 __global__ void __launch_bounds__(128, 1) merge_kernel(const Params p, int n_jobs) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the main grid has finished
     const int lane = threadIdx.x % 32;
+    const unsigned stamp = p.state ? state_stamp(ld_tagged(p.state) / kLaunchStep) : p.stamp;   // (the main grid has counted itself)
     const long long n_warps = (long long)gridDim.x * blockDim.x / 32;
     for (long long wi = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; wi < (long long)n_jobs * HG;
          wi += n_warps) {
         const int j = (int)(wi / HG);
         const int hl = (int)(wi - (long long)j * HG);
         const Job jb = p.jobs[j];
-        if (jb.epoch != p.epoch || jb.h0 + hl >= p.n_kv_heads) continue;
+        if (jb.stamp != stamp || jb.h0 + hl >= p.n_kv_heads) continue;
         int qrow0 = jb.s, nq = 1;
         if (p.cu_q != nullptr) {
             qrow0 = p.cu_q[jb.s];

@@ -66,7 +66,7 @@ extern "C" int pf_paged_decode_attention_noalloc(const pf_pool *pool, int layer,
     int rc = pkv::scratch_for_current_device(&ws);
     if (rc) return rc;
     // The scratch is zero when the library loads.  Every word a call reads
-    // back (merge jobs, span records) carries the epoch of the launch that
+    // back (merge jobs, span records) carries the stamp of the launch that
     // wrote it, so nothing left by an earlier call -- one that timed out
     // included -- is taken for this call's data, and nothing needs resetting.
     // (8-bit pools: what a call writes to read back, it clears.)

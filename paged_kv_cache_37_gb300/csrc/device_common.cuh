@@ -122,12 +122,12 @@ __device__ __forceinline__ unsigned atomic_inc_relaxed_gpu(unsigned *p, unsigned
 __device__ __forceinline__ void fence_acq_rel_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 // One 64-bit word of a record shared between CTAs: the value's bits in the
-// low half and the writing launch's epoch in the high half, stored and loaded
+// low half and the writing launch's stamp in the high half, stored and loaded
 // as single 64-bit relaxed GPU-scope accesses (each indivisible), so a reader
-// that finds the current epoch in a word holds that launch's value, with no
+// that finds the current stamp in a word holds that launch's value, with no
 // fence on either side.
-__device__ __forceinline__ void st_tagged(unsigned long long *p, float v, unsigned epoch) {
-    const unsigned long long w = (unsigned long long)__float_as_uint(v) | ((unsigned long long)epoch << 32);
+__device__ __forceinline__ void st_tagged(unsigned long long *p, float v, unsigned stamp) {
+    const unsigned long long w = (unsigned long long)__float_as_uint(v) | ((unsigned long long)stamp << 32);
     asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
 }
 
@@ -138,7 +138,7 @@ __device__ __forceinline__ unsigned long long ld_tagged(const unsigned long long
 }
 
 __device__ __forceinline__ float tagged_value(unsigned long long w) { return __uint_as_float((unsigned)w); }
-__device__ __forceinline__ unsigned tagged_epoch(unsigned long long w) { return (unsigned)(w >> 32); }
+__device__ __forceinline__ unsigned tag_of(unsigned long long w) { return (unsigned)(w >> 32); }
 
 __device__ __forceinline__ void st_relaxed(unsigned *p, unsigned v) {
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");

@@ -30,13 +30,15 @@ constexpr int kTileTokens = 16;
 // the tcgen05 kernel, fewer the warp-level MMA kernel.
 constexpr int kTcMinRows = 128;
 
-// Front of every attention workspace: kFlagOffset reserved bytes, then the
-// flags of the few-rows kernel (two per warp of up to kFlagSms CTAs of
-// kFlagWarps warps).  Records of every kernel lie behind it, so that whatever
-// calls share a workspace -- other kernels, shapes or pool types -- a flag word
-// only ever holds a stamp or zero.
+// Front of every attention workspace: reserved bytes; from kStateOffset on the
+// count of the decode kernel's captured launches over it (64 bits); from
+// kFlagOffset on the flags of the few-rows kernel (two per warp of up to
+// kFlagSms CTAs of kFlagWarps warps).  Records of every kernel lie behind it,
+// so that whatever calls share a workspace -- other kernels, shapes or pool
+// types -- the count stays one and a flag word holds a stamp or zero.
 constexpr int kFlagSms = 256;
 constexpr int kFlagWarps = 16;
+constexpr size_t kStateOffset = 256;
 constexpr size_t kFlagOffset = 512;
 constexpr size_t kWorkspaceFront = kFlagOffset + (size_t)kFlagSms * kFlagWarps * 2 * sizeof(unsigned);
 
@@ -172,8 +174,8 @@ struct GatherArgs {
 int launch_gather_kv(const GatherArgs &a, cudaStream_t stream);
 int launch_gather_e4m3(const GatherArgs &a, cudaStream_t stream);
 
-// Stamp of each launch that leaves records of cut work in a workspace (never
-// 0, so a zeroed workspace holds none of any launch).
+// Stamp of each launch of the few-rows kernel, which clears the flags that it
+// sets (never 0: clear).
 unsigned next_epoch();
 
 // SMs of the current device; without one an error, or a bound for sizing.
@@ -224,7 +226,7 @@ struct AttnPlan {
     int chunk;             // chunk schedule: tokens per chunk
     int grid;              // persistent grid (0 when planned without a device)
     size_t counter_bytes;  // the workspace's front (kWorkspaceFront)
-    size_t partial_bytes;  // partial records (spans: epoch-tagged 64-bit words; chunks: fp32), then merge jobs
+    size_t partial_bytes;  // partial records (spans: 64-bit words tagged with the launch's stamp; chunks: fp32), then merge jobs
     size_t n_jobs;         // chunk schedule: merge job slots (0: no merge kernel)
 };
 int attention_plan(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks, int split_tokens,
