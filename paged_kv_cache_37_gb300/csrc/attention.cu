@@ -311,8 +311,6 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     e = cudaStreamIsCapturing(stream, &capture);
     if (e != cudaSuccess) return cuda_error(e, "pf_paged_decode_attention: cudaStreamIsCapturing");
-    p.state = capture == cudaStreamCaptureStatusNone ? nullptr
-                                                     : reinterpret_cast<unsigned long long *>(ws + kStateOffset);
     p.status = status;
     p.max_blocks = a.max_blocks;
     p.n_q_heads = a.n_q_heads;
@@ -357,7 +355,7 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
         p.bt = a.block_tables + (size_t)s0 * a.max_blocks;
         p.lens = a.context_lens + s0;
         p.n_seqs = n;
-        p.stamp = attn::host_stamp(next_epoch());
+        p.stamp = capture == cudaStreamCaptureStatusNone ? attn::host_stamp(next_epoch()) : 0;
         if (a.overlap_previous) {
             // A programmatic dependent of the previous kernel on the stream:
             // resident while that kernel drains; the kernel waits for it

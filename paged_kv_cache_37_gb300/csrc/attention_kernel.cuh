@@ -65,6 +65,7 @@
 #pragma once
 
 #include "device_common.cuh"
+#include "internal.h"
 
 namespace pkv {
 namespace attn {
@@ -139,8 +140,7 @@ struct Params {
     // span schedule: records of the parts of cut pairs, 64-bit words
     // (value, stamp) per float (see st_tagged)
     unsigned long long *span_recs;
-    unsigned stamp;              // this launch's (launch_stamp)
-    unsigned long long *state;   // or the workspace's count of captured launches
+    unsigned stamp;   // this launch's, 0 when it is captured (launch_stamp)
     int *status;
     int n_seqs;
     int max_blocks;
@@ -859,14 +859,16 @@ __device__ __forceinline__ void merge_pair(const Params &p, int first, int n, in
 }
 
 // The stamp of a launch marks what it leaves in the workspace.  A plain launch
-// brings its own (p.stamp, the host's count).  A captured one is the same every
-// time that it is replayed, so its stamp comes from a count in the workspace
-// (p.state, zero at first) to which it adds kLaunchStep in all: one from each CTA
-// and the rest from the first.  A CTA's first consumer warp reads the word at its
-// start and adds to it at its end, so until every CTA has read it, state /
-// kLaunchStep is what the launch found; the next launch over the workspace
-// starts after this one's end.  (Added to by every warp, or at the start, the
-// back-to-back steps of 32.3 us took 32.8; so, 32.5.)
+// brings its own (p.stamp, the host's count).  A captured one (p.stamp = 0) is the
+// same every time that it is replayed, so its stamp comes from a count in the
+// front of the workspace, zero at first, to which it adds kLaunchStep in all: one
+// from each CTA and the rest from the first.  A CTA's first consumer warp reads
+// the count at its start and the producer adds at its end, so until every CTA has
+// read it, count / kLaunchStep is what the launch found; the next launch over the
+// workspace starts after this one's end.  (Replayed back to back, 128 mixed
+// sequences: 30.95 us a step with the host's stamps, 31.07 so, 31.2 when consumer
+// warps add, 31.5 when each of them also reads; 32 short ones 8.55, 8.76, 8.81,
+// 8.9.)
 // The bits of a stamp are those of an fp32 NaN, an infinity or a number below
 // -2^65, 0xe... for the host's and 0xf... for the workspace's.  Neither a
 // record's finite values nor a job's integers are, so what other kinds of calls
@@ -874,13 +876,17 @@ __device__ __forceinline__ void merge_pair(const Params &p, int first, int n, in
 // launches.
 constexpr unsigned long long kLaunchStep = 1 << 16;
 __host__ __device__ constexpr unsigned host_stamp(unsigned count) { return 0xe0000000u | (count & 0x0fffffffu); }
-__device__ __forceinline__ unsigned state_stamp(unsigned long long launches) {
+__device__ __forceinline__ unsigned count_stamp(unsigned long long launches) {
     return 0xf0000000u | (unsigned)(launches & 0x0fffffffu);
+}
+
+__device__ __forceinline__ unsigned long long *launch_count(const Params &p) {
+    return p.span_recs - (kWorkspaceFront - kStateOffset) / sizeof(unsigned long long);
 }
 
 template <typename S>
 __device__ __forceinline__ unsigned launch_stamp(const Params &p, S &sm) {
-    if (p.state == nullptr) return p.stamp;
+    if (p.stamp != 0) return p.stamp;
     mbar_wait(smem_addr(&sm.stamped), 0, p.status);
     return sm.stamp;
 }
@@ -892,9 +898,9 @@ __device__ __forceinline__ unsigned launch_stamp(const Params &p, S &sm) {
 template <int D, typename S>
 __device__ __forceinline__ void consumer_start(const Params &p, S &sm, int cw, int lane) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const bool stamper = p.state != nullptr && cw == 0 && lane == 0;
-    unsigned long long state = 0;
-    if (stamper) state = ld_tagged(p.state);
+    const bool stamper = p.stamp == 0 && cw == 0 && lane == 0;
+    unsigned long long count = 0;
+    if (stamper) count = ld_tagged(launch_count(p));
     const int Hq = p.n_q_heads;
     for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
         if (p.lens[s] <= 0) {
@@ -908,7 +914,7 @@ __device__ __forceinline__ void consumer_start(const Params &p, S &sm, int cw, i
         }
     }
     if (stamper) {
-        sm.stamp = state_stamp(state / kLaunchStep + 1);
+        sm.stamp = count_stamp(count / kLaunchStep + 1);
         mbar_arrive(smem_addr(&sm.stamped));
     }
 }
@@ -1723,11 +1729,15 @@ __device__ __forceinline__ void decode_attention(const CUtensorMap &tmk, const C
         if (threadIdx.x == 0) sm.pre[0] = 0;
     }
     __syncthreads();
-    if (warp == 0) producer<D, G, HG, MMA>(&tmk, &tmv, p, sm, lane);
+    if (warp == 0) {
+        producer<D, G, HG, MMA>(&tmk, &tmv, p, sm, lane);
+        if (p.stamp == 0 && lane == 0) {   // (launch_stamp)
+            mbar_wait(smem_addr(&sm.stamped), 0, p.status);
+            atomicAdd(launch_count(p), blockIdx.x == 0 ? kLaunchStep - (unsigned long long)(gridDim.x - 1) : 1ull);
+        }
+    }
     else if constexpr (MMA) consumers_mma<D, G, HG, HILO>(p, sm, warp - 1, lane);
     else consumers<D, G, HG>(p, sm, warp - 1, lane);
-    if (p.state != nullptr && warp == 1 && lane == 0)
-        atomicAdd(p.state, blockIdx.x == 0 ? kLaunchStep - (unsigned long long)(gridDim.x - 1) : 1ull);
 }
 
 // Resident CTAs per SM are set by shared memory (3 at head_dim 64 with the
@@ -1781,7 +1791,7 @@ template <int D, int G, int HG>
 __global__ void __launch_bounds__(128, 1) merge_kernel(const Params p, int n_jobs) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the main grid has finished
     const int lane = threadIdx.x % 32;
-    const unsigned stamp = p.state ? state_stamp(ld_tagged(p.state) / kLaunchStep) : p.stamp;   // (the main grid has counted itself)
+    const unsigned stamp = p.stamp ? p.stamp : count_stamp(ld_tagged(launch_count(p)) / kLaunchStep);   // (the main grid has counted itself)
     const long long n_warps = (long long)gridDim.x * blockDim.x / 32;
     for (long long wi = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 32; wi < (long long)n_jobs * HG;
          wi += n_warps) {
