@@ -23,6 +23,8 @@
 // registers between the maximum and the rounding, so they are read once; the
 // group is a warp for 16-token pages (4 or 8 16-byte loads in flight per
 // lane), 8 or 16 lanes for 1-token pages, 4 or 8 warps above.
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "internal.h"
 
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     }
     const int start = L - n;
     const int page = start / B + j;
-    bool live = n > 0 && j < p.max_pages && page * B < L;
+    bool live = n > 0 && j < p.max_pages && page < (L + B - 1) / B;
     int blk = 0;
     if (live) {
         blk = p.bt[(size_t)s * p.max_blocks + page];
@@ -315,7 +317,9 @@ int launch_append(const AppendArgs &a, cudaStream_t stream) {
     p.max_new = a.max_new;
     p.n_blocks = pool->n_blocks;
     p.n_kv_heads = pool->n_kv_heads;
-    p.max_pages = (int)(((long long)a.max_new - 1 + B - 1) / B + 1);
+    // (max_new is a bound that may be loose: no more new tokens than the table holds)
+    const long long most_new = std::min((long long)a.max_new, (long long)a.max_blocks * B);
+    p.max_pages = (int)((most_new - 1 + B - 1) / B + 1);
     p.layer_page0 = (long long)a.layer * pool->n_blocks;
     switch (B) {
         case 1: return launch_append_b<1>(a, p, stream);
