@@ -454,7 +454,8 @@ PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
  *   out[row][hq][d] = sum_{t < L} softmax_t(scale * q . K[slot(s, t)][h]) V[..][h][d]
  * with h = hq / (n_q_heads / Hkv), fp32 accumulation; L = 0 gives zeros.
  * Arguments as pf_paged_prefill_attention; max_q_tokens bounds every query
- * count (more are flagged with PF_DEV_BAD_LENGTH and left out).  Block tables
+ * count (more are flagged with PF_DEV_BAD_LENGTH and left out), and times the
+ * q-heads per kv-head it must not pass 2^31 - 513.  Block tables
  * of several rows may name the same pages (several hypotheses of one input).
  * Either pool type.  With a workspace (pf_cross_workspace_bytes, initialised
  * once with pf_decode_workspace_init, not shared by overlapping calls) and at

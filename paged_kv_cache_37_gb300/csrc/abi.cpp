@@ -2,6 +2,7 @@
 // error reporting, pool descriptors, host-side argument validation and the
 // dispatch of the device calls to their launchers.
 #include <algorithm>
+#include <climits>
 #include <cstdio>
 #include <cstring>
 #include <new>
@@ -491,6 +492,13 @@ int pf_decode_step(const pf_pool *pool, int layer, const void *q, const void *k_
                        n_q_heads, scale, out, out_dtype, split_tokens, workspace, ws_bytes, stream);
 }
 
+// Query rows of a (sequence, kv-head) that a call allows, counted in 32 bits by
+// the kernels: refused above (a whole block of rows more has to fit).
+static int check_query_rows(const pf_pool *pool, int max_tokens, int n_q_heads, const char *fn) {
+    if ((long long)max_tokens * (n_q_heads / pool->n_kv_heads) <= INT_MAX - 512) return PF_OK;
+    return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": too many query tokens x q-heads per kv-head");
+}
+
 // Hands the prompt kernel a workspace to cut contexts with, as many parts as fit.
 static int prompt_workspace(pkv::PrefillArgs &a, void *workspace, size_t ws_bytes, const char *fn) {
     if (!workspace || (a.causal && a.pool->dtype == PF_F16)) return PF_OK;   // (causal fp16 contexts are not cut)
@@ -583,6 +591,12 @@ int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, co
                         workspace, ws_bytes};
         return pkv::launch_attention(a, static_cast<cudaStream_t>(stream));
     }
+    // a loose bound: there are no more new tokens than the table holds
+    if (check_query_rows(pool, max_new_tokens, n_q_heads, "pf_paged_prefill_attention") != PF_OK) {
+        max_new_tokens = std::min(max_new_tokens, max_blocks_per_seq * pool->block_size);
+        if ((rc = check_query_rows(pool, max_new_tokens, n_q_heads, "pf_paged_prefill_attention")) != PF_OK) return rc;
+        pkv::clear_error();
+    }
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_new_tokens,
                        n_q_heads, scale, out, out_dtype, true};
     if ((rc = prompt_workspace(a, workspace, ws_bytes, "pf_paged_prefill_attention")) != PF_OK) return rc;
@@ -634,6 +648,7 @@ int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, cons
         return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: bad max_blocks_per_seq");
     if (!(scale > 0.0f))
         return pkv::set_error(PF_ERR_INVALID, "pf_paged_cross_attention: scale must be a positive number");
+    if ((rc = check_query_rows(pool, max_q_tokens, n_q_heads, "pf_paged_cross_attention")) != PF_OK) return rc;
     const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
     if (workspace != nullptr && rows > 0) {
         pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
