@@ -440,7 +440,9 @@ PF_API int pf_paged_prefill_attention(const pf_pool *pool, int layer,
  * kv-head, or 8 on pages of fewer than 16 tokens; the call then needs no
  * workspace) or on bad arguments.  8-bit pools: also what the tcgen05 kernel
  * takes to cut these sizes' contexts over the SMs (without a workspace the
- * call does not cut them, with a smaller one into fewer parts). */
+ * call does not cut them, with a smaller one into fewer parts).  A workspace
+ * serves calls of fewer sequences and of fewer tokens than it was made for (and
+ * where it is none, they run without one). */
 PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
                                          int n_q_heads, int max_blocks_per_seq,
                                          int max_new_tokens);
@@ -470,9 +472,9 @@ PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *
                              void *workspace, size_t ws_bytes, void *stream);
 /* Workspace bytes of pf_paged_cross_attention for these sizes, or 0 when it
  * needs none (more than 16 rows per kv-head and contexts that are not worth
- * cutting) or on bad arguments.  Smaller batches need no more.  Up to 16 rows
- * take no less; above, contexts are cut into as many parts as fit, and not at
- * all without a workspace. */
+ * cutting) or on bad arguments.  Calls of fewer sequences or query tokens need
+ * no more.  Above 16 rows contexts are cut into as many parts as fit, and not
+ * at all without a workspace. */
 PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                 int max_q_tokens);
 

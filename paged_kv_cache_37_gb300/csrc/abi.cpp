@@ -294,15 +294,29 @@ int pf_swap_in(const pf_pool *pool, const void *host_src, const int32_t *ids, in
 // parts more than the prompt kernel does.
 static bool wide_rows(const pf_pool *pool, int rows) { return rows * pool->head_dim > 512; }
 
-// Workspace bytes of a call of `rows` rows per kv-head on either kernel.  (The
-// prompt kernel's are asked for as for a single sequence: a workspace serves
-// smaller batches than its own.)
+// Workspace bytes for calls of up to `rows` rows per kv-head on either kernel.
+// (Fewer rows may take more: up to 8 run with 16 warps a CTA, more with 12.  The
+// prompt kernel's bytes, with which it cuts as far as it likes, are those of a
+// single sequence: a workspace serves smaller batches than its own.)
 static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads, int max_blocks, bool causal) {
-    pkv::RowsPlan plan;
-    if (pkv::rows_plan(pool, rows, false, &plan) != PF_OK) return 0;
-    if (!wide_rows(pool, rows)) return plan.bytes;
-    return std::max(plan.bytes, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks,
-                                                            rows / (n_q_heads / pool->n_kv_heads)));
+    const int group = n_q_heads / pool->n_kv_heads;
+    size_t most = 0;
+    for (int r = group; r <= rows; r += group) {
+        pkv::RowsPlan plan;
+        if (pkv::rows_plan(pool, r, false, &plan) != PF_OK) return 0;
+        most = std::max(most, plan.bytes);
+        if (wide_rows(pool, r))
+            most = std::max(most, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks, r / group));
+    }
+    return most;
+}
+
+// The same for calls on the prompt kernel alone: 0, or enough for calls of
+// fewer rows too.
+static size_t prompt_or_rows_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads,
+                                             int max_blocks, int max_tokens) {
+    const size_t bytes = pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks, max_tokens);
+    return bytes == 0 ? 0 : std::max(bytes, rows_workspace_bytes(pool, pkv::kMaxRows, n_q_heads, max_blocks, causal));
 }
 
 size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
@@ -377,11 +391,9 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad max_blocks_per_seq");
     int rc = pkv::rows_plan(a.pool, a.rows, true, &a.plan, fit ? ws_bytes : SIZE_MAX);
     if (rc) return rc;
-    const size_t need = fit ? a.plan.bytes
-                            : rows_workspace_bytes(a.pool, a.rows, a.n_q_heads, a.max_blocks, a.causal && a.cu_q);
-    if (ws_bytes < need)
+    if (ws_bytes < a.plan.bytes)
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
-                                                  " bytes, needs " + std::to_string(need));
+                                                  " bytes, needs " + std::to_string(a.plan.bytes));
     if (prompt_kernel_pays(a, ws_bytes)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
@@ -431,11 +443,10 @@ static int decode_call(const pf_pool *pool, int layer, const void *q, const void
             // the append first: a launch of its own, since a page's new scale is needed before any of its rows
             pkv::AppendArgs w{pool, layer, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, nullptr,
                               n_seqs, 1};
-            const size_t need8 = rows_workspace_bytes(pool, group, n_q_heads, max_blocks_per_seq, false);
-            if (need8 == 0) return PF_ERR_CUDA;   // message set
-            if (ws_bytes < need8)   // nothing is launched by a call that fails
+            if ((rc = pkv::rows_plan(pool, group, true, &a.plan)) != PF_OK) return rc;
+            if (ws_bytes < a.plan.bytes)   // nothing is launched by a call that fails
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: workspace has " + std::to_string(ws_bytes) +
-                                                          " bytes, needs " + std::to_string(need8));
+                                                          " bytes, needs " + std::to_string(a.plan.bytes));
             if ((long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
                 return pkv::set_error(PF_ERR_INVALID, "pf_decode_step: bad max_blocks_per_seq");
             rc = pkv::launch_append(w, static_cast<cudaStream_t>(stream));
@@ -530,16 +541,23 @@ size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads
     }
     const int rows = append_rows(pool, n_q_heads, max_new_tokens);
     if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
-        return pkv::prompt_workspace_bytes(pool, true, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens);
+        return prompt_or_rows_workspace_bytes(pool, true, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens);
     if (pool->dtype == PF_E4M3) {
         return rows_workspace_bytes(pool, rows, n_q_heads, max_blocks_per_seq, true);
     }
-    pkv::AttnPlan plan;
-    // sized like pf_decode_workspace_bytes: by the resident grid, or by a
-    // bound on it when no device can be queried
-    if (pkv::attention_plan(pool, n_seqs, rows * pool->n_kv_heads, max_blocks_per_seq, 0, false, &plan) != PF_OK)
-        return 0;
-    return plan.counter_bytes + plan.partial_bytes;
+    // sized like pf_decode_workspace_bytes, by the resident grid, or by a bound
+    // on it when no device can be queried; the most that any count of tokens up
+    // to this one takes (above 8 rows of 128 values the kernel serves fewer heads
+    // at a time, whose records are smaller)
+    const int group = n_q_heads / pool->n_kv_heads;
+    size_t most = 0;
+    for (int r = group; r <= rows; r += group) {
+        pkv::AttnPlan plan;
+        if (pkv::attention_plan(pool, n_seqs, r * pool->n_kv_heads, max_blocks_per_seq, 0, false, &plan) != PF_OK)
+            return 0;
+        most = std::max(most, plan.counter_bytes + plan.partial_bytes);
+    }
+    return most;
 }
 
 int pf_paged_prefill_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
@@ -619,7 +637,7 @@ size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, 
     }
     const int rows = cross_rows(pool, n_q_heads, max_q_tokens);
     if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
-        return pkv::prompt_workspace_bytes(pool, false, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens);
+        return prompt_or_rows_workspace_bytes(pool, false, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens);
     return rows_workspace_bytes(pool, rows, n_q_heads, max_blocks_per_seq, false);
 }
 

@@ -1,6 +1,7 @@
 """One workspace under calls of every kind: the kernels share its layout, a
 front of 33,280 bytes (reserved bytes, then from byte 512 the few-rows
-kernel's flags) and records behind it."""
+kernel's flags) and records behind it; and under calls of fewer tokens than it
+was made for."""
 import numpy as np
 import pytest
 
@@ -58,4 +59,45 @@ def test_flags_hold_nothing_but_flags(pkv, cuda_dev):
         for i in np.random.default_rng(3).permutation(np.repeat(np.arange(len(calls)), 2)):
             calls[i](dtype)
             assert not host(ws[FLAGS]).any(), f"call {i}"
+    assert pkv.pf_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("made_for", [9, 12, 16, 40])
+@pytest.mark.parametrize("h,d", [(12, 64), (4, 128)])
+@pytest.mark.parametrize("kind", ["e4m3", "f16", "cross"])
+def test_workspace_made_for_more_tokens(pkv, cuda_dev, made_for, h, d, kind):
+    """A program sizes its workspace for the most tokens of a step; steps of fewer use the same."""
+    import torch
+    lens = [900, 60]
+    scale = float(np.float32(d ** -0.5))
+    if kind == "e4m3":
+        c = Case(pkv, cuda_dev, lens, h, h, d, 16)
+        c.fill()
+        pool, layer, table = c.pool, 1, dev(wide_table(c), cuda_dev)
+    else:
+        c = PagedCase(pkv, cuda_dev, lens, h, h, d, 16)
+        pool, layer, table = c.pool, 0, c.bt_dev
+    make = pkv.make_cross_workspace if kind == "cross" else pkv.make_prefill_workspace
+    call = pkv.pf_paged_cross_attention if kind == "cross" else pkv.pf_paged_prefill_attention
+    ws = make(pool, 2, h, table.shape[1], made_for)
+    for n in (1, 4, 7, 8, 9, 12, 16, 40):
+        if n > made_for:
+            break
+        offs = np.array([0, n, 2 * n], np.int32)
+        q = np.random.default_rng(n).standard_normal((2 * n, h, d)).astype(np.float16)
+        for dtype in (torch.float16, torch.float32):
+            out = torch.empty((2 * n, h, d), dtype=dtype, device=cuda_dev)
+            call(pool, layer, dev(q, cuda_dev), table, dev(np.array(lens, np.int32), cuda_dev), dev(offs, cuda_dev), n,
+                 scale, out, ws)
+            if kind == "e4m3":
+                want, tol = c.want(q, offs, True, F16, F16)
+                tol = tol + c.small_terms(q, offs)
+            else:
+                got = []
+                for s, L in enumerate(lens):
+                    rows = [x[0][c.bt[s][np.arange(L) // 16], np.arange(L) % 16] for x in (c.k_host, c.v_host)]
+                    got.append(attention64(q[offs[s]:offs[s + 1]], *rows, scale, kind != "cross", F16, F16))
+                # (the fp16 pools' kernels may sum the rounded weights: as far off again at most)
+                want, tol = np.concatenate([o for o, _ in got]), 2 * np.concatenate([t for _, t in got])
+            assert_within(host(out), want, tol, f"{n} tokens")
     assert pkv.pf_device_status(reset=True) == 0
