@@ -423,7 +423,7 @@ def pf_paged_prefill_attention(pool, layer, q, block_tables, context_lens, cu_q,
     n = context_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != n or cu_q.numel() != n + 1:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
-    if tuple(out.shape) != tuple(q.shape) or q.shape[-1] != pool.head_dim:
+    if q.dim() != 3 or q.shape[2] != pool.head_dim or tuple(out.shape) != tuple(q.shape):
         raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out must have the shape of q")
     dev = None if pool.k_scale is None else _pool_device(pool)
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
@@ -592,8 +592,8 @@ def pf_paged_decode_attention_noalloc(pool, layer, q, block_tables, context_lens
     n, hq, d = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.numel() != n:
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; context_lens [n_seqs]")
-    if tuple(out.shape) != (n, hq, d):
-        raise PagedKVError(PF_ERR_INVALID, "out must have the shape of q")
+    if tuple(out.shape) != (n, hq, d) or d != pool.head_dim:
+        raise PagedKVError(PF_ERR_INVALID, "q must be [n_seqs, n_q_heads, head_dim], out must have the shape of q")
     out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
     if out_dtype is None:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
