@@ -345,7 +345,11 @@ PF_API int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stre
  * often as wanted) must not overlap on the GPU.
  * 8-bit pools: split_tokens 0 only (any page size, up to 16 q-heads per
  * kv-head); K and V are code * scale, the products run on tensor cores as
- * above (codes are exact in fp16). */
+ * above (codes are exact in fp16).  There the weight and its V scale, taken
+ * relative to the largest of the context, are rounded together: to 11 bits or
+ * 2^-32 of the largest weight times the largest V scale, whichever is more, for
+ * fp16 output (2^-25 on the prompt kernel, which small batches take), to 22 bits
+ * or as much for fp32 output. */
 PF_API int pf_paged_decode_attention(const pf_pool *pool, int layer, const void *q,
                               const int32_t *block_tables,
                               int max_blocks_per_seq,
@@ -462,7 +466,8 @@ PF_API size_t pf_prefill_workspace_bytes(const pf_pool *pool, int n_seqs,
  * Either pool type.  With a workspace (pf_cross_workspace_bytes, initialised
  * once with pf_decode_workspace_init, not shared by overlapping calls) and at
  * most 16 query rows (tokens x q-heads) per kv-head, a kernel that cuts long
- * contexts over the SMs, fp32 output with the weights to about 22 bits;
+ * contexts over the SMs, fp32 output with the weights to about 22 bits (or
+ * 2^-32 of the largest, over 8-bit pools as pf_paged_decode_attention says);
  * otherwise, and for fp16 output of small batches, the tcgen05 kernel, the
  * weights rounded to fp16; with a workspace it cuts long contexts of few
  * blocks over the SMs and merges the parts in a second launch. */

@@ -43,7 +43,9 @@
 //   (row sums too, so it cancels) and relative to the largest V scale met so
 //   far: at most 2^15, and normal fp16 down to 2^-21 of the largest scale's.
 //   The row sum is that of the fp32 weights.  fp32 output takes the product
-//   twice, with the weight's fp16 part and with its rounding error.
+//   twice, with the weight's fp16 part and with its rounding error, which is
+//   normal fp16 down to 2^-10 of the largest scale's.  Below these a weight is
+//   off by half of fp16's smallest, 2^-32 of the largest weight and scale.
 // * A pair cut between spans leaves its parts (acc, m, l) in the workspace,
 //   each with a flag that carries the launch's stamp, set behind one fence once
 //   the warp's span is done; the warp of the pair's last part then waits for
