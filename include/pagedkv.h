@@ -44,8 +44,9 @@
  * powers of two, set by pf_append_kv.  The pool's type decides what a call
  * does; calls that do not exist for it give PF_ERR_UNSUPPORTED.
  *
- * Block tables are int32 [n_seqs][max_blocks_per_seq], row-major; entries
- * past a sequence's ceil(L / block_size) used blocks are never read.
+ * Block tables are int32 [n_seqs][max_blocks_per_seq], row-major.  Entries
+ * past a sequence's ceil(L / block_size) used blocks may hold anything: they
+ * are never used (though some are read before the length is known).
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -89,7 +90,8 @@ typedef struct pf_alloc pf_alloc;
 /* Message of the last failing call on this thread ("" if none). */
 PF_API const char *pf_last_error(void);
 
-/* ABI version of this header (PF_ABI_VERSION). */
+/* ABI version of this header (PF_ABI_VERSION): raised when a call or a constant
+ * changes its meaning, not when calls are added. */
 #define PF_ABI_VERSION 3
 PF_API int pf_abi_version(void);
 

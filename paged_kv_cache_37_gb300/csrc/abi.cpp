@@ -365,6 +365,10 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
 //   x 128, fp16: 256 tokens 27.7 / 16.4, 1024 tokens, e4m3 38.6 / 39.1; 32
 //   sequences of 512 tokens, e4m3 x 128: 8 rows 22.5 / 23.8, 9 25.9 / 23.9;
 //   38 of 512 tokens, e4m3 x 64: 9 rows 18.2 / 19.0, 16 19.5 / 19.2.
+// So at its border the rule is a few per cent from the better kernel either way
+// (two waves of 9 rows x 64 and 512 tokens take the prompt kernel, 4 % slower).
+// The table's width stands for the contexts, which the host does not know: over
+// tables much wider than their contexts few rows stay with the few-rows kernel.
 // fp32 results stay with the few-rows kernel, which does not round its weights
 // to fp16.
 static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {

@@ -17,12 +17,12 @@
 // as 0, and neither counts for the scale.
 //
 // Append: 2 bytes read and 1 written per value, HBM bound: 8192 tokens of 40
-// heads x 128 take 39.7 us, 6.35 TB/s; one token each for 128 sequences 3.1 us,
+// heads x 128 take 40.4 us, 6.24 TB/s; one token each for 128 sequences 2.9 us,
 // a launch and three dependent loads.  One group of
 // threads takes one (page, kv-head, K or V) and keeps all its new rows in
 // registers between the maximum and the rounding, so they are read once; the
 // group is a warp for 16-token pages (4 or 8 16-byte loads in flight per
-// lane), 8 or 16 lanes for 1-token pages, 4 or 8 warps above.
+// lane), 8 or 16 lanes for 1-token pages, 2 to 8 warps above.
 #include <algorithm>
 
 #include "device_common.cuh"

@@ -37,11 +37,14 @@
 // the softmax threads exponentiate.
 //
 // Measured (GB300; 4 prompts of 2048 tokens): 12 heads x 64 46 us, 32 q-heads
-// over 8 kv-heads x 128 142 us, over an e4m3 pool 144 us.  What bounds it (clock64
-// traces): of a K/V step's 2,400 cycles at head_dim 64 the exponentials of two
-// query tiles take 2,050 on the MUFU pipe -- so P lives in tensor memory, the
-// row sums are summed on the CUDA cores rather than by another MMA over P, and
-// nothing else of a step may wait.  At head_dim 128 MMAs and softmax share it.
+// over 8 kv-heads x 128 142 us, over an e4m3 pool 145 us.  A K/V step at head_dim
+// 64 takes 2,400 cycles (clock64), and no pipe is full: the exponentials of two
+// query tiles are 1,024 cycles at the 32 per cycle and SM that a loop of
+// ex2.approx reaches, and whole cross prompts have the issue slots 51 %, the
+// tensor pipe 32 % and the MUFU pipe 34 % busy.  A step is a chain (scores,
+// maximum, exponentials, P, product) in two softmax warps per scheduler, so its
+// latency counts: P lives in tensor memory, the row sums are summed on the CUDA
+// cores rather than by another MMA over P, and nothing else of a step may wait.
 // TMA boxes issued from one warp arrive at a few hundred cycles each whatever
 // their size, and the rate grows with the number of issuing warps (measured:
 // 1, 2, 4 warps -> 11.8, 23.4, 44 bytes a cycle per SM on 8 KB boxes), hence

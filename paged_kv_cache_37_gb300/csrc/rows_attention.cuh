@@ -11,9 +11,13 @@
 //
 // Bound: every K and V byte of the context is read once and used for at most
 // 16 rows, so HBM bounds it; the rest is kept below that.  Measured on GB300:
-// 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 24.1 us, of
-// which about 10 are the way to the first rows and the last merge; 16 x 2048
-// tokens, 40 heads x 128, fp32 results (336 MB) 64 us, 5.3 TB/s.
+// 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 23.8 us (26.5
+// when the pool is not in L2), of which about 10 are the way to the first rows
+// and the last merge; 256 sequences of 32 to 4096 tokens, 7 rows, 2 heads x 64
+// (137 MB) 35.6 us; 16 x 2048 tokens, 40 heads x 128, fp32 results (336 MB) 63 us,
+// 5.3 TB/s.  The first two are bound by latency and issue, not by HBM: 565 and
+// 485 warp instructions per 4 KB stage, 45 % of the issue slots with four warps
+// per scheduler.
 // * Work: stages of ST tokens (a 4 KB piece of K and V for one head at 64-
 //   and 128-byte rows).  The stages of all (sequence, group of HG kv-heads)
 //   pairs are cut into equal spans, one per team of HG warps; warp hl of a
