@@ -165,8 +165,8 @@ int kernel_for(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_cores, 
     return PF_OK;
 }
 
-// A captured launch is counted by its CTAs (attn::kLaunchStep).
-constexpr int kMaxGrid = (int)attn::kLaunchStep;
+// A captured launch is counted by its CTAs.
+constexpr int kMaxGrid = (int)kLaunchStep;
 
 // Persistent grid of the kernel on the current device: SMs x resident CTAs.
 int resident_grid(const pf_pool *pool, int n_q_heads, bool spans, bool cuda_cores, int *grid) {
@@ -217,10 +217,14 @@ std::atomic<int> g_inject_timeout{0};
 
 }  // namespace
 
-unsigned next_epoch() {
-    unsigned e = ++g_epoch;
-    if (e == 0) e = ++g_epoch;
-    return e;
+unsigned next_epoch() { return ++g_epoch; }
+
+int is_captured(cudaStream_t stream, bool *out) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(stream, &capture);
+    if (e != cudaSuccess) return cuda_error(e, "attention: cudaStreamIsCapturing");
+    *out = capture != cudaStreamCaptureStatusNone;
+    return PF_OK;
 }
 
 int attention_plan(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks, int split_tokens,
@@ -308,9 +312,9 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
     p.partials = reinterpret_cast<float *>(ws + plan.counter_bytes);
     p.span_recs = reinterpret_cast<unsigned long long *>(ws + plan.counter_bytes);
     p.jobs = reinterpret_cast<attn::Job *>(ws + plan.counter_bytes + rec_bytes);
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(stream, &capture);
-    if (e != cudaSuccess) return cuda_error(e, "pf_paged_decode_attention: cudaStreamIsCapturing");
+    bool captured = false;
+    rc = is_captured(stream, &captured);
+    if (rc) return rc;
     p.status = status;
     p.max_blocks = a.max_blocks;
     p.n_q_heads = a.n_q_heads;
@@ -355,7 +359,7 @@ int launch_attention(const AttnArgs &a, cudaStream_t stream) {
         p.bt = a.block_tables + (size_t)s0 * a.max_blocks;
         p.lens = a.context_lens + s0;
         p.n_seqs = n;
-        p.stamp = capture == cudaStreamCaptureStatusNone ? attn::host_stamp(next_epoch()) : 0;
+        p.stamp = captured ? 0 : host_stamp(next_epoch());
         if (a.overlap_previous) {
             // A programmatic dependent of the previous kernel on the stream:
             // resident while that kernel drains; the kernel waits for it

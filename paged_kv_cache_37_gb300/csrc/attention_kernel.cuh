@@ -858,28 +858,12 @@ __device__ __forceinline__ void merge_pair(const Params &p, int first, int n, in
     }
 }
 
-// The stamp of a launch marks what it leaves in the workspace.  A plain launch
-// brings its own (p.stamp, the host's count).  A captured one (p.stamp = 0) is the
-// same every time that it is replayed, so its stamp comes from a count in the
-// front of the workspace, zero at first, to which it adds kLaunchStep in all: one
-// from each CTA and the rest from the first.  A CTA's first consumer warp reads
-// the count at its start and the producer adds at its end, so until every CTA has
-// read it, count / kLaunchStep is what the launch found; the next launch over the
-// workspace starts after this one's end.  (Replayed back to back, 128 mixed
-// sequences: 30.95 us a step with the host's stamps, 31.07 so, 31.2 when consumer
-// warps add, 31.5 when each of them also reads; 32 short ones 8.55, 8.76, 8.81,
-// 8.9.)
-// The bits of a stamp are those of an fp32 NaN, an infinity or a number below
-// -2^65, 0xe... for the host's and 0xf... for the workspace's.  Neither a
-// record's finite values nor a job's integers are, so what other kinds of calls
-// left in a workspace is not taken for stamped.  It comes round after 2^28
-// launches.
-constexpr unsigned long long kLaunchStep = 1 << 16;
-__host__ __device__ constexpr unsigned host_stamp(unsigned count) { return 0xe0000000u | (count & 0x0fffffffu); }
-__device__ __forceinline__ unsigned count_stamp(unsigned long long launches) {
-    return 0xf0000000u | (unsigned)(launches & 0x0fffffffu);
-}
-
+// The launch's stamp (device_common.cuh): of a captured launch (p.stamp = 0) from
+// the count in the front of the workspace, which a CTA's first consumer warp reads
+// at its start and the producer adds to at its end.  (Replayed back to back, 128
+// mixed sequences: 30.95 us a step with the host's stamps, 31.07 so, 31.2 when
+// consumer warps add, 31.5 when each of them also reads; 32 short ones 8.55, 8.76,
+// 8.81, 8.9.)
 __device__ __forceinline__ unsigned long long *launch_count(const Params &p) {
     return p.span_recs - (kWorkspaceFront - kStateOffset) / sizeof(unsigned long long);
 }
@@ -1733,7 +1717,7 @@ __device__ __forceinline__ void decode_attention(const CUtensorMap &tmk, const C
         producer<D, G, HG, MMA>(&tmk, &tmv, p, sm, lane);
         if (p.stamp == 0 && lane == 0) {   // (launch_stamp)
             mbar_wait(smem_addr(&sm.stamped), 0, p.status);
-            atomicAdd(launch_count(p), blockIdx.x == 0 ? kLaunchStep - (unsigned long long)(gridDim.x - 1) : 1ull);
+            add_launch(launch_count(p));
         }
     }
     else if constexpr (MMA) consumers_mma<D, G, HG, HILO>(p, sm, warp - 1, lane);

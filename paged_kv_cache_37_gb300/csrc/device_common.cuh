@@ -140,6 +140,27 @@ __device__ __forceinline__ unsigned long long ld_tagged(const unsigned long long
 __device__ __forceinline__ float tagged_value(unsigned long long w) { return __uint_as_float((unsigned)w); }
 __device__ __forceinline__ unsigned tag_of(unsigned long long w) { return (unsigned)(w >> 32); }
 
+// The stamp of a launch marks what it leaves in a workspace for other CTAs.  A
+// plain launch brings the host's count.  A captured one is the same every time that
+// it is replayed, so its stamp comes from a count in the front of the workspace,
+// zero at first, to which it adds kLaunchStep in all: one from each CTA and the
+// rest from the first.  A CTA adds after it has read, so until every CTA has read
+// it, count / kLaunchStep is what the launch found; the next launch over the
+// workspace starts after this one's end.
+// The bits of a stamp are those of an fp32 NaN, an infinity or a number below
+// -2^65, 0xe... for the host's and 0xf... for the workspace's.  Neither a
+// record's finite values nor a job's integers are, so what other kinds of calls
+// left in a workspace is not taken for stamped.  It comes round after 2^28
+// launches.
+constexpr unsigned long long kLaunchStep = 1 << 16;
+__host__ __device__ constexpr unsigned host_stamp(unsigned count) { return 0xe0000000u | (count & 0x0fffffffu); }
+__device__ __forceinline__ unsigned count_stamp(unsigned long long launches) {
+    return 0xf0000000u | (unsigned)(launches & 0x0fffffffu);
+}
+__device__ __forceinline__ void add_launch(unsigned long long *count) {   // one thread of each CTA
+    atomicAdd(count, blockIdx.x == 0 ? kLaunchStep - (unsigned long long)(gridDim.x - 1) : 1ull);
+}
+
 __device__ __forceinline__ void st_relaxed(unsigned *p, unsigned v) {
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }

@@ -31,7 +31,7 @@ constexpr int kTileTokens = 16;
 constexpr int kTcMinRows = 128;
 
 // Front of every attention workspace: reserved bytes; from kStateOffset on the
-// count of the decode kernel's captured launches over it (64 bits); from
+// count of captured launches over it (64 bits, device_common.cuh); from
 // kFlagOffset on the flags of the few-rows kernel (two per warp of up to
 // kFlagSms CTAs of kFlagWarps warps).  Records of every kernel lie behind it,
 // so that whatever calls share a workspace -- other kernels, shapes or pool
@@ -174,9 +174,10 @@ struct GatherArgs {
 int launch_gather_kv(const GatherArgs &a, cudaStream_t stream);
 int launch_gather_e4m3(const GatherArgs &a, cudaStream_t stream);
 
-// Stamp of each launch of the few-rows kernel, which clears the flags that it
-// sets (never 0: clear).
+// What plain launches are stamped by, counted; whether a launch on the stream is
+// captured (then stamp 0: device_common.cuh).
 unsigned next_epoch();
+int is_captured(cudaStream_t stream, bool *out);
 
 // SMs of the current device; without one an error, or a bound for sizing.
 int device_sms(bool need_device, int *sms);

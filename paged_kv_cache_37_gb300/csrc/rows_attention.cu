@@ -109,6 +109,9 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     // as many as keep the work units below 2^31 however long the contexts are.
     const long long most = ((long long)a.max_blocks * pool->block_size / 16 + 1 + rows::kPairCost) * p.n_groups;
     if (most > 0x7fffffffll) return set_error(PF_ERR_INVALID, "attention: max_blocks_per_seq is too large for the heads");
+    bool captured = false;
+    const int rc = is_captured(stream, &captured);
+    if (rc) return rc;
     const int step = (int)(0x7fffffffll / most < rows::kMaxSeqs ? 0x7fffffffll / most : rows::kMaxSeqs);
     for (int s0 = 0; s0 < a.n_seqs; s0 += step) {
         const size_t q0 = a.cu_q ? 0 : (size_t)s0 * row;   // cu_q holds absolute rows
@@ -118,7 +121,7 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
         p.lens = a.context_lens + s0;
         p.cu_q = a.cu_q ? a.cu_q + s0 : nullptr;
         p.n_seqs = a.n_seqs - s0 < step ? a.n_seqs - s0 : step;
-        p.stamp = next_epoch();
+        p.stamp = captured ? 0 : host_stamp(next_epoch());
         p.after_append = a.after_append && s0 == 0;
         // a programmatic dependent of the kernel before it: its blocks take
         // their SMs as that kernel's leave them, and then wait for its end

@@ -11,10 +11,10 @@
 //
 // Bound: every K and V byte of the context is read once and used for at most
 // 16 rows, so HBM bounds it; the rest is kept below that.  Measured on GB300:
-// 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 23.8 us (26.5
+// 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 24.0 us (26.6
 // when the pool is not in L2), of which about 10 are the way to the first rows
 // and the last merge; 256 sequences of 32 to 4096 tokens, 7 rows, 2 heads x 64
-// (137 MB) 35.6 us; 16 x 2048 tokens, 40 heads x 128, fp32 results (336 MB) 63 us,
+// (137 MB) 35.5 us; 16 x 2048 tokens, 40 heads x 128, fp32 results (336 MB) 63 us,
 // 5.3 TB/s.  The first two are bound by latency and issue, not by HBM: 565 and
 // 485 warp instructions per 4 KB stage, 45 % of the issue slots with four warps
 // per scheduler.
@@ -54,8 +54,8 @@
 //   each with a flag that carries the launch's stamp, set behind one fence once
 //   the warp's span is done; the warp of the pair's last part then waits for
 //   the others' flags, merges the parts with the log-sum-exp rule and clears
-//   the flags (a captured launch has the same stamp every time it is
-//   replayed).  The parts waited for belong to earlier spans, whose warps wait
+//   the flags.  Every launch and replay has a stamp of its own, so a flag that
+//   is set after a wait for it ran out counts for no later one.  The parts waited for belong to earlier spans, whose warps wait
 //   for nothing but still earlier ones, and the wait is bounded (1 s).  Where
 //   pairs are cut into many parts (few long contexts), the teams of a CTA merge
 //   theirs first, behind a CTA barrier, and the CTAs' records are the parts.
@@ -119,7 +119,7 @@ struct Params {
     int *status;
     unsigned *flags;            // [team][2][head]: the stamp once that part's record is written
     float *recs;                // [team][2][head][rows][D + 4]: parts of cut pairs (acc, m, l)
-    unsigned stamp;             // this launch's (the flags' part of a workspace holds stamps and zeros only)
+    unsigned stamp;             // this launch's, 0 when it is captured (device_common.cuh)
     int n_seqs;
     int max_blocks;
     int n_blocks;
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     __shared__ unsigned warp_sum[32];
     __shared__ int warp_max[32];
     __shared__ Spans span_sh;
+    __shared__ unsigned stamp_sh;
 
     const int warp = (int)threadIdx.x / 32;
     const int lane = (int)threadIdx.x % 32;
@@ -309,6 +310,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     // stream's previous kernel wrote, or after a step's own append (which was
     // launched when everything before it had ended) the pages only.
     if (!p.after_append) griddep_wait();
+
+    unsigned long long *count =          // of captured launches
+        reinterpret_cast<unsigned long long *>(p.flags) - (kFlagOffset - kStateOffset) / sizeof(unsigned long long);
+    if (warp == NW - 2 && lane == 0) stamp_sh = p.stamp ? p.stamp : count_stamp(ld_tagged(count) / kLaunchStep + 1);
 
     // The front of every table row into L2, shared out over the grid: the
     // lengths are not known yet.
@@ -372,6 +377,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         }
         __syncthreads();
     }
+
+    if (p.stamp == 0 && threadIdx.x == 0) add_launch(count);   // (stamp_sh has been read)
 
     // Rows of empty contexts: zeros.
     for (int s = (int)blockIdx.x * NW + warp; s < p.n_seqs; s += (int)gridDim.x * NW) {
@@ -914,8 +921,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         __syncwarp();
         if (lane == 0) {
             fence_acq_rel_gpu();
-            if (slot0) st_relaxed(p.flags + team * 2 * p.hg + hl, p.stamp);
-            if (slot1) st_relaxed(p.flags + (team * 2 + 1) * p.hg + hl, p.stamp);
+            if (slot0) st_relaxed(p.flags + team * 2 * p.hg + hl, stamp_sh);
+            if (slot1) st_relaxed(p.flags + (team * 2 + 1) * p.hg + hl, stamp_sh);
         }
     };
     flag_parts(sp.T == 1 && cut.x >= 0 && !ends, goes_on && group_end);
@@ -952,7 +959,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         unsigned long long since = 0;
         for (int k0 = 0; k0 < n_parts - 1; k0 += 32) {
             unsigned *flag = p.flags + place(min(k0 + lane, n_parts - 2));
-            while (!__all_sync(FULL, ld_acquire(flag) == p.stamp)) {
+            while (!__all_sync(FULL, ld_acquire(flag) == stamp_sh)) {
                 const unsigned long long now = global_timer_ns();
                 if (since == 0) since = now;
                 if (__any_sync(FULL, now - since > kWaitLimitNs)) {

@@ -1,11 +1,11 @@
-"""Captured calls over fp16 pools, replayed: nothing that one replay leaves in
-the workspace may count as the next one's."""
+"""Captured calls, replayed: nothing that one replay leaves in the workspace may
+count as the next one's."""
 import numpy as np
 import pytest
 
 from e4m3_util import assert_within, attention64
 from gpu_util import PagedCase, dev, host
-from test_gpu_e4m3 import F16
+from test_gpu_e4m3 import F16, Case, wide_table
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,41 @@ def test_two_graphs_and_plain_calls_share_a_workspace(pkv, cuda_dev):
             call(o)
         torch.cuda.synchronize()
         assert_within(host(o), *want(c, qn, lens), f"call {i}")
+
+
+@pytest.mark.parametrize("call", ["decode", "step", "cross"])
+def test_few_rows_replays_count_themselves(pkv, cuda_dev, call):
+    """The few-rows kernel's flags carry the launch's stamp.  A replay takes its own from the count of
+    launches at byte 256 of the workspace, 2^16 for each: with one stamp for all replays, a flag set
+    after the wait for it had run out would pass for the next replay's."""
+    import torch
+    lens = [3000, 700, 31]
+    c = Case(pkv, cuda_dev, lens, 4, 4, 64, 16)
+    c.fill()
+    table, lens_dev = dev(wide_table(c), cuda_dev), dev(c.lens, cuda_dev)
+    q = torch.zeros((3, 4, 64), dtype=torch.float16, device=cuda_dev)
+    out = torch.empty_like(q)
+    ws = pkv.make_workspace(c.pool, 3, 4, table.shape[1], 0)
+    cu = dev(np.arange(4, dtype=np.int32), cuda_dev)
+    last = [dev(np.stack([m.rows(c.table[s], L)[-1] for s, L in enumerate(lens)]).astype(np.float16), cuda_dev)
+            for m in (c.km, c.vm)]            # the newest rows once more: their codes stay
+    run = {"decode": lambda: pkv.pf_paged_decode_attention(c.pool, 1, q, table, lens_dev, c.scale(), out, 0, ws),
+           "step": lambda: pkv.pf_decode_step(c.pool, 1, q, *last, table, lens_dev, c.scale(), out, 0, ws),
+           "cross": lambda: pkv.pf_paged_cross_attention(c.pool, 1, q, table, lens_dev, cu, 1, c.scale(), out, ws)}[call]
+    g = captured(run)
+    count = lambda: int(host(ws[256:264].view(torch.int64))[0])   # noqa: E731
+    offs = np.arange(4)
+    for i in range(4):
+        qn = c.rng.standard_normal((3, 4, 64)).astype(np.float16)
+        q.copy_(dev(qn, cuda_dev))
+        assert count() == i << 16
+        g.replay()
+        torch.cuda.synchronize()
+        want, tol = c.want(qn, offs, False, F16, F16)
+        assert_within(host(out), want, tol + c.small_terms(qn, offs), f"replay {i}")
+        run()                                 # a plain call takes the host's stamp
+        torch.cuda.synchronize()
+        assert_within(host(out), want, tol + c.small_terms(qn, offs), f"after replay {i}")
+        assert count() == (i + 1) << 16
+    assert not host(ws[512:33280]).any()
+    assert pkv.pf_device_status(reset=True) == 0
