@@ -9,8 +9,8 @@
 // t < L (cross, decode) or t <= L - n + i (causal).  e4m3 pools: K_t = code *
 // k_scale[page][h], V_t = code * v_scale[page][h].
 //
-// Bound: every K and V byte of the context is read once and used for at most
-// 16 rows, so HBM bounds it; the rest is kept below that.  Measured on GB300:
+// Floor: every K and V byte of the context is read once and used for at most 16
+// rows, so it is HBM's.  Measured on GB300:
 // 128 sequences of 16 to 2048 tokens, 12 heads x 64, e4m3 (93 MB) 24.0 us (26.6
 // when the pool is not in L2), of which about 10 are the way to the first rows
 // and the last merge; 256 sequences of 32 to 4096 tokens, 7 rows, 2 heads x 64

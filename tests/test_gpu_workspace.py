@@ -7,7 +7,7 @@ import pytest
 
 from e4m3_util import assert_within, attention64
 from gpu_util import PagedCase, dev, host
-from test_gpu_e4m3 import F16, Case, wide_table
+from test_gpu_e4m3 import F16, F32, Case, wide_table
 
 pytestmark = pytest.mark.gpu
 
@@ -100,4 +100,42 @@ def test_workspace_made_for_more_tokens(pkv, cuda_dev, made_for, h, d, kind):
                 # (the fp16 pools' kernels may sum the rounded weights: as far off again at most)
                 want, tol = np.concatenate([o for o, _ in got]), 2 * np.concatenate([t for _, t in got])
             assert_within(host(out), want, tol, f"{n} tokens")
+    assert pkv.pf_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["decode", "step", "cross"])
+def test_more_sequences_than_a_launch_takes(pkv, cuda_dev, kind):
+    """2,500 sequences, some of them empty: consecutive launches over one workspace."""
+    import torch
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 40, 2500).astype(np.int32)
+    c = Case(pkv, cuda_dev, lens, 4, 2, 64, 16)
+    n = len(lens)
+    if kind == "step":
+        c.append(np.maximum(lens - 1, 0))
+    else:
+        c.fill()
+    q = rng.standard_normal((n, 4, 64)).astype(np.float16)
+    out = torch.full((n + 1, 4, 64), 7.0, dtype=torch.float32, device=cuda_dev)
+    ws = pkv.make_workspace(c.pool, n, 4, c.table.shape[1], 0)
+    args = (c.table_dev, dev(c.lens, cuda_dev))
+    pkv.pf_device_status(reset=True)
+    for _ in range(2):
+        if kind == "decode":
+            pkv.pf_paged_decode_attention(c.pool, 1, dev(q, cuda_dev), *args, c.scale(), out[:-1], 0, ws)
+        elif kind == "cross":
+            pkv.pf_paged_cross_attention(c.pool, 1, dev(q, cuda_dev), *args, dev(np.arange(n + 1, dtype=np.int32), cuda_dev),
+                                         1, c.scale(), out[:-1], ws)
+        elif c.at.sum() < lens.sum():
+            k, v = c.rows(n), c.rows(n)
+            pkv.pf_decode_step(c.pool, 1, dev(q, cuda_dev), dev(k, cuda_dev), dev(v, cuda_dev), *args, c.scale(),
+                               out[:-1], 0, ws)
+            one = np.concatenate([[0], np.cumsum(lens > 0)])     # an empty context takes no row
+            c.km.append(k[lens > 0], c.table, c.lens, one)
+            c.vm.append(v[lens > 0], c.table, c.lens, one)
+            c.at = c.lens.copy()
+            c.check_pool()
+        want, tol = c.want(q, np.arange(n + 1), False, 2.0 ** -21, F32)
+        assert_within(host(out)[:-1], want, tol)
+    assert bool((out[-1] == 7.0).all())
     assert pkv.pf_device_status(reset=True) == 0
