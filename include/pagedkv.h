@@ -215,6 +215,41 @@ PF_API int pf_write_kv(const pf_pool *pool, int layer, const void *k_new,
                 const int32_t *seq_idx, const int32_t *pos, int n_tokens,
                 void *stream);
 
+/* Norms of queries and keys for each head, the position rotation and the
+ * write of K and V into their pages, in one pass (no counterpart on the pages,
+ * whose rows come rotated).  Row i of q ([n_tokens][n_q_heads][D]), k and v
+ * ([n_tokens][Hkv][D], all fp16) are token i's; heads are contiguous, tokens
+ * q_stride, k_stride and v_stride values apart (multiples of 8: slices of one
+ * projection's output will do).  For each row x of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * weight   (q_weight, k_weight: fp32 [D]; NULL:
+ *                                             y = x)
+ *   (a, b) -> (a c_j - b s_j, b c_j + a s_j) for the pairs a = y_j, b = y_{j +
+ *             rot_dim / 2}, or with PF_ROPE_INTERLEAVED a = y_2j, b = y_{2j + 1},
+ *             j < rot_dim / 2, the other values as they are; c_j = angles[p][j]
+ *             and s_j = angles[p][rot_dim / 2 + j], p = rope_pos[i] or, where
+ *             that is NULL, pos[i]
+ * in fp32, rounded once.  angles: fp32 [n_positions][rot_dim], cosines and sines
+ * (any frequencies, and any factor in them); rot_dim: a multiple of 16, at most
+ * D, 0 for no rotation (angles may then be NULL).
+ * q_out takes the queries; K rows go to their slots of layer `layer` with the V
+ * rows, as pf_write_kv writes them (block_tables, seq_idx, pos as there; fp16
+ * pools), and to k_out if that is not NULL.  block_tables NULL: no cache is
+ * written, k_out is needed (8-bit pools: pf_append_kv takes it), v, seq_idx and
+ * with rope_pos or rot_dim = 0 also pos may be NULL.  q NULL with n_q_heads 0: no
+ * queries; k NULL: no keys.  q_out and k_out have strides too and may be q and
+ * k themselves (same address and stride); otherwise outputs overlap no input.
+ * A rotation position outside [0, n_positions) sets PF_DEV_BAD_POSITION and the
+ * token's queries and keys are not written; a slot that pf_write_kv would skip is
+ * flagged and skipped the same way. */
+enum pf_rope_flags { PF_ROPE_INTERLEAVED = 1 };
+PF_API int pf_norm_rope_write(const pf_pool *pool, int layer, const void *q, int64_t q_stride, const void *k,
+                       int64_t k_stride, const void *v, int64_t v_stride, int n_tokens, int n_q_heads,
+                       const float *q_weight, const float *k_weight, float eps, const float *angles,
+                       int n_positions, int rot_dim, int flags, const int32_t *rope_pos,
+                       const int32_t *block_tables, int n_table_rows, int max_blocks_per_seq,
+                       const int32_t *seq_idx, const int32_t *pos, void *q_out, int64_t q_out_stride, void *k_out,
+                       int64_t k_out_stride, void *stream);
+
 /* Quantising append into an 8-bit pool (no counterpart on the pages): the
  * last n_s tokens of sequence s, n_s = cu_new[s + 1] - cu_new[s], of its
  * L = context_lens[s] (the new ones included), are rows cu_new[s] ..

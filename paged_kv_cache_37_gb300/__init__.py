@@ -10,7 +10,7 @@ is missing or whose CUDA launch fails raises.
 """
 from ._native import (  # noqa: F401
     PF_DEV_BAD_BLOCK_ID, PF_DEV_BAD_LENGTH, PF_DEV_BAD_POSITION, PF_DEV_NONFINITE, PF_DEV_WAIT_TIMEOUT,
-    PF_STEP_OVERLAP_PREVIOUS,
+    PF_ROPE_INTERLEAVED, PF_STEP_OVERLAP_PREVIOUS,
     PF_ERR_CUDA, PF_ERR_DOUBLE_FREE, PF_ERR_INVALID, PF_ERR_OOM, PF_ERR_UNSUPPORTED,
     PF_E4M3, PF_F16, PF_F32, PF_OK,
     Allocator, DoubleFree, OutOfBlocks, PagedKVError, Pool,
@@ -24,6 +24,7 @@ from ._native import (  # noqa: F401
     pf_paged_prefill_attention, pf_prefill_workspace_bytes,
     pf_alloc_compact, pf_append_kv, pf_compact_blocks, pf_cross_workspace_bytes, pf_paged_cross_attention,
     pf_pool_bytes, pf_pool_create, pf_pool_create_e4m3, pf_scale_bytes,
+    pf_norm_rope_write,
     pf_pool_destroy, pf_seq_release, pf_seq_reserve, pf_write_kv,
 )
 
@@ -59,3 +60,15 @@ def make_workspace(pool, n_seqs, n_q_heads, max_blocks_per_seq, split_tokens=0, 
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device or pool.k_pool.device)
     pf_decode_workspace_init(ws)
     return ws
+
+
+def make_rope_angles(n_positions, rot_dim, theta=10000.0, device=None):
+    """The table of pf_norm_rope_write for positions 0 .. n_positions - 1 (with
+    torch): fp32 [n_positions, rot_dim], the cosines, then
+    the sines, of p * theta^(-2 j / rot_dim), j < rot_dim / 2.  The angles are
+    taken in 64 bits: in 32 a position past 2^20 is off by up to 2^-4 radians."""
+    import torch
+    p = torch.arange(n_positions, device=device or "cuda", dtype=torch.float64)
+    f = float(theta) ** (-2.0 * torch.arange(rot_dim // 2, device=p.device, dtype=torch.float64) / rot_dim)
+    a = p[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()

@@ -30,6 +30,7 @@ PF_DEV_BAD_POSITION = 4
 PF_DEV_WAIT_TIMEOUT = 8
 PF_DEV_NONFINITE = 16
 PF_STEP_OVERLAP_PREVIOUS = 1
+PF_ROPE_INTERLEAVED = 1
 
 _lib = None
 
@@ -64,6 +65,7 @@ def lib():
                            f"{path} is not built; call paged_kv_cache_37_gb300.build() first")
     L = ctypes.CDLL(path)
     P, I, Z, F, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint64
+    I64 = ctypes.c_int64
     sigs = {
         "pf_last_error": (ctypes.c_char_p, []),
         "pf_abi_version": (I, []),
@@ -94,6 +96,8 @@ def lib():
         "pf_swap_out": (I, [P, P, I, P, P]),
         "pf_swap_in": (I, [P, P, P, I, P]),
         "pf_write_kv": (I, [P, I, P, P, P, I, I, P, P, I, P]),
+        "pf_norm_rope_write": (I, [P, I, P, I64, P, I64, P, I64, I, I, P, P, F, P, I, I, I, P, P, I, I, P, P, P, I64, P,
+                                   I64, P]),
         "pf_append_kv": (I, [P, I, P, P, P, I, P, P, I, I, P]),
         "pf_gather_kv": (I, [P, I, P, I, P, P, I, P, P, P]),
         "pf_decode_workspace_bytes": (Z, [P, I, I, I, I]),
@@ -137,6 +141,25 @@ def _dev_ptr(t, name, dtype=None, dev=None):
     if dtype is not None and t.dtype != dtype:
         raise PagedKVError(PF_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _rows_ptr(t, name, heads, head_dim, dev):
+    """Address and stride between tokens (in values) of fp16 rows [T, heads,
+    head_dim] whose heads are contiguous and tokens any distance apart."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
+        raise PagedKVError(PF_ERR_INVALID, f"{name} must be [n_tokens, {heads}, {head_dim}]")
+    if not t.is_cuda:
+        raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise PagedKVError(PF_ERR_INVALID, f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.dtype != torch.float16:
+        raise PagedKVError(PF_ERR_INVALID, f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise PagedKVError(PF_ERR_INVALID, f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim
 
 
 def _stream_ptr(stream):
@@ -492,6 +515,59 @@ def pf_append_kv(pool, layer, k_new, v_new, block_tables, context_lens, cu_new, 
                               _dev_ptr(context_lens, "context_lens", torch.int32, dev),
                               None if cu_new is None else _dev_ptr(cu_new, "cu_new", torch.int32, dev), n,
                               int(max_new_tokens), _stream_ptr(stream)))
+
+
+def pf_norm_rope_write(pool, layer, q, k, v, block_tables, seq_idx, pos, angles, q_out, k_out=None, q_weight=None,
+                       k_weight=None, eps=1e-6, interleaved=False, rope_pos=None, stream=None):
+    """Norm (with weights, fp32 [head_dim]) and rotate q and k rows, and write K
+    and V into the pages of an fp16 pool, in one launch.  angles: fp32
+    [n_positions, rot_dim] (make_rope_angles), or None for no rotation; token
+    i's is row rope_pos[i], or pos[i].  q [T, n_q_heads, D], k, v [T, n_kv_heads,
+    D] and the outputs may be slices of wider rows (heads contiguous).  Without
+    block_tables nothing is cached and k_out takes the keys; q or k None: only the
+    other."""
+    import torch
+    dev = _pool_device(pool)
+    D = pool.head_dim
+    first = k if q is None else q
+    if first is None:
+        raise PagedKVError(PF_ERR_INVALID, "neither queries nor keys")
+    n = first.shape[0]
+    for t, name in ((k, "k"), (v, "v"), (q_out, "q_out"), (k_out, "k_out")):
+        if t is not None and t.shape[0] != n:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} must have {n} rows")
+    if (q is None) != (q_out is None):
+        raise PagedKVError(PF_ERR_INVALID, "q needs q_out, and q_out q")
+    hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise PagedKVError(PF_ERR_INVALID, "q must be [n_tokens, n_q_heads, head_dim]")
+        hq = q.shape[1]
+    for t, name in ((seq_idx, "seq_idx"), (pos, "pos"), (rope_pos, "rope_pos")):
+        if t is not None and t.numel() != n:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} must have n_tokens entries")
+    if block_tables is not None and block_tables.dim() != 2:
+        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
+    if angles is not None and angles.dim() != 2:
+        raise PagedKVError(PF_ERR_INVALID, "angles must be [n_positions, rot_dim]")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and tuple(t.shape) != (D,):
+            raise PagedKVError(PF_ERR_INVALID, f"{name} must be [head_dim]")
+
+    def rows(t, name, heads):
+        return (None, 0) if t is None else _rows_ptr(t, name, heads, D, dev)
+
+    def flat(t, name, dtype):
+        return None if t is None else _dev_ptr(t, name, dtype, dev)
+    _check(lib().pf_norm_rope_write(
+        pool.handle, layer, *rows(q, "q", hq), *rows(k, "k", pool.n_kv_heads), *rows(v, "v", pool.n_kv_heads), n, hq,
+        flat(q_weight, "q_weight", torch.float32), flat(k_weight, "k_weight", torch.float32), float(eps),
+        flat(angles, "angles", torch.float32), 0 if angles is None else angles.shape[0],
+        0 if angles is None else angles.shape[1], PF_ROPE_INTERLEAVED if interleaved else 0,
+        flat(rope_pos, "rope_pos", torch.int32), flat(block_tables, "block_tables", torch.int32),
+        0 if block_tables is None else block_tables.shape[0], 0 if block_tables is None else block_tables.shape[1],
+        flat(seq_idx, "seq_idx", torch.int32), flat(pos, "pos", torch.int32), *rows(q_out, "q_out", hq),
+        *rows(k_out, "k_out", pool.n_kv_heads), _stream_ptr(stream)))
 
 
 def pf_write_kv(pool, layer, k_new, v_new, block_tables, seq_idx, pos, stream=None):

@@ -2,6 +2,7 @@
 // error reporting, pool descriptors, host-side argument validation and the
 // dispatch of the device calls to their launchers.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cstdio>
 #include <cstring>
@@ -160,6 +161,53 @@ int pf_write_kv(const pf_pool *pool, int layer, const void *k_new, const void *v
     pkv::WriteArgs a{pool, layer, k_new, v_new, block_tables, n_table_rows, max_blocks_per_seq,
                      seq_idx, pos, n_tokens};
     return pkv::launch_write_kv(a, static_cast<cudaStream_t>(stream));
+}
+
+int pf_norm_rope_write(const pf_pool *pool, int layer, const void *q, int64_t q_stride, const void *k,
+                       int64_t k_stride, const void *v, int64_t v_stride, int n_tokens, int n_q_heads,
+                       const float *q_weight, const float *k_weight, float eps, const float *angles, int n_positions,
+                       int rot_dim, int flags, const int32_t *rope_pos, const int32_t *block_tables, int n_table_rows,
+                       int max_blocks_per_seq, const int32_t *seq_idx, const int32_t *pos, void *q_out,
+                       int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream) {
+    pkv::clear_error();
+    const auto bad = [](const char *what) {
+        return pkv::set_error(PF_ERR_INVALID, std::string("pf_norm_rope_write: ") + what);
+    };
+    int rc = check_pool(pool, layer, "pf_norm_rope_write");
+    if (rc) return rc;
+    if (flags & ~PF_ROPE_INTERLEAVED) return bad("unknown flags");
+    if (n_tokens < 0) return bad("negative n_tokens");
+    if (n_tokens == 0) return PF_OK;
+    const int D = pool->head_dim;
+    const bool cached = block_tables != nullptr;
+    if (cached && (rc = need_dtype(pool, PF_F16, "pf_norm_rope_write", ": without block_tables, then pf_append_kv of k_out")) != PF_OK)
+        return rc;
+    if (!q && !k) return bad("neither queries nor keys");
+    if (q && (n_q_heads <= 0 || !q_out)) return bad("queries need n_q_heads > 0 and q_out");
+    if (q && n_q_heads > 65536) return bad("n_q_heads is too large");
+    if (!q && (n_q_heads != 0 || q_out || q_weight)) return bad("n_q_heads, q_out or q_weight without q");
+    if (!k && (cached || k_out || k_weight)) return bad("block_tables, k_out or k_weight without k");
+    if (k && !cached && !k_out) return bad("keys need block_tables or k_out");
+    if (cached && (!v || !seq_idx || !pos)) return bad("a cache write needs v, seq_idx and pos");
+    if (cached && (max_blocks_per_seq <= 0 || n_table_rows <= 0))
+        return bad("n_table_rows and max_blocks_per_seq must be positive");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || !aligned16(angles))
+        return bad("rows, weights and angles must be 16-byte aligned");
+    for (const int64_t s : {q ? q_stride : 0, k ? k_stride : 0, cached ? v_stride : 0, q ? q_out_stride : 0, k_out ? k_out_stride : 0})
+        if (s < 0 || s % 8 || s > (1ll << 40)) return bad("strides must be multiples of 8 values, not negative");
+    if (n_tokens > 1 && ((q && q_out_stride < (int64_t)n_q_heads * D) || (k_out && k_out_stride < (int64_t)pool->n_kv_heads * D)))
+        return bad("the output rows of neighbouring tokens overlap");
+    if ((q_weight || k_weight) && !(eps >= 0.0f && eps <= FLT_MAX)) return bad("eps must be a number, not negative");
+    if (rot_dim < 0 || rot_dim > D) return bad("rot_dim must be in [0, head_dim]");
+    if (rot_dim % 16) return pkv::set_error(PF_ERR_UNSUPPORTED, "pf_norm_rope_write: rot_dim must be a multiple of 16");
+    if (rot_dim && (!angles || n_positions <= 0)) return bad("a rotation needs angles of n_positions > 0");
+    if (rot_dim && !rope_pos && !pos) return bad("a rotation needs rope_pos or pos");
+    pkv::NormRopeArgs a{pool, layer, q, q_stride, k, k_stride, cached ? v : nullptr, v_stride, n_tokens, n_q_heads,
+                        q_weight, k_weight, eps, angles, n_positions, rot_dim, (flags & PF_ROPE_INTERLEAVED) != 0,
+                        rope_pos, block_tables, n_table_rows, max_blocks_per_seq, seq_idx, pos, q_out, q_out_stride,
+                        k_out, k_out_stride};
+    return pkv::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
 }
 
 int pf_append_kv(const pf_pool *pool, int layer, const void *k_new, const void *v_new, const int32_t *block_tables,

@@ -112,6 +112,39 @@ struct AppendArgs {
 };
 int launch_append(const AppendArgs &a, cudaStream_t stream);
 
+// Norms, rotation and cache write of a layer's new rows (pf_norm_rope_write).
+// Strides in values between tokens.
+struct NormRopeArgs {
+    const pf_pool *pool;
+    int layer;
+    const void *q;           // null: no queries
+    long long q_stride;
+    const void *k;           // null: no keys (and no cache write)
+    long long k_stride;
+    const void *v;
+    long long v_stride;
+    int n_tokens;
+    int n_q_heads;
+    const float *q_weight;   // null: no norm
+    const float *k_weight;
+    float eps;
+    const float *angles;
+    int n_positions;
+    int rot_dim;
+    bool interleaved;
+    const int32_t *rope_pos;       // null: pos
+    const int32_t *block_tables;   // null: no cache write
+    int n_table_rows;
+    int max_blocks;
+    const int32_t *seq_idx;
+    const int32_t *pos;
+    void *q_out;
+    long long q_out_stride;
+    void *k_out;             // null: K goes to the cache only
+    long long k_out_stride;
+};
+int launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+
 // Whole-block copies: pool -> pool (both id arrays set), pool -> image
 // (dst_ids null: destination i is image i of `image`), image -> pool
 // (src_ids null).  Ids are device int32 arrays of n entries.
