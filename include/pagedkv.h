@@ -520,6 +520,56 @@ PF_API int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *
 PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                 int max_q_tokens);
 
+/* Sliding-window attention with sinks (no counterpart on the pages): as
+ * pf_paged_prefill_attention, but the query at position p sees of the tokens t
+ * <= p only the last `window` (t > p - window, its own among them) and the first
+ * n_sinks (t < n_sinks):
+ *   out[row][hq][d] = sum_t softmax_t(scale * q . K[slot(s, t)][h]) V[..][h][d]
+ * over those.  window >= 1, n_sinks >= 0 (either may be larger than the context).
+ * cu_q NULL: one query per sequence, row s, at position context_lens[s] - 1
+ * (max_new_tokens 1: a decode step); zeros where the context is empty.
+ * A block that holds only tokens that no query of the call sees is not the
+ * sequence's to keep: it may be freed, and its table entry may hold anything.
+ * Tokens of other blocks up to a sequence's last position have been written.
+ * Either pool type.  With a workspace (pf_window_workspace_bytes, initialised once
+ * with pf_decode_workspace_init, not shared by overlapping calls; one made for
+ * other windows will do) and at most 16 query rows (tokens x q-heads) per
+ * kv-head, the kernel and the roundings of pf_paged_cross_attention's few rows
+ * (fp32 output with the weights to about 22 bits); otherwise, and for fp16 output
+ * of small batches, the tcgen05 kernel, the weights rounded to fp16, which with a
+ * workspace cuts long windows of few blocks over the SMs.  A max_new_tokens above
+ * what the table holds counts as that. */
+PF_API int pf_paged_window_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                              int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q,
+                              int n_seqs, int max_new_tokens, int n_q_heads, float scale, int window, int n_sinks,
+                              void *out, int out_dtype, void *workspace, size_t ws_bytes, void *stream);
+/* Workspace bytes of pf_paged_window_attention for these sizes, or 0 when it
+ * needs none or on bad arguments (as pf_cross_workspace_bytes). */
+PF_API size_t pf_window_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                                 int max_new_tokens, int window, int n_sinks);
+
+/* Attention of drafted tokens that form a tree (no counterpart on the pages): the
+ * last n_s = cu_q[s + 1] - cu_q[s] tokens of sequence s, written into its pages
+ * like any others, are drafts 0 .. n_s - 1, at slots L - n_s + i (whatever the
+ * positions that they were rotated for); rows cu_q[s] + i of q are theirs.  A draft sees
+ * all L - n_s tokens before the drafts, and draft j where bit j % 64 of word
+ * tree[cu_q[s] + i][j / 64] is set: its ancestors and itself, or whatever the bits
+ * say (bits of j >= n_s do not count).  A draft that sees nothing gives zeros.
+ *   out[row][hq][d] = sum_t softmax_t(scale * q . K[slot(s, t)][h]) V[..][h][d]
+ * tree: device [T_q][tree_words], 8-byte aligned, 64 * tree_words at least
+ * max_draft_tokens, which bounds every n_s.  Arguments, pool types, kernels and
+ * roundings as pf_paged_window_attention (workspace: pf_tree_workspace_bytes).
+ * The rows of drafts that are kept are written again where they then belong
+ * (pf_write_kv, pf_norm_rope_write; 8-bit pools: pf_append_kv). */
+PF_API int pf_paged_tree_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                            int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q, int n_seqs,
+                            int max_draft_tokens, int n_q_heads, float scale, const uint64_t *tree,
+                            int tree_words, void *out, int out_dtype, void *workspace, size_t ws_bytes, void *stream);
+/* Workspace bytes of pf_paged_tree_attention for these sizes, or 0 when it needs
+ * none or on bad arguments (as pf_cross_workspace_bytes). */
+PF_API size_t pf_tree_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                               int max_draft_tokens);
+
 /* The decode attention call for callers that cannot allocate device memory.
  * No counterpart on the pages: it exists for code that may only touch the
  * buffers it is handed -- for instance an operator inside another runtime

@@ -24,7 +24,8 @@ from ._native import (  # noqa: F401
     pf_paged_prefill_attention, pf_prefill_workspace_bytes,
     pf_alloc_compact, pf_append_kv, pf_compact_blocks, pf_cross_workspace_bytes, pf_paged_cross_attention,
     pf_pool_bytes, pf_pool_create, pf_pool_create_e4m3, pf_scale_bytes,
-    pf_norm_rope_write,
+    pf_norm_rope_write, pf_paged_tree_attention, pf_paged_window_attention, pf_tree_workspace_bytes,
+    pf_window_workspace_bytes,
     pf_pool_destroy, pf_seq_release, pf_seq_reserve, pf_write_kv,
 )
 
@@ -46,6 +47,30 @@ def make_cross_workspace(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_q_toke
     pf_paged_cross_attention; None when it needs none."""
     import torch
     nbytes = pf_cross_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_q_tokens)
+    if nbytes == 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or pool.k_pool.device)
+    pf_decode_workspace_init(ws)
+    return ws
+
+
+def make_window_workspace(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, window, n_sinks=0, device=None):
+    """Allocate (with torch) and initialise a workspace for
+    pf_paged_window_attention; None when it needs none."""
+    import torch
+    nbytes = pf_window_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, window, n_sinks)
+    if nbytes == 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or pool.k_pool.device)
+    pf_decode_workspace_init(ws)
+    return ws
+
+
+def make_tree_workspace(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens, device=None):
+    """Allocate (with torch) and initialise a workspace for
+    pf_paged_tree_attention; None when it needs none."""
+    import torch
+    nbytes = pf_tree_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens)
     if nbytes == 0:
         return None
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device or pool.k_pool.device)

@@ -91,6 +91,10 @@ def lib():
         "pf_prefill_workspace_bytes": (Z, [P, I, I, I, I]),
         "pf_paged_cross_attention": (I, [P, I, P, P, I, P, P, I, I, I, F, P, I, P, Z, P]),
         "pf_cross_workspace_bytes": (Z, [P, I, I, I, I]),
+        "pf_paged_window_attention": (I, [P, I, P, P, I, P, P, I, I, I, F, I, I, P, I, P, Z, P]),
+        "pf_window_workspace_bytes": (Z, [P, I, I, I, I, I, I]),
+        "pf_paged_tree_attention": (I, [P, I, P, P, I, P, P, I, I, I, F, P, I, P, I, P, Z, P]),
+        "pf_tree_workspace_bytes": (Z, [P, I, I, I, I]),
         "pf_copy_blocks": (I, [P, P, P, I, P]),
         "pf_compact_blocks": (I, [P, P, P, I, P, P, I, I, P, P]),
         "pf_swap_out": (I, [P, P, I, P, P]),
@@ -489,6 +493,76 @@ def pf_paged_cross_attention(pool, layer, q, block_tables, context_lens, cu_q, m
         _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
         _dev_ptr(context_lens, "context_lens", torch.int32, dev),
         _dev_ptr(cu_q, "cu_q", torch.int32, dev), n, int(max_q_tokens), q.shape[1], float(scale),
+        _dev_ptr(out, "out", None, dev), out_dtype,
+        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+
+
+def _masked_args(pool, q, block_tables, context_lens, cu_q, out):
+    """Checked arguments that the masked attention calls share: the device, the
+    number of sequences, out's type code."""
+    import torch
+    n = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or (cu_q is not None and cu_q.numel() != n + 1):
+        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
+    if q.dim() != 3 or q.shape[2] != pool.head_dim or tuple(out.shape) != tuple(q.shape):
+        raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out of its shape")
+    if cu_q is None and q.shape[0] != n:
+        raise PagedKVError(PF_ERR_INVALID, "without cu_q, q must have a row per sequence")
+    out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
+    if out_dtype is None:
+        raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
+    return _pool_device(pool), n, out_dtype
+
+
+def pf_window_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, window, n_sinks=0):
+    """Workspace bytes of pf_paged_window_attention (0: it needs none)."""
+    return lib().pf_window_workspace_bytes(pool.handle, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens,
+                                           window, n_sinks)
+
+
+def pf_paged_window_attention(pool, layer, q, block_tables, context_lens, cu_q, max_new_tokens, scale, window, n_sinks,
+                              out, workspace=None, stream=None):
+    """Causal attention of each sequence's last tokens (q rows
+    cu_q[s]..cu_q[s+1]-1; cu_q None: one each, row s) over the last `window`
+    tokens up to the query's own and the first n_sinks."""
+    import torch
+    dev, n, out_dtype = _masked_args(pool, q, block_tables, context_lens, cu_q, out)
+    if q.numel() == 0:
+        return
+    _check(lib().pf_paged_window_attention(
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev),
+        None if cu_q is None else _dev_ptr(cu_q, "cu_q", torch.int32, dev), n, int(max_new_tokens), q.shape[1],
+        float(scale), int(window), int(n_sinks), _dev_ptr(out, "out", None, dev), out_dtype,
+        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+
+
+def pf_tree_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens):
+    """Workspace bytes of pf_paged_tree_attention (0: it needs none)."""
+    return lib().pf_tree_workspace_bytes(pool.handle, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens)
+
+
+def pf_paged_tree_attention(pool, layer, q, block_tables, context_lens, cu_q, max_draft_tokens, scale, tree, out,
+                            workspace=None, stream=None):
+    """Attention of each sequence's last tokens, drafts that form a tree: all see
+    the tokens before them, and draft j where bit j % 64 of the query's
+    tree[row, j // 64] is set (tree: int64 [T_q, words])."""
+    import torch
+    dev, n, out_dtype = _masked_args(pool, q, block_tables, context_lens, cu_q, out)
+    if cu_q is None:
+        raise PagedKVError(PF_ERR_INVALID, "cu_q must be given")
+    if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
+        raise PagedKVError(PF_ERR_INVALID, "tree must be [T_q, words], a row per query")
+    if q.numel() == 0:
+        return
+    _check(lib().pf_paged_tree_attention(
+        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
+        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
+        _dev_ptr(context_lens, "context_lens", torch.int32, dev), _dev_ptr(cu_q, "cu_q", torch.int32, dev), n,
+        int(max_draft_tokens), q.shape[1], float(scale), _dev_ptr(tree, "tree", torch.int64, dev), tree.shape[1],
         _dev_ptr(out, "out", None, dev), out_dtype,
         None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))

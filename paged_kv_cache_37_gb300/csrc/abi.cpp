@@ -346,7 +346,8 @@ static bool wide_rows(const pf_pool *pool, int rows) { return rows * pool->head_
 // (Fewer rows may take more: up to 8 run with 16 warps a CTA, more with 12.  The
 // prompt kernel's bytes, with which it cuts as far as it likes, are those of a
 // single sequence: a workspace serves smaller batches than its own.)
-static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads, int max_blocks, bool causal) {
+static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads, int max_blocks, bool causal,
+                                   const pkv::AttnMask &mask = {}) {
     const int group = n_q_heads / pool->n_kv_heads;
     size_t most = 0;
     for (int r = group; r <= rows; r += group) {
@@ -354,7 +355,7 @@ static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads,
         if (pkv::rows_plan(pool, r, false, &plan) != PF_OK) return 0;
         most = std::max(most, plan.bytes);
         if (wide_rows(pool, r))
-            most = std::max(most, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks, r / group));
+            most = std::max(most, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks, r / group, mask));
     }
     return most;
 }
@@ -362,9 +363,9 @@ static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads,
 // The same for calls on the prompt kernel alone: 0, or enough for calls of
 // fewer rows too.
 static size_t prompt_or_rows_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads,
-                                             int max_blocks, int max_tokens) {
-    const size_t bytes = pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks, max_tokens);
-    return bytes == 0 ? 0 : std::max(bytes, rows_workspace_bytes(pool, pkv::kMaxRows, n_q_heads, max_blocks, causal));
+                                             int max_blocks, int max_tokens, const pkv::AttnMask &mask = {}) {
+    const size_t bytes = pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks, max_tokens, mask);
+    return bytes == 0 ? 0 : std::max(bytes, rows_workspace_bytes(pool, pkv::kMaxRows, n_q_heads, max_blocks, causal, mask));
 }
 
 size_t pf_decode_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
@@ -398,6 +399,10 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
     return PF_OK;
 }
 
+// Whether the prompt kernel takes a call of few rows as causal: one query per
+// sequence without offsets sees the whole context, but for a mask.
+static bool prompt_causal(const pkv::RowsArgs &a) { return a.mask.kind != pkv::kMaskNone || (a.causal && a.cu_q); }
+
 // Whether a call of few rows takes the prompt kernel, whose blocks (one per
 // sequence and kv-head) need no partition and no merge, instead of a cut over
 // all SMs.  A wave of its blocks takes about 4 + steps microseconds, steps of
@@ -425,11 +430,13 @@ static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
     const long long waves = (items + a.plan.sms - 1) / a.plan.sms;
     const int step = a.pool->head_dim == 64 ? 128 : 64;
     long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
+    if (a.mask.kind == pkv::kMaskWindow)   // a block's: its sinks, and its window (and one of either is cut)
+        steps = std::min(steps, (a.mask.sinks + step - 1ll) / step + (a.mask.window + step - 1ll) / step + 1);
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
     if (!wide_rows(a.pool, a.rows)) return waves == 1 && steps <= 8;
     if (waves > 1) return waves == 2 && steps <= (a.rows * a.pool->head_dim > 1024 ? 8 : 4);
-    const int parts = pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
-                                         a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes);
+    const int parts = pkv::prompt_splits(a.pool, prompt_causal(a), a.n_seqs, a.n_q_heads, a.max_blocks,
+                                         a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes, a.mask);
     return steps <= 32 || parts > 1;
 }
 
@@ -449,7 +456,7 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
     if (prompt_kernel_pays(a, ws_bytes)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
-                           a.causal && a.cu_q, workspace, ws_bytes};
+                           prompt_causal(a), workspace, ws_bytes, a.mask};
         return pkv::launch_prefill_tc(b, static_cast<cudaStream_t>(stream));
     }
     a.workspace = workspace;
@@ -564,7 +571,8 @@ static int check_query_rows(const pf_pool *pool, int max_tokens, int n_q_heads, 
 
 // Hands the prompt kernel a workspace to cut contexts with, as many parts as fit.
 static int prompt_workspace(pkv::PrefillArgs &a, void *workspace, size_t ws_bytes, const char *fn) {
-    if (!workspace || (a.causal && a.pool->dtype == PF_F16)) return PF_OK;   // (causal fp16 contexts are not cut)
+    // (causal fp16 contexts are not cut, but under a mask)
+    if (!workspace || (a.causal && a.mask.kind == pkv::kMaskNone && a.pool->dtype == PF_F16)) return PF_OK;
     if (!aligned16(workspace))
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace must be 16-byte aligned");
     a.workspace = workspace;
@@ -729,6 +737,125 @@ int pf_paged_cross_attention(const pf_pool *pool, int layer, const void *q, cons
                        n_q_heads, scale, out, out_dtype, false};
     if ((rc = prompt_workspace(a, workspace, ws_bytes, "pf_paged_cross_attention")) != PF_OK) return rc;
     return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+}
+
+// Checks and launch that masked attention calls share; max_tokens bounds the
+// query tokens of a sequence.
+static int masked_call(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                       int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q, int n_seqs,
+                       int max_tokens, int n_q_heads, float scale, const pkv::AttnMask &mask, void *out, int out_dtype,
+                       void *workspace, size_t ws_bytes, const char *fn, void *stream) {
+    const auto bad = [fn](const char *what) { return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": " + what); };
+    if (!q || !block_tables || !context_lens || !out) return bad("null pointer");
+    if (!aligned16(q) || !aligned16(out)) return bad("q and out must be 16-byte aligned");
+    if (out_dtype != PF_F16 && out_dtype != PF_F32) return bad("out_dtype must be PF_F16 or PF_F32");
+    if (n_q_heads <= 0 || n_q_heads % pool->n_kv_heads) return bad("n_q_heads must be a positive multiple of n_kv_heads");
+    if (n_q_heads / pool->n_kv_heads > pkv::kMaxRows)
+        return pkv::set_error(PF_ERR_UNSUPPORTED, std::string(fn) + ": at most 16 q-heads per kv-head are built");
+    if (max_blocks_per_seq <= 0 || (long long)max_blocks_per_seq * pool->block_size > (1ll << 30))
+        return bad("bad max_blocks_per_seq");
+    if (!(scale > 0.0f)) return bad("scale must be a positive number");
+    // a loose bound: there are no more query tokens than the table holds
+    max_tokens = std::min(max_tokens, max_blocks_per_seq * pool->block_size);
+    int rc = check_query_rows(pool, max_tokens, n_q_heads, fn);
+    if (rc) return rc;
+    const int rows = cross_rows(pool, n_q_heads, max_tokens);
+    if (workspace != nullptr && rows > 0) {
+        pkv::RowsArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, n_q_heads,
+                        rows, true, scale, out, out_dtype, {}, nullptr, false, mask};
+        return rows_call(a, workspace, ws_bytes, fn, stream);
+    }
+    pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_tokens,
+                       n_q_heads, scale, out, out_dtype, true, nullptr, 0, mask};
+    if ((rc = prompt_workspace(a, workspace, ws_bytes, fn)) != PF_OK) return rc;
+    return pkv::launch_prefill_tc(a, static_cast<cudaStream_t>(stream));
+}
+
+// Their workspaces' bytes.
+static size_t masked_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                                     int max_tokens, const pkv::AttnMask &mask, const char *fn) {
+    if (!pool || n_seqs < 0 || max_blocks_per_seq <= 0 || max_tokens < 0) {
+        pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad arguments");
+        return 0;
+    }
+    max_tokens = (int)std::min<long long>(max_tokens, (long long)max_blocks_per_seq * pool->block_size);
+    const int rows = cross_rows(pool, n_q_heads, max_tokens);
+    if (rows == 0)   // the prompt kernel, which needs none but for long contexts cut over the SMs
+        return prompt_or_rows_workspace_bytes(pool, true, n_seqs, n_q_heads, max_blocks_per_seq, max_tokens, mask);
+    return rows_workspace_bytes(pool, rows, n_q_heads, max_blocks_per_seq, true, mask);
+}
+
+static bool window_mask(int window, int n_sinks, pkv::AttnMask *mask) {
+    if (window < 1 || n_sinks < 0) return false;
+    mask->kind = pkv::kMaskWindow;
+    mask->window = std::min(window, 1 << 30);   // no context is longer
+    mask->sinks = std::min(n_sinks, 1 << 30);
+    return true;
+}
+
+size_t pf_window_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                                 int max_new_tokens, int window, int n_sinks) {
+    pkv::clear_error();
+    pkv::AttnMask mask;
+    if (!window_mask(window, n_sinks, &mask)) {
+        pkv::set_error(PF_ERR_INVALID, "pf_window_workspace_bytes: window must be positive, n_sinks not negative");
+        return 0;
+    }
+    return masked_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, mask,
+                                  "pf_window_workspace_bytes");
+}
+
+int pf_paged_window_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                              int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q, int n_seqs,
+                              int max_new_tokens, int n_q_heads, float scale, int window, int n_sinks, void *out,
+                              int out_dtype, void *workspace, size_t ws_bytes, void *stream) {
+    pkv::clear_error();
+    const char *fn = "pf_paged_window_attention";
+    int rc = check_pool(pool, layer, fn);
+    if (rc) return rc;
+    if (n_seqs < 0 || max_new_tokens < 0)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_window_attention: negative n_seqs or max_new_tokens");
+    pkv::AttnMask mask;
+    if (!window_mask(window, n_sinks, &mask))
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_window_attention: window must be positive, n_sinks not negative");
+    if (n_seqs == 0 || max_new_tokens == 0) return PF_OK;
+    if (!cu_q && max_new_tokens != 1)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_window_attention: max_new_tokens must be 1 without cu_q");
+    return masked_call(pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_new_tokens,
+                       n_q_heads, scale, mask, out, out_dtype, workspace, ws_bytes, fn, stream);
+}
+
+size_t pf_tree_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+                               int max_draft_tokens) {
+    pkv::clear_error();
+    pkv::AttnMask mask;
+    mask.kind = pkv::kMaskTree;
+    return masked_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens, mask,
+                                  "pf_tree_workspace_bytes");
+}
+
+int pf_paged_tree_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
+                            int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q, int n_seqs,
+                            int max_draft_tokens, int n_q_heads, float scale, const uint64_t *tree, int tree_words,
+                            void *out, int out_dtype, void *workspace, size_t ws_bytes, void *stream) {
+    pkv::clear_error();
+    const char *fn = "pf_paged_tree_attention";
+    int rc = check_pool(pool, layer, fn);
+    if (rc) return rc;
+    if (n_seqs < 0 || max_draft_tokens < 0)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_tree_attention: negative n_seqs or max_draft_tokens");
+    if (n_seqs == 0 || max_draft_tokens == 0) return PF_OK;
+    if (!cu_q || !tree) return pkv::set_error(PF_ERR_INVALID, "pf_paged_tree_attention: null cu_q or tree");
+    if (reinterpret_cast<uintptr_t>(tree) & 7u)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_tree_attention: tree must be 8-byte aligned");
+    if (tree_words <= 0 || (long long)tree_words * 64 < max_draft_tokens)
+        return pkv::set_error(PF_ERR_INVALID, "pf_paged_tree_attention: tree_words holds no max_draft_tokens bits");
+    pkv::AttnMask mask;
+    mask.kind = pkv::kMaskTree;
+    mask.tree = tree;
+    mask.tree_words = tree_words;
+    return masked_call(pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_draft_tokens,
+                       n_q_heads, scale, mask, out, out_dtype, workspace, ws_bytes, fn, stream);
 }
 
 int pf_device_status(int *status_out, int reset, void *stream) {

@@ -164,6 +164,21 @@ struct BlockCopyArgs {
 };
 int launch_block_copy(const BlockCopyArgs &a, cudaStream_t stream);
 
+// What a query sees of its context, beside what a call's `causal` says.
+enum MaskKind {
+    kMaskNone = 0,
+    kMaskWindow = 1,   // of the tokens up to its position p: t > p - window or t < sinks
+    kMaskTree = 2      // the queries are the context's last tokens, drafts: all tokens before them,
+                       // and those drafts whose bits its row of the tree holds
+};
+struct AttnMask {
+    int kind = kMaskNone;
+    int window = 0;                   // 1 .. 2^30
+    int sinks = 0;                    // 0 .. 2^30
+    const uint64_t *tree = nullptr;   // [query token][tree_words]: bit j of word w for draft 64 w + j
+    int tree_words = 0;
+};
+
 // Multi-token attention (pf_paged_prefill_attention, pf_paged_cross_attention).
 struct PrefillArgs {
     const pf_pool *pool;
@@ -182,14 +197,16 @@ struct PrefillArgs {
     bool causal;   // the queries are the context's last tokens
     void *workspace = nullptr;   // for the parts of contexts cut over the SMs, or null: not cut
     size_t ws_bytes = 0;
+    AttnMask mask = {};          // (not none: causal)
 };
 // Parts that the prompt kernel cuts contexts of these sizes into with a
 // workspace of ws_bytes (1: none).
 int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms,
-                  size_t ws_bytes);
+                  size_t ws_bytes, const AttnMask &mask);
 // Bytes of that workspace for these sizes and for smaller batches, 0 if these
-// are not cut (or causal fp16).
-size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new);
+// are not cut (or causal fp16 without a mask).
+size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new,
+                              const AttnMask &mask);
 int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu (causal, fp16 pools)
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);   // prefill_tc.cu
 
@@ -250,6 +267,7 @@ struct RowsArgs {
     RowsPlan plan;
     void *workspace;
     bool after_append;     // the stream's previous kernel is this call's append
+    AttnMask mask = {};    // (not none: causal)
 };
 int launch_rows(const RowsArgs &a, cudaStream_t stream);
 

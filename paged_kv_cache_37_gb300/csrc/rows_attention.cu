@@ -18,11 +18,18 @@ int heads_per_team(int n_kv_heads) {
     return (n_kv_heads + groups - 1) / groups;
 }
 
-rows::Kernel kernel_for(const pf_pool *pool, int n_rows, bool f32) {
+rows::Kernel kernel_for(const pf_pool *pool, int n_rows, bool f32, int mask) {
     const bool paged = pool->block_size >= 16;
-    if (pool->dtype == PF_E4M3)
-        return pool->head_dim == 64 ? rows::kernel_e4m3_d64(n_rows, f32, paged) : rows::kernel_e4m3_d128(n_rows, f32, paged);
-    return pool->head_dim == 64 ? rows::kernel_f16_d64(n_rows, f32, paged) : rows::kernel_f16_d128(n_rows, f32, paged);
+    const bool d64 = pool->head_dim == 64;
+    const bool q8 = pool->dtype == PF_E4M3;
+    if (mask == kMaskWindow)
+        return q8 ? (d64 ? rows::kernel_e4m3_d64_window : rows::kernel_e4m3_d128_window)(n_rows, f32, paged)
+                  : (d64 ? rows::kernel_f16_d64_window : rows::kernel_f16_d128_window)(n_rows, f32, paged);
+    if (mask == kMaskTree)
+        return q8 ? (d64 ? rows::kernel_e4m3_d64_tree : rows::kernel_e4m3_d128_tree)(n_rows, f32, paged)
+                  : (d64 ? rows::kernel_f16_d64_tree : rows::kernel_f16_d128_tree)(n_rows, f32, paged);
+    return q8 ? (d64 ? rows::kernel_e4m3_d64 : rows::kernel_e4m3_d128)(n_rows, f32, paged)
+              : (d64 ? rows::kernel_f16_d64 : rows::kernel_f16_d128)(n_rows, f32, paged);
 }
 
 }  // namespace
@@ -51,7 +58,7 @@ int rows_plan(const pf_pool *pool, int n_rows, bool need_device, RowsPlan *plan,
     if (rc) return rc;
     plan->sms = sms;
     const int hg = heads_per_team(pool->n_kv_heads);
-    const size_t warps = (size_t)(kernel_for(pool, n_rows, false).warps / hg) * hg;   // of a CTA
+    const size_t warps = (size_t)(kernel_for(pool, n_rows, false, kMaskNone).warps / hg) * hg;   // of a CTA
     const size_t recs = warps * 2 * (size_t)n_rows * (size_t)(pool->head_dim + 4) * sizeof(float);
     const size_t room = (most < kWorkspaceFront ? 0 : most - kWorkspaceFront) / recs;
     plan->grid = (int)std::min(room, (size_t)std::min(sms, kFlagSms));
@@ -64,14 +71,14 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     const pf_pool *pool = a.pool;
     int *status = device_status_ptr();
     if (!status) return PF_ERR_CUDA;
-    const rows::Kernel k = kernel_for(pool, a.rows, a.out_dtype == PF_F32);
+    const rows::Kernel k = kernel_for(pool, a.rows, a.out_dtype == PF_F32, a.mask.kind);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "attention: cudaGetDevice");
     if (dev < 0 || dev >= kMaxDevices) return set_error(PF_ERR_UNSUPPORTED, "device index out of range");
     // once per device and kernel (setting it twice does no harm)
-    static std::atomic<bool> ready[kMaxDevices][32];
-    std::atomic<bool> &done = ready[dev][(pool->dtype == PF_E4M3) + 2 * (pool->head_dim == 64) + 4 * (a.rows <= 8) +
+    static std::atomic<bool> ready[kMaxDevices][3][32];
+    std::atomic<bool> &done = ready[dev][a.mask.kind][(pool->dtype == PF_E4M3) + 2 * (pool->head_dim == 64) + 4 * (a.rows <= 8) +
                                          8 * (a.out_dtype == PF_F32) + 16 * (pool->block_size >= 16)];
     if (!done.load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -102,6 +109,7 @@ int launch_rows(const RowsArgs &a, cudaStream_t stream) {
     p.out_f32 = a.out_dtype == PF_F32;
     p.layer_page0 = (long long)a.layer * pool->n_blocks;
     p.layer_row0 = p.layer_page0 * pool->block_size;
+    p.mask = a.mask;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     const size_t row = (size_t)a.n_q_heads * pool->head_dim;
     const size_t out_elem = a.out_dtype == PF_F32 ? 4 : 2;

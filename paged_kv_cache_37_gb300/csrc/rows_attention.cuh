@@ -6,7 +6,8 @@
 // For a (sequence s, kv-head h) with L tokens and at most 16 query rows (its
 // query tokens x its gh q-heads, row r = i * gh + g of token i):
 //   z_rt = scale * q_r . K_t,  out_r = sum_t softmax_t(z_r) V_t,
-// t < L (cross, decode) or t <= L - n + i (causal).  e4m3 pools: K_t = code *
+// t < L (cross, decode) or t <= L - n + i (causal), or what a window with sinks
+// or a tree of drafts leaves (MASK; internal.h).  e4m3 pools: K_t = code *
 // k_scale[page][h], V_t = code * v_scale[page][h].
 //
 // Floor: every K and V byte of the context is read once and used for at most 16
@@ -137,6 +138,7 @@ struct Params {
     long long layer_row0;   // layer * n_blocks * block_size
     long long layer_page0;  // layer * n_blocks
     float scale_log2;
+    AttnMask mask;
 };
 
 // PAGED: pages of 16 tokens and more, whose 16-token tiles lie in one page and
@@ -283,7 +285,12 @@ __device__ __forceinline__ int context_length(const Params &p, int s, bool flag)
     return L;
 }
 
-template <typename T, int D, int NT, bool HILO, bool PAGED>
+// MASK: a MaskKind.  A window's pair has the stages that hold a sink, then those
+// from the first token of its first query's window on; stage i of the pair is
+// stage i or i + skip of the context.  What no query of the pair sees is not
+// read: rows are zero-filled, and blocks that hold only such tokens are not
+// looked up.
+template <typename T, int D, int NT, bool HILO, bool PAGED, int MASK>
 __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_attention_kernel(const Params p) {
     using S = Shape<T, D, NT, PAGED>;
     constexpr int NW = S::NW;
@@ -298,6 +305,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ unsigned pre[kMaxSeqs + 1];   // units before sequence s
     __shared__ int len_sh[kMaxSeqs];
+    __shared__ int lo_sh[MASK == kMaskWindow ? kMaxSeqs : 1];   // first token that the first query sees by its window
     __shared__ unsigned warp_sum[32];
     __shared__ int warp_max[32];
     __shared__ Spans span_sh;
@@ -323,6 +331,15 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
             prefetch_l2(p.bt + (size_t)(e / lines) * p.max_blocks + e % lines * 32);
     }
 
+    constexpr bool WINDOW = MASK == kMaskWindow, TREE = MASK == kMaskTree;
+    // stages of a pair of sequence s (WINDOW: those with a sink of its L tokens, and the rest)
+    auto sink_stages = [&](int L) { return (min(p.mask.sinks, L) + ST - 1) / ST; };
+    auto n_stages = [&](int s) {
+        const int L = len_sh[s], n = (L + ST - 1) / ST;
+        if constexpr (WINDOW) return n - max(0, lo_sh[s] / ST - sink_stages(L));
+        else return n;
+    };
+
     // Prefix of the units over the sequences: each thread scans a run of
     // consecutive ones.
     {
@@ -334,8 +351,14 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         for (int s = s0; s < s1; ++s) {
             const int L = context_length(p, s, blockIdx.x == 0);
             len_sh[s] = L;
-            longest = max(longest, L);
-            if (L > 0) mine += ((unsigned)(L + ST - 1) / ST + kPairCost) * p.n_groups;
+            if constexpr (WINDOW) {
+                const int nq = p.cu_q ? min(p.cu_q[s + 1] - p.cu_q[s], p.rows / p.gh) : 1;
+                lo_sh[s] = max(0, L - nq - p.mask.window + 1);
+                longest = max(longest, n_stages(s) * ST);
+            } else {
+                longest = max(longest, L);
+            }
+            if (L > 0) mine += ((unsigned)n_stages(s) + kPairCost) * p.n_groups;
         }
         unsigned incl = mine;
 #pragma unroll
@@ -352,8 +375,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         unsigned at = __reduce_add_sync(FULL, lane < warp ? warp_sum[lane] : 0u) + incl - mine;
         for (int s = s0; s < s1; ++s) {
             pre[s] = at;
-            const int L = len_sh[s];
-            if (L > 0) at += ((unsigned)(L + ST - 1) / ST + kPairCost) * p.n_groups;
+            if (len_sh[s] > 0) at += ((unsigned)n_stages(s) + kPairCost) * p.n_groups;
         }
         if (warp == NW - 1) {
             longest = __reduce_max_sync(FULL, lane < NW ? warp_max[lane] : 0);
@@ -409,7 +431,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         // the last sequence with pre <= x: of 32 samples, then of 32 entries
         const int top = 32 * (__popc(__ballot_sync(FULL, lane * 32 < p.n_seqs && pre[lane * 32] <= x)) - 1);
         s = top + __popc(__ballot_sync(FULL, top + lane < p.n_seqs && pre[top + lane] <= x)) - 1;
-        per = (unsigned)(len_sh[s] + ST - 1) / ST + kPairCost;
+        per = (unsigned)n_stages(s) + kPairCost;
         const unsigned d = x - pre[s];
         g = (int)(d / per);
         return d - (unsigned)g * per;
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                 c.g = 0;
             }
             if (c.s >= p.n_seqs) return;
-            c.n_tiles = (len_sh[c.s] + ST - 1) / ST;
+            c.n_tiles = n_stages(c.s);
             const unsigned ub = pre[c.s] + (unsigned)c.g * (c.n_tiles + kPairCost) + kPairCost;   // its first stage
             if (ub >= u_hi) {
                 c.s = p.n_seqs;
@@ -482,6 +504,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     // U; otherwise that of token l mod ST (-2: no such token).
     struct Ahead {
         int id, tok0, h, n;              // first token, kv-head, tokens (0: nothing to copy)
+        int lo, sinks;                   // WINDOW: of these the first, and those from lo on, are seen
     };
     Ahead ahead[PF];
     auto look_up = [&](Ahead &a) {
@@ -491,9 +514,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
         a.h = look.g * p.hg + hl;
         if (a.h < p.n_kv_heads) {        // the last group may have fewer heads
             const int L = len_sh[look.s];
+            if constexpr (WINDOW) {
+                if (look.tile >= sink_stages(L)) a.tok0 += ((L + ST - 1) / ST - look.n_tiles) * ST;
+                a.lo = lo_sh[look.s] - a.tok0;
+                a.sinks = p.mask.sinks - a.tok0;
+            }
             a.n = min(ST, L - a.tok0);
-            const int t = a.tok0 + (PAGED ? ((lane >> 1) & (U - 1)) * 16 : (lane & (ST - 1)));
-            a.id = t < L ? p.bt[(size_t)look.s * p.max_blocks + (PAGED ? t >> p.block_shift : t)] : -2;
+            const int i = PAGED ? ((lane >> 1) & (U - 1)) * 16 : (lane & (ST - 1)), t = a.tok0 + i;
+            bool seen = t < L;
+            if constexpr (WINDOW) seen = seen && (i + (PAGED ? 15 : 0) >= a.lo || i < a.sinks);
+            a.id = seen ? p.bt[(size_t)look.s * p.max_blocks + (PAGED ? t >> p.block_shift : t)] : -2;
         }
         advance(look);
     };
@@ -507,15 +537,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                     const int id = __shfl_sync(FULL, a.id, 2 * u);
                     int left = a.n - 16 * u;
                     if ((unsigned)id >= (unsigned)p.n_blocks) {
-                        if (left > 0 && lane == 0) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                        if (left > 0 && lane == 0 && !(WINDOW && id == -2)) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
                         left = 0;
                     }
+                    const bool whole = left >= 16 && (!WINDOW || 16 * u >= a.lo || 16 * u + 16 <= a.sinks);
                     const uint32_t kd = k_at + base + u * 16 * RB, vd = v_at + base + u * 16 * RB;
                     const unsigned row = (unsigned)p.layer_row0 + (unsigned)id * (unsigned)p.block_size +
                                          (unsigned)((a.tok0 + 16 * u) & (p.block_size - 1));   // below 2^31
                     const size_t at = (size_t)row * tok_bytes + (unsigned)(a.h * RB);
                     const uint8_t *ks = k_lane + at, *vs = v_lane + at;
-                    if (left >= 16) {
+                    if (whole) {
 #pragma unroll
                         for (int i = 0; i < 16 / TI; ++i) {
                             cp16(kd + i * KSTEP * RB, ks, 16u);
@@ -523,10 +554,12 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                             ks += TI * tok_bytes;
                             vs += TI * tok_bytes;
                         }
-                    } else {   // rows past the context: zeros
+                    } else {   // rows past the context (that no query sees): zeros
 #pragma unroll 1
                         for (int i = 0; i < 16 / TI; ++i) {
-                            const uint32_t n = i * TI + lane / CPR < left ? 16u : 0u;
+                            const int row_i = i * TI + lane / CPR;
+                            const bool seen = !WINDOW || 16 * u + row_i >= a.lo || 16 * u + row_i < a.sinks;
+                            const uint32_t n = row_i < left && seen ? 16u : 0u;
                             cp16(kd + i * KSTEP * RB, n ? ks : p.k_pool, n);
                             cp16((vd ^ v_xor(i)) + i * TI * RB, n ? vs : p.v_pool, n);
                             ks += TI * tok_bytes;
@@ -630,10 +663,30 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * tq + e;
-                vis[nt][e] = p.causal && nq > 1 && r < n_rows ? max(0, L - nq + r / p.gh + 1) : L;
+                vis[nt][e] = !TREE && p.causal && nq > 1 && r < n_rows ? max(0, L - nq + r / p.gh + 1) : L;
             }
         }
-        if (p.causal) vis_min = max(0, L - nq + 1);
+        if (p.causal) vis_min = max(0, L - nq + (TREE ? 0 : 1));
+        int first_window = 0, skip = 0;  // WINDOW: the pair's first stage by the window, and how far it is moved
+        int lo_max = 0;                  // the first token that the last query sees by its window
+        if constexpr (WINDOW) {
+            first_window = sink_stages(L);
+            skip = (L + ST - 1) / ST - n_tiles;
+            lo_max = L - p.mask.window;
+        }
+        uint32_t drafts[NT][2];          // TREE: those that rows 2 tq, 2 tq + 1 see
+        if constexpr (TREE) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nt * 8 + 2 * tq + e;
+                    drafts[nt][e] = r < n_rows ? (uint32_t)p.mask.tree[(size_t)(q0 + r / p.gh) * p.mask.tree_words] &
+                                                     ((1u << nq) - 1u)
+                                               : 0u;
+                }
+            }
+        }
 
         float m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
@@ -726,8 +779,34 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                     }
                 }
             }
-            const int tok0 = tile * ST;
-            if (tok0 + ST > vis_min) {   // the context's end, or a causal limit
+            const int tok0 = (tile + (WINDOW && tile >= first_window ? skip : 0)) * ST;
+            if constexpr (WINDOW) {      // before the window of some row, and no sink
+                if (tok0 < lo_max && tok0 + ST > p.mask.sinks) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int t = tok0 + u * 16 + (e >> 1) * SLOT8 + tslot;
+                                if (t < vis[nt][e & 1] - p.mask.window && t >= p.mask.sinks) z[u][nt][e] = -INFINITY;
+                            }
+                }
+            }
+            if constexpr (TREE) {
+                if (tok0 + ST > vis_min) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int d = tok0 + u * 16 + (e >> 1) * SLOT8 + tslot - (L - nq);   // draft
+                                if (d >= 0 && (d >= 32 || !(drafts[nt][e & 1] >> (d & 31) & 1u))) z[u][nt][e] = -INFINITY;
+                            }
+                }
+            }
+            if (!TREE && tok0 + ST > vis_min) {   // the context's end, or a causal limit
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -869,8 +948,9 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
             bool ok[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                f[nt][0] = vs / l[nt][0];
-                f[nt][1] = vs / l[nt][1];
+                // (a draft may see nothing at all: zeros)
+                f[nt][0] = TREE && l[nt][0] == 0.0f ? 0.0f : vs / l[nt][0];
+                f[nt][1] = TREE && l[nt][1] == 0.0f ? 0.0f : vs / l[nt][1];
                 const int r = nt * 8 + 2 * tq + (gq & 1);
                 const int i = nq > 1 ? r / p.gh : 0;
                 ok[nt] = r < n_rows;
@@ -912,7 +992,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     unsigned ub = 0, team0 = 0;          // the pair that began earlier: first stage's unit, first team
     bool ends = false;                   // its last part is here
     if (cut.x >= 0) {
-        const unsigned n_tiles = (unsigned)(len_sh[cut.x] + ST - 1) / ST;
+        const unsigned n_tiles = (unsigned)n_stages(cut.x);
         ub = pre[cut.x] + (unsigned)cut.y * (n_tiles + kPairCost) + kPairCost;
         ends = ub + n_tiles <= u_hi;
     }
@@ -1077,7 +1157,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                     continue;
                 }
                 const int j = nq > 1 ? row[i] / p.gh : 0;
-                const float f = 1.0f / sum_l[row[i]];
+                const float f = TREE && sum_l[row[i]] == 0.0f ? 0.0f : 1.0f / sum_l[row[i]];
                 const size_t o = ((size_t)(q0 + j) * p.n_q_heads + (size_t)h * p.gh + row[i] - j * p.gh) * D + d4;
                 if (p.out_f32)
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + o) =
@@ -1111,21 +1191,30 @@ struct Kernel {
     int smem;
     int warps;
 };
-template <typename T, int D, int NT, bool PAGED>
+template <typename T, int D, int MASK, int NT, bool PAGED>
 Kernel instance(bool f32) {
-    return {f32 ? rows_attention_kernel<T, D, NT, true, PAGED> : rows_attention_kernel<T, D, NT, false, PAGED>,
+    return {f32 ? rows_attention_kernel<T, D, NT, true, PAGED, MASK> : rows_attention_kernel<T, D, NT, false, PAGED, MASK>,
             Shape<T, D, NT, PAGED>::SMEM, Shape<T, D, NT, PAGED>::NW};
 }
-template <typename T, int D>
+template <typename T, int D, int MASK = kMaskNone>
 Kernel pick(int n_rows, bool f32, bool paged) {
-    if (n_rows <= 8) return paged ? instance<T, D, 1, true>(f32) : instance<T, D, 1, false>(f32);
-    return paged ? instance<T, D, 2, true>(f32) : instance<T, D, 2, false>(f32);
+    if (n_rows <= 8) return paged ? instance<T, D, MASK, 1, true>(f32) : instance<T, D, MASK, 1, false>(f32);
+    return paged ? instance<T, D, MASK, 2, true>(f32) : instance<T, D, MASK, 2, false>(f32);
 }
-// one file each: rows_attention_<type>_d<head_dim>.cu
+// one file each: rows_attention_<type>_d<head_dim>.cu, and with a mask
+// rows_attention_<type>_d<head_dim>_<mask>.cu
 Kernel kernel_e4m3_d64(int n_rows, bool f32, bool paged);
 Kernel kernel_e4m3_d128(int n_rows, bool f32, bool paged);
 Kernel kernel_f16_d64(int n_rows, bool f32, bool paged);
 Kernel kernel_f16_d128(int n_rows, bool f32, bool paged);
+Kernel kernel_e4m3_d64_window(int n_rows, bool f32, bool paged);
+Kernel kernel_e4m3_d128_window(int n_rows, bool f32, bool paged);
+Kernel kernel_f16_d64_window(int n_rows, bool f32, bool paged);
+Kernel kernel_f16_d128_window(int n_rows, bool f32, bool paged);
+Kernel kernel_e4m3_d64_tree(int n_rows, bool f32, bool paged);
+Kernel kernel_e4m3_d128_tree(int n_rows, bool f32, bool paged);
+Kernel kernel_f16_d64_tree(int n_rows, bool f32, bool paged);
+Kernel kernel_f16_d128_tree(int n_rows, bool f32, bool paged);
 
 }  // namespace rows
 }  // namespace pkv

@@ -1,0 +1,12 @@
+// rows_attention_f16_d128_tree.cu -- instances of rows_attention.cuh: fp16 pools, head_dim 128, a tree of drafts.
+#include "rows_attention.cuh"
+
+namespace pkv {
+namespace rows {
+
+Kernel kernel_f16_d128_tree(int n_rows, bool f32, bool paged) {
+    return pick<__half, 128, kMaskTree>(n_rows, f32, paged);
+}
+
+}  // namespace rows
+}  // namespace pkv
