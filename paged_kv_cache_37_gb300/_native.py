@@ -132,10 +132,11 @@ def _check(rc):
 def _dev_ptr(t, name, dtype=None, dev=None):
     """Address of a contiguous CUDA tensor, on device dev if given (an int: what
     ctypes takes for a pointer argument without a wrapper object)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if dev is None or t.get_device() != dev:
+    try:
+        on = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    if dev is None or on != dev:
         if not t.is_cuda:
             raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
         if dev is not None:
@@ -147,23 +148,23 @@ def _dev_ptr(t, name, dtype=None, dev=None):
     return t.data_ptr()
 
 
-def _rows_ptr(t, name, heads, head_dim, dev):
+def _rows_ptr(t, name, shape, dev, float16):
     """Address and stride between tokens (in values) of fp16 rows [T, heads,
-    head_dim] whose heads are contiguous and tokens any distance apart."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
-        raise PagedKVError(PF_ERR_INVALID, f"{name} must be [n_tokens, {heads}, {head_dim}]")
-    if not t.is_cuda:
-        raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
+    head_dim] on device dev, heads contiguous and tokens any distance apart."""
+    if t.shape != shape:
+        raise PagedKVError(PF_ERR_INVALID, f"{name} must have {shape[0]} rows of [{shape[1]}, {shape[2]}]")
     if t.get_device() != dev:
+        if not t.is_cuda:
+            raise PagedKVError(PF_ERR_INVALID, f"{name} must be a CUDA tensor")
         raise PagedKVError(PF_ERR_INVALID, f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if t.dtype != torch.float16:
-        raise PagedKVError(PF_ERR_INVALID, f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    if t.dtype is not float16:
+        raise PagedKVError(PF_ERR_INVALID, f"{name} must be {float16}, got {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
+    apart, head, one = t.stride()
+    if one != 1 or (shape[1] > 1 and head != shape[2]):
         raise PagedKVError(PF_ERR_INVALID, f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return t.data_ptr(), apart if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _stream_ptr(stream):
@@ -601,47 +602,66 @@ def pf_norm_rope_write(pool, layer, q, k, v, block_tables, seq_idx, pos, angles,
     block_tables nothing is cached and k_out takes the keys; q or k None: only the
     other."""
     import torch
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
     dev = _pool_device(pool)
-    D = pool.head_dim
     first = k if q is None else q
     if first is None:
         raise PagedKVError(PF_ERR_INVALID, "neither queries nor keys")
-    n = first.shape[0]
-    for t, name in ((k, "k"), (v, "v"), (q_out, "q_out"), (k_out, "k_out")):
-        if t is not None and t.shape[0] != n:
-            raise PagedKVError(PF_ERR_INVALID, f"{name} must have {n} rows")
+    if first.dim() != 3:
+        raise PagedKVError(PF_ERR_INVALID, "q and k must be [n_tokens, heads, head_dim]")
+    n, hq, D = first.shape
+    if D != pool.head_dim:
+        raise PagedKVError(PF_ERR_INVALID, f"q and k must have head_dim {pool.head_dim}")
     if (q is None) != (q_out is None):
         raise PagedKVError(PF_ERR_INVALID, "q needs q_out, and q_out q")
-    hq = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise PagedKVError(PF_ERR_INVALID, "q must be [n_tokens, n_q_heads, head_dim]")
-        hq = q.shape[1]
-    for t, name in ((seq_idx, "seq_idx"), (pos, "pos"), (rope_pos, "rope_pos")):
-        if t is not None and t.numel() != n:
-            raise PagedKVError(PF_ERR_INVALID, f"{name} must have n_tokens entries")
-    if block_tables is not None and block_tables.dim() != 2:
-        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
-    if angles is not None and angles.dim() != 2:
-        raise PagedKVError(PF_ERR_INVALID, "angles must be [n_positions, rot_dim]")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and tuple(t.shape) != (D,):
-            raise PagedKVError(PF_ERR_INVALID, f"{name} must be [head_dim]")
-
-    def rows(t, name, heads):
-        return (None, 0) if t is None else _rows_ptr(t, name, heads, D, dev)
-
-    def flat(t, name, dtype):
-        return None if t is None else _dev_ptr(t, name, dtype, dev)
+    keys = (n, pool.n_kv_heads, D)
+    q_ptr = k_ptr = v_ptr = q_to = k_to = w_q = w_k = ang = rp = bt = seq = at = None
+    q_apart = k_apart = v_apart = q_to_apart = k_to_apart = n_positions = rot = rows = width = 0
+    if q is None:
+        hq = 0
+    else:
+        q_ptr, q_apart = _rows_ptr(q, "q", (n, hq, D), dev, f16)
+        q_to, q_to_apart = _rows_ptr(q_out, "q_out", (n, hq, D), dev, f16)
+    if k is not None:
+        k_ptr, k_apart = _rows_ptr(k, "k", keys, dev, f16)
+    if v is not None:
+        v_ptr, v_apart = _rows_ptr(v, "v", keys, dev, f16)
+    if k_out is not None:
+        k_to, k_to_apart = _rows_ptr(k_out, "k_out", keys, dev, f16)
+    if q_weight is not None:
+        if q_weight.numel() != D:
+            raise PagedKVError(PF_ERR_INVALID, "q_weight must be [head_dim]")
+        w_q = _dev_ptr(q_weight, "q_weight", f32, dev)
+    if k_weight is not None:
+        if k_weight.numel() != D:
+            raise PagedKVError(PF_ERR_INVALID, "k_weight must be [head_dim]")
+        w_k = _dev_ptr(k_weight, "k_weight", f32, dev)
+    if angles is not None:
+        if angles.dim() != 2:
+            raise PagedKVError(PF_ERR_INVALID, "angles must be [n_positions, rot_dim]")
+        n_positions, rot = angles.shape
+        ang = _dev_ptr(angles, "angles", f32, dev)
+    if rope_pos is not None:
+        if rope_pos.numel() != n:
+            raise PagedKVError(PF_ERR_INVALID, "rope_pos must have n_tokens entries")
+        rp = _dev_ptr(rope_pos, "rope_pos", i32, dev)
+    if block_tables is not None:
+        if block_tables.dim() != 2:
+            raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
+        rows, width = block_tables.shape
+        bt = _dev_ptr(block_tables, "block_tables", i32, dev)
+    if seq_idx is not None:
+        if seq_idx.numel() != n:
+            raise PagedKVError(PF_ERR_INVALID, "seq_idx must have n_tokens entries")
+        seq = _dev_ptr(seq_idx, "seq_idx", i32, dev)
+    if pos is not None:
+        if pos.numel() != n:
+            raise PagedKVError(PF_ERR_INVALID, "pos must have n_tokens entries")
+        at = _dev_ptr(pos, "pos", i32, dev)
     _check(lib().pf_norm_rope_write(
-        pool.handle, layer, *rows(q, "q", hq), *rows(k, "k", pool.n_kv_heads), *rows(v, "v", pool.n_kv_heads), n, hq,
-        flat(q_weight, "q_weight", torch.float32), flat(k_weight, "k_weight", torch.float32), float(eps),
-        flat(angles, "angles", torch.float32), 0 if angles is None else angles.shape[0],
-        0 if angles is None else angles.shape[1], PF_ROPE_INTERLEAVED if interleaved else 0,
-        flat(rope_pos, "rope_pos", torch.int32), flat(block_tables, "block_tables", torch.int32),
-        0 if block_tables is None else block_tables.shape[0], 0 if block_tables is None else block_tables.shape[1],
-        flat(seq_idx, "seq_idx", torch.int32), flat(pos, "pos", torch.int32), *rows(q_out, "q_out", hq),
-        *rows(k_out, "k_out", pool.n_kv_heads), _stream_ptr(stream)))
+        pool.handle, layer, q_ptr, q_apart, k_ptr, k_apart, v_ptr, v_apart, n, hq, w_q, w_k, eps, ang, n_positions,
+        rot, PF_ROPE_INTERLEAVED if interleaved else 0, rp, bt, rows, width, seq, at, q_to, q_to_apart, k_to,
+        k_to_apart, _stream_ptr(stream)))
 
 
 def pf_write_kv(pool, layer, k_new, v_new, block_tables, seq_idx, pos, stream=None):

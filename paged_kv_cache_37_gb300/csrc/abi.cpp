@@ -108,7 +108,7 @@ static int pool_create(pf_pool **out, void *k_base, void *v_base, float *k_scale
     p->dtype = dtype;
     for (int i = 0; i < pkv::kMaxDevices; ++i) {
         for (int j = 0; j < 6; ++j) p->tmap_ready[i][j] = false;
-        p->tmap_pf_ready[i] = false;
+        p->tmap_pf_ready[i][0] = p->tmap_pf_ready[i][1] = false;
     }
     *out = p;
     return PF_OK;
@@ -355,7 +355,9 @@ static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads,
         if (pkv::rows_plan(pool, r, false, &plan) != PF_OK) return 0;
         most = std::max(most, plan.bytes);
         if (wide_rows(pool, r))
-            most = std::max(most, pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks, r / group, mask));
+            most = std::max(most, mask.kind == pkv::kMaskNone
+                                      ? pkv::prompt_workspace_bytes(pool, causal, 1, n_q_heads, max_blocks, r / group)
+                                      : pkv::masked_workspace_bytes(pool, mask, 1, n_q_heads, max_blocks, r / group));
     }
     return most;
 }
@@ -364,7 +366,9 @@ static size_t rows_workspace_bytes(const pf_pool *pool, int rows, int n_q_heads,
 // fewer rows too.
 static size_t prompt_or_rows_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads,
                                              int max_blocks, int max_tokens, const pkv::AttnMask &mask = {}) {
-    const size_t bytes = pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks, max_tokens, mask);
+    const size_t bytes = mask.kind == pkv::kMaskNone
+                             ? pkv::prompt_workspace_bytes(pool, causal, n_seqs, n_q_heads, max_blocks, max_tokens)
+                             : pkv::masked_workspace_bytes(pool, mask, n_seqs, n_q_heads, max_blocks, max_tokens);
     return bytes == 0 ? 0 : std::max(bytes, rows_workspace_bytes(pool, pkv::kMaxRows, n_q_heads, max_blocks, causal, mask));
 }
 
@@ -399,10 +403,6 @@ int pf_decode_workspace_init(void *workspace, size_t ws_bytes, void *stream) {
     return PF_OK;
 }
 
-// Whether the prompt kernel takes a call of few rows as causal: one query per
-// sequence without offsets sees the whole context, but for a mask.
-static bool prompt_causal(const pkv::RowsArgs &a) { return a.mask.kind != pkv::kMaskNone || (a.causal && a.cu_q); }
-
 // Whether a call of few rows takes the prompt kernel, whose blocks (one per
 // sequence and kv-head) need no partition and no merge, instead of a cut over
 // all SMs.  A wave of its blocks takes about 4 + steps microseconds, steps of
@@ -435,8 +435,11 @@ static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
     if (!wide_rows(a.pool, a.rows)) return waves == 1 && steps <= 8;
     if (waves > 1) return waves == 2 && steps <= (a.rows * a.pool->head_dim > 1024 ? 8 : 4);
-    const int parts = pkv::prompt_splits(a.pool, prompt_causal(a), a.n_seqs, a.n_q_heads, a.max_blocks,
-                                         a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes, a.mask);
+    const int tokens = a.rows / (a.n_q_heads / a.pool->n_kv_heads);
+    const int parts = a.mask.kind == pkv::kMaskNone
+                          ? pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks, tokens,
+                                               a.plan.sms, ws_bytes)
+                          : pkv::masked_splits(a.pool, a.mask, a.n_seqs, a.n_q_heads, a.max_blocks, tokens, a.plan.sms, ws_bytes);
     return steps <= 32 || parts > 1;
 }
 
@@ -456,8 +459,9 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
     if (prompt_kernel_pays(a, ws_bytes)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
-                           prompt_causal(a), workspace, ws_bytes, a.mask};
-        return pkv::launch_prefill_tc(b, static_cast<cudaStream_t>(stream));
+                           a.causal && a.cu_q, workspace, ws_bytes, a.mask};
+        return a.mask.kind == pkv::kMaskNone ? pkv::launch_prefill_tc(b, static_cast<cudaStream_t>(stream))
+                                             : pkv::launch_prompt_masked(b, static_cast<cudaStream_t>(stream));
     }
     a.workspace = workspace;
     return pkv::launch_rows(a, static_cast<cudaStream_t>(stream));
@@ -768,11 +772,11 @@ static int masked_call(const pf_pool *pool, int layer, const void *q, const int3
     pkv::PrefillArgs a{pool, layer, q, block_tables, max_blocks_per_seq, context_lens, cu_q, n_seqs, max_tokens,
                        n_q_heads, scale, out, out_dtype, true, nullptr, 0, mask};
     if ((rc = prompt_workspace(a, workspace, ws_bytes, fn)) != PF_OK) return rc;
-    return pkv::launch_prefill_tc(a, static_cast<cudaStream_t>(stream));
+    return pkv::launch_prompt_masked(a, static_cast<cudaStream_t>(stream));
 }
 
 // Their workspaces' bytes.
-static size_t masked_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
+static size_t masked_call_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, int max_blocks_per_seq,
                                      int max_tokens, const pkv::AttnMask &mask, const char *fn) {
     if (!pool || n_seqs < 0 || max_blocks_per_seq <= 0 || max_tokens < 0) {
         pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": bad arguments");
@@ -801,7 +805,7 @@ size_t pf_window_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads,
         pkv::set_error(PF_ERR_INVALID, "pf_window_workspace_bytes: window must be positive, n_sinks not negative");
         return 0;
     }
-    return masked_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, mask,
+    return masked_call_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, mask,
                                   "pf_window_workspace_bytes");
 }
 
@@ -830,7 +834,7 @@ size_t pf_tree_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_heads, i
     pkv::clear_error();
     pkv::AttnMask mask;
     mask.kind = pkv::kMaskTree;
-    return masked_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens, mask,
+    return masked_call_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens, mask,
                                   "pf_tree_workspace_bytes");
 }
 

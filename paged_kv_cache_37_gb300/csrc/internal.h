@@ -65,11 +65,12 @@ struct pf_pool {
     bool tmap_ready[pkv::kMaxDevices][6];
     CUtensorMap tmap_k[pkv::kMaxDevices][6];
     CUtensorMap tmap_v[pkv::kMaxDevices][6];
-    // per device: the prompt kernel's boxes (one 64-element half of up to a
-    // page of rows of one kv-head, swizzled)
-    bool tmap_pf_ready[pkv::kMaxDevices];
-    CUtensorMap tmap_pf_k[pkv::kMaxDevices];
-    CUtensorMap tmap_pf_v[pkv::kMaxDevices];
+    // per device: the prompt kernels' boxes (one 64-element half of up to a
+    // page of rows of one kv-head, swizzled), at most a tile of prefill_tc.cu, and
+    // at most a tile of prompt_masked.cuh
+    bool tmap_pf_ready[pkv::kMaxDevices][2];
+    CUtensorMap tmap_pf_k[pkv::kMaxDevices][2];
+    CUtensorMap tmap_pf_v[pkv::kMaxDevices][2];
 };
 
 namespace pkv {
@@ -202,13 +203,19 @@ struct PrefillArgs {
 // Parts that the prompt kernel cuts contexts of these sizes into with a
 // workspace of ws_bytes (1: none).
 int prompt_splits(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new, int sms,
-                  size_t ws_bytes, const AttnMask &mask);
+                  size_t ws_bytes);
 // Bytes of that workspace for these sizes and for smaller batches, 0 if these
-// are not cut (or causal fp16 without a mask).
-size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new,
-                              const AttnMask &mask);
+// are not cut (or causal fp16).
+size_t prompt_workspace_bytes(const pf_pool *pool, bool causal, int n_seqs, int n_q_heads, int max_blocks, int max_new);
 int launch_prefill(const PrefillArgs &a, cudaStream_t stream);   // prefill_mma.cu (causal, fp16 pools)
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);   // prefill_tc.cu
+// fp16 pools: the boxes of prompt kernel `which`, of box_rows rows, on first use.
+int encode_prompt_tmaps(pf_pool *pool, int dev, int which, int box_rows);
+// The same under a mask (prompt_masked.cu).
+int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new,
+                  int sms, size_t ws_bytes);
+size_t masked_workspace_bytes(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new);
+int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream);
 
 struct GatherArgs {
     const pf_pool *pool;

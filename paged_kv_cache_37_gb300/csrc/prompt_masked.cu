@@ -1,0 +1,152 @@
+// prompt_masked.cu -- host side of prompt_masked.cuh: how contexts are cut, the
+// workspace and the launches.
+#include <algorithm>
+#include <atomic>
+
+#include "prompt_masked.cuh"
+
+namespace pkv {
+namespace {
+
+int tile_tokens(const pf_pool *pool) {
+    return pool->head_dim == 64 ? prompt_masked::Cfg<64, false>::BN : prompt_masked::Cfg<128, false>::BN;
+}
+
+// Rows that are looked up and copied together: what a page holds of a tile (the
+// TMA boxes of fp16 pools), 16 of e4m3 pages.
+int unit_rows(const pf_pool *pool) {
+    if (pool->block_size < 16) return 1;
+    return pool->dtype == PF_E4M3 ? 16 : std::min(pool->block_size, tile_tokens(pool));
+}
+
+// Workspace of a block's part.
+size_t part_bytes(const pf_pool *pool) {
+    return (size_t)prompt_masked::ROWS * (pool->head_dim + 2) * sizeof(float);
+}
+
+}  // namespace
+
+// Parts that contexts are cut into: as many as give every SM a block, of at
+// least kMinTiles tiles at the table's longest context (a window's), if that
+// pays: prompt_splits has both sides, and the same costs.
+int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new,
+                  int sms, size_t ws_bytes) {
+    const long long group = n_q_heads / pool->n_kv_heads, all_rows = max_new * group;
+    const long long blocks = (long long)n_seqs * pool->n_kv_heads * ((all_rows + prompt_masked::ROWS - 1) / prompt_masked::ROWS);
+    if (blocks <= 0) return 1;
+    long long tokens = (long long)max_blocks * pool->block_size;
+    if (mask.kind == kMaskWindow)   // of a block: its sinks, and its rows' windows
+        tokens = std::min(tokens, (long long)mask.sinks + mask.window + std::min<long long>(max_new, prompt_masked::ROWS / group + 1) +
+                                      2 * unit_rows(pool));
+    const long long tiles = (tokens + tile_tokens(pool) - 1) / tile_tokens(pool);
+    const long long room = ws_bytes < kWorkspaceFront ? 0 : (long long)((ws_bytes - kWorkspaceFront) / part_bytes(pool));
+    const long long n = std::min(std::min(std::min((long long)sms, room) / blocks, tiles / prompt_masked::kMinTiles),
+                                 (long long)prompt_masked::kMaxParts);
+    if (n < 2) return 1;
+    const double bytes = 2.0 * (double)(blocks * n * std::min<long long>(all_rows, prompt_masked::ROWS)) * pool->head_dim * sizeof(float);
+    return 0.9 * (double)(tiles - (tiles + n - 1) / n) > 4.0 + bytes / 5e6 ? (int)n : 1;
+}
+
+size_t masked_workspace_bytes(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new) {
+    int sms = 0;
+    if (n_seqs <= 0 || max_new <= 0 || n_q_heads <= 0 || n_q_heads % pool->n_kv_heads || max_blocks <= 0 ||
+        device_sms(false, &sms) != PF_OK)
+        return 0;
+    // a part per SM, whatever the batch: a smaller one takes no more
+    return masked_splits(pool, mask, n_seqs, n_q_heads, max_blocks, max_new, sms, SIZE_MAX) == 1
+               ? 0
+               : kWorkspaceFront + sms * part_bytes(pool);
+}
+
+int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
+    int *status = device_status_ptr();
+    if (!status) return PF_ERR_CUDA;
+    pf_pool *pool = const_cast<pf_pool *>(a.pool);
+    const int D = pool->head_dim;
+    const bool q8 = pool->dtype == PF_E4M3;
+    const int gh = a.n_q_heads / pool->n_kv_heads;
+    const long long rows = (long long)a.max_new * gh;
+    const long long n_items = (long long)a.n_seqs * pool->n_kv_heads;
+    const long long n_qp = (rows + prompt_masked::ROWS - 1) / prompt_masked::ROWS;
+    const long long blocks = n_items * n_qp;
+    if (blocks > 0x7fffffffll) return set_error(PF_ERR_INVALID, "attention: too many query tiles for one launch");
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "attention: cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return set_error(PF_ERR_UNSUPPORTED, "device index out of range");
+    int rc = device_sms(true, &sms);
+    if (rc) return rc;
+    if (!q8 && (rc = encode_prompt_tmaps(pool, dev, 1, unit_rows(pool))) != PF_OK) return rc;   // e4m3 tiles are not copied by TMA
+    prompt_masked::Params p;
+    p.q = static_cast<const __half *>(a.q);
+    p.k_pool = pool->k_base;
+    p.v_pool = pool->v_base;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.out = a.out;
+    p.bt = a.block_tables;
+    p.lens = a.context_lens;
+    p.cu_q = a.cu_q;
+    p.status = status;
+    p.n_q_heads = a.n_q_heads;
+    p.n_kv_heads = pool->n_kv_heads;
+    p.gh = gh;
+    p.gh_magic = (65536 + gh - 1) / gh;
+    p.max_blocks = a.max_blocks;
+    p.max_new = a.max_new;
+    p.n_blocks = pool->n_blocks;
+    p.block_size = pool->block_size;
+    p.block_shift = 0;
+    while ((1 << p.block_shift) < pool->block_size) ++p.block_shift;
+    p.unit_shift = 0;
+    while ((1 << p.unit_shift) < unit_rows(pool)) ++p.unit_shift;
+    p.n_seqs = a.n_seqs;
+    p.n_items = (int)n_items;
+    p.n_qp = (int)n_qp;
+    p.layer_page0 = (long long)a.layer * pool->n_blocks;
+    p.layer_row0 = p.layer_page0 * pool->block_size;
+    p.out_f32 = a.out_dtype == PF_F32;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.mask = a.mask;
+    p.splits = 1;
+    p.part_ml = nullptr;
+    p.part_o = nullptr;
+    if (a.workspace) {
+        p.splits = masked_splits(pool, a.mask, a.n_seqs, a.n_q_heads, a.max_blocks, a.max_new, sms, a.ws_bytes);
+        p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceFront);
+        p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * prompt_masked::ROWS);
+    }
+    const bool split = p.splits > 1;
+    p.n_work = (int)(blocks * p.splits);     // (cut: no more than SMs)
+    const prompt_masked::Kernels k = a.mask.kind == kMaskWindow ? prompt_masked::window_kernels(D, q8, split)
+                                                                : prompt_masked::tree_kernels(D, q8, split);
+    // once per device and kernel (setting it twice does no harm)
+    static std::atomic<bool> ready[kMaxDevices][16];
+    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * q8 + 4 * split + 8 * (a.mask.kind == kMaskWindow)];
+    if (!done.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k.main), cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (e != cudaSuccess) return cuda_error(e, "attention: cudaFuncSetAttribute");
+        done.store(true, std::memory_order_release);
+    }
+    const unsigned grid = (unsigned)std::min(p.n_work, sms);
+    k.main<<<grid, prompt_masked::NTHREADS, k.smem, stream>>>(pool->tmap_pf_k[dev][1], pool->tmap_pf_v[dev][1], p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_error(e, "attention: launch");
+    if (split) {
+        cudaLaunchConfig_t cfg = {};
+        const long long most = std::min<long long>(rows, prompt_masked::ROWS);   // rows of a block
+        cfg.gridDim = dim3((unsigned)blocks, (unsigned)((most + prompt_masked::kMergeWarps - 1) / prompt_masked::kMergeWarps));
+        cfg.blockDim = dim3(32 * prompt_masked::kMergeWarps);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k.merge, p);
+        if (e != cudaSuccess) return cuda_error(e, "attention: merge launch");
+    }
+    return PF_OK;
+}
+
+}  // namespace pkv

@@ -68,22 +68,30 @@ def test_not_built(pkv):
 
 def test_binding_refuses_shapes(pkv, monkeypatch):
     import torch
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    # (a host tensor's device is -1: as if that were the current one, every shape is looked at)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
     pool = SimpleNamespace(handle=None, n_layers=1, n_blocks=8, block_size=16, n_kv_heads=2, head_dim=64, k_scale=None,
-                           device=0)
+                           device=-1)
     q, k = torch.zeros((3, 4, 64), dtype=torch.float16), torch.zeros((3, 2, 64), dtype=torch.float16)
     i3, table, ang = torch.zeros(3, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32), torch.zeros((9, 64))
     good = dict(q=q, k=k, v=k, block_tables=table, seq_idx=i3, pos=i3, angles=ang, q_out=q.clone())
     for kw, word in ((dict(q=None, k=None), "neither"), (dict(k=k[:2]), "rows"), (dict(v=k[:2]), "rows"),
-                     (dict(q_out=None), "q_out"), (dict(q=None), "q_out"), (dict(q=q[0], k=None, v=None, q_out=q), "rows"),
+                     (dict(q_out=None), "q_out"), (dict(q=None), "q_out"), (dict(q=q[0], k=None, v=None, q_out=q), "n_tokens"),
+                     (dict(v=k[0]), "rows"), (dict(q_out=q[:2]), "rows"), (dict(q=q.float()), "float16"),
+                     (dict(k=k.transpose(0, 1).contiguous().transpose(0, 1)), "contiguous"), (dict(k_out=q), "rows"),
+                     (dict(pos=i3.long()), "int32"),
                      (dict(seq_idx=i3[:2]), "seq_idx"), (dict(pos=i3[:2]), "pos"), (dict(rope_pos=i3[:2]), "rope_pos"),
                      (dict(block_tables=i3), "block_tables"), (dict(angles=ang[0]), "angles"),
                      (dict(q_weight=ang[0, :32]), "q_weight"), (dict(k_weight=ang), "k_weight"),
-                     (dict(q=q[..., :32]), "64"), (dict(), "CUDA")):
+                     (dict(q=q[..., :32]), "64"), (dict(), "pool is null")):
         with pytest.raises(pkv.PagedKVError, match=word):
             pkv.pf_norm_rope_write(pool, 0, **{**good, **kw})
     pool.device = 1
     with pytest.raises(pkv.PagedKVError, match="current device"):
+        pkv.pf_norm_rope_write(pool, 0, **good)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(pkv.PagedKVError, match="CUDA"):
         pkv.pf_norm_rope_write(pool, 0, **good)
 
 
