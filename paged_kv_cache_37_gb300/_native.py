@@ -499,21 +499,27 @@ def pf_paged_cross_attention(pool, layer, q, block_tables, context_lens, cu_q, m
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
 
 
-def _masked_args(pool, q, block_tables, context_lens, cu_q, out):
-    """Checked arguments that the masked attention calls share: the device, the
-    number of sequences, out's type code."""
+def _masked_args(pool, q, block_tables, context_lens, cu_q, out, workspace):
+    """Checked arguments that the masked attention calls share: addresses of q,
+    tables, lengths, cu_q, out and workspace, and the sizes among the arguments."""
     import torch
+    shape, table = q.shape, block_tables.shape
     n = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != n or (cu_q is not None and cu_q.numel() != n + 1):
+    if len(table) != 2 or table[0] != n or (cu_q is not None and cu_q.numel() != n + 1):
         raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
-    if q.dim() != 3 or q.shape[2] != pool.head_dim or tuple(out.shape) != tuple(q.shape):
+    if len(shape) != 3 or shape[2] != pool.head_dim or out.shape != shape:
         raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out of its shape")
-    if cu_q is None and q.shape[0] != n:
+    if cu_q is None and shape[0] != n:
         raise PagedKVError(PF_ERR_INVALID, "without cu_q, q must have a row per sequence")
-    out_dtype = {torch.float16: PF_F16, torch.float32: PF_F32}.get(out.dtype)
-    if out_dtype is None:
+    out_dtype = PF_F16 if out.dtype is torch.float16 else PF_F32
+    if out_dtype == PF_F32 and out.dtype is not torch.float32:
         raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
-    return _pool_device(pool), n, out_dtype
+    dev, i32 = _pool_device(pool), torch.int32
+    return (dev, shape[0], n, shape[1], table[1], out_dtype, _dev_ptr(q, "q", torch.float16, dev),
+            _dev_ptr(block_tables, "block_tables", i32, dev), _dev_ptr(context_lens, "context_lens", i32, dev),
+            None if cu_q is None else _dev_ptr(cu_q, "cu_q", i32, dev), _dev_ptr(out, "out", None, dev),
+            None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
+            0 if workspace is None else workspace.nbytes)
 
 
 def pf_window_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, window, n_sinks=0):
@@ -527,18 +533,12 @@ def pf_paged_window_attention(pool, layer, q, block_tables, context_lens, cu_q, 
     """Causal attention of each sequence's last tokens (q rows
     cu_q[s]..cu_q[s+1]-1; cu_q None: one each, row s) over the last `window`
     tokens up to the query's own and the first n_sinks."""
-    import torch
-    dev, n, out_dtype = _masked_args(pool, q, block_tables, context_lens, cu_q, out)
-    if q.numel() == 0:
+    _, rows, n, hq, width, out_dtype, q_p, bt_p, len_p, cu_p, out_p, ws_p, ws_bytes = _masked_args(
+        pool, q, block_tables, context_lens, cu_q, out, workspace)
+    if rows == 0:
         return
-    _check(lib().pf_paged_window_attention(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
-        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
-        _dev_ptr(context_lens, "context_lens", torch.int32, dev),
-        None if cu_q is None else _dev_ptr(cu_q, "cu_q", torch.int32, dev), n, int(max_new_tokens), q.shape[1],
-        float(scale), int(window), int(n_sinks), _dev_ptr(out, "out", None, dev), out_dtype,
-        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    _check(lib().pf_paged_window_attention(pool.handle, layer, q_p, bt_p, width, len_p, cu_p, n, int(max_new_tokens), hq, float(scale),
+                                           int(window), int(n_sinks), out_p, out_dtype, ws_p, ws_bytes, _stream_ptr(stream)))
 
 
 def pf_tree_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_draft_tokens):
@@ -552,21 +552,18 @@ def pf_paged_tree_attention(pool, layer, q, block_tables, context_lens, cu_q, ma
     the tokens before them, and draft j where bit j % 64 of the query's
     tree[row, j // 64] is set (tree: int64 [T_q, words])."""
     import torch
-    dev, n, out_dtype = _masked_args(pool, q, block_tables, context_lens, cu_q, out)
     if cu_q is None:
         raise PagedKVError(PF_ERR_INVALID, "cu_q must be given")
-    if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
+    dev, rows, n, hq, width, out_dtype, q_p, bt_p, len_p, cu_p, out_p, ws_p, ws_bytes = _masked_args(
+        pool, q, block_tables, context_lens, cu_q, out, workspace)
+    bits = tree.shape
+    if len(bits) != 2 or bits[0] != rows:
         raise PagedKVError(PF_ERR_INVALID, "tree must be [T_q, words], a row per query")
-    if q.numel() == 0:
+    if rows == 0:
         return
-    _check(lib().pf_paged_tree_attention(
-        pool.handle, layer, _dev_ptr(q, "q", torch.float16, dev),
-        _dev_ptr(block_tables, "block_tables", torch.int32, dev), block_tables.shape[1],
-        _dev_ptr(context_lens, "context_lens", torch.int32, dev), _dev_ptr(cu_q, "cu_q", torch.int32, dev), n,
-        int(max_draft_tokens), q.shape[1], float(scale), _dev_ptr(tree, "tree", torch.int64, dev), tree.shape[1],
-        _dev_ptr(out, "out", None, dev), out_dtype,
-        None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    _check(lib().pf_paged_tree_attention(pool.handle, layer, q_p, bt_p, width, len_p, cu_p, n, int(max_draft_tokens), hq, float(scale),
+                                         _dev_ptr(tree, "tree", torch.int64, dev), bits[1], out_p, out_dtype, ws_p, ws_bytes,
+                                         _stream_ptr(stream)))
 
 
 def pf_append_kv(pool, layer, k_new, v_new, block_tables, context_lens, cu_new, max_new_tokens=1, stream=None):
@@ -659,7 +656,7 @@ def pf_norm_rope_write(pool, layer, q, k, v, block_tables, seq_idx, pos, angles,
             raise PagedKVError(PF_ERR_INVALID, "pos must have n_tokens entries")
         at = _dev_ptr(pos, "pos", i32, dev)
     _check(lib().pf_norm_rope_write(
-        pool.handle, layer, q_ptr, q_apart, k_ptr, k_apart, v_ptr, v_apart, n, hq, w_q, w_k, eps, ang, n_positions,
+        pool.handle, layer, q_ptr, q_apart, k_ptr, k_apart, v_ptr, v_apart, n, hq, w_q, w_k, float(eps), ang, n_positions,
         rot, PF_ROPE_INTERLEAVED if interleaved else 0, rp, bt, rows, width, seq, at, q_to, q_to_apart, k_to,
         k_to_apart, _stream_ptr(stream)))
 

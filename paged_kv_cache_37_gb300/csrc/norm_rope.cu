@@ -9,13 +9,20 @@
 // over the pairs (y_i, y_{i + rot / 2}), or (y_2i, y_2i+1), i < rot / 2.  All in
 // fp32 and rounded once, to the fp16 result.  V rows are copied.
 //
-// Floor: 2 bytes read and 2 written per value, so it is HBM's.  A row is
-// spread over D / 8 lanes, 16 bytes each: the norm is a butterfly among them, the
-// partner of a pair (i, i + rot / 2) lies in the lane rot / 16 chunks away and comes
-// as the fp16 values read, before the norm (4 shuffles instead of 8).  A group
-// of D / 8 lanes takes up to kRows heads of one token, all loads of which are on
-// their way before the first is used, and reads the token's cosines and sines
-// (fp32, from L2) once for them.
+// Floor: 2 bytes read and 2 written per value, so it is HBM's.  Measured on
+// GB300: four prompts of 2,048 tokens, 40 heads x 128 (503 MB) 87 us, 5.8 TB/s,
+// 85 % of the measured copy rate; one token each for 4 and 256 sequences 3 to
+// 3.6 us, a launch and a chain of dependent loads.  A row is spread over D / 8
+// lanes, 16 bytes each: the norm is a butterfly among them, the partner of a pair
+// (i, i + rot / 2) lies in the lane rot / 16 chunks away and comes as the fp16
+// values read, before the norm.  A group of D / 8 lanes takes up to kRows heads of
+// one token, all loads of which are on their way before the first is used, and
+// folds the token's cosines and sines (fp32, from L2) and the weights into two
+// factors per value, once for them.  Instructions count: with the norm, weights
+// and rotation one after another the prompts took 106 us; with the two factors and
+// two-wide fp32 instructions 92; with streaming stores 87.  (kRows 2, 4, 8 at 128
+// threads: 111, 87, 88 us, the 4 sequences 3.0, 3.6, 4.5; 256 threads a CTA were
+// slower, 108 us with 4, its CTAs ending less evenly.)
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -59,6 +66,45 @@ struct RopeParams {
     long long layer_row0;
 };
 
+// 16 bytes read once (coherent: outputs may be the inputs, in place).
+__device__ __forceinline__ uint4 ld_once(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Pairs of fp32 values for the two-wide instructions.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t widen(uint32_t half2_bits) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&half2_bits));
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+    const float2 f = both(v);
+    return pair(f.y, f.x);
+}
+// Eight floats.
 __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
@@ -92,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p)
     uint4 x[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-        x[r] = r < n ? *reinterpret_cast<const uint4 *>(src + r * D) : make_uint4(0u, 0u, 0u, 0u);
+        x[r] = r < n ? ld_once(reinterpret_cast<const uint4 *>(src + r * D)) : make_uint4(0u, 0u, 0u, 0u);
 
     // the token's angles, and its slot
     const bool rotated = p.rot && kind < 2;
@@ -121,8 +167,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p)
     if (kind == 1 && p.k_out) dense = p.k_out + (long long)token * p.k_out_stride;
     auto store = [&](int r, uint4 v) {
         const int at = (h0 + r) * D + c * 8;
-        if (dense) *reinterpret_cast<uint4 *>(dense + at) = v;
-        if (page) *reinterpret_cast<uint4 *>(page + at) = v;
+        if (dense) st_stream(reinterpret_cast<uint4 *>(dense + at), v);
+        if (page) st_stream(reinterpret_cast<uint4 *>(page + at), v);
     };
     if (kind == 2) {
 #pragma unroll
@@ -131,82 +177,87 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p)
         return;
     }
 
-    // the lane's place in the rotation: its pairs, and the chunk of their other halves
+    // The lane's eight values x and their partners p (the other values of their
+    // pairs) become inv * (x A + p B), A = w c and B = -+ w' s with the partner's
+    // weight w': the token's, for all of its rows.
     const bool turns = c < p.rot / 8;
     const int half = p.rot / 16;                     // chunks of half the rotated values
     const int partner = INTERLEAVED || !turns ? c : (c < half ? c + half : c - half);
-    float cs[8], sn[8];                              // (interleaved: 4 of each)
-    if (INTERLEAVED) {
-        float both[8] = {1.0f, 1.0f, 1.0f, 1.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (turns) {
-            const float *at = p.angles + (size_t)rp * p.rot + c * 4;
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(at)), b = __ldg(reinterpret_cast<const float4 *>(at + p.rot / 2));
-            both[0] = a.x, both[1] = a.y, both[2] = a.z, both[3] = a.w;
-            both[4] = b.x, both[5] = b.y, both[6] = b.z, both[7] = b.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = both[i], sn[i] = both[4 + i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
-        if (turns) {
-            const float *at = p.angles + (size_t)rp * p.rot + (c < half ? c : c - half) * 8;
-            load8(at, cs);
-            load8(at + p.rot / 2, sn);
-            if (c < half) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
-            }
-        }
-    }
     const float *weight = p.weight[kind];
     float w[8], wp[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = wp[i] = 1.0f;
     if (weight) {
         load8(weight + c * 8, w);
         if (!INTERLEAVED) load8(weight + partner * 8, wp);
     }
+    uint64_t A[4], B[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        A[i] = pair(w[2 * i], w[2 * i + 1]);
+        B[i] = 0;
+    }
+    if (turns) {
+        const float *at = p.angles + (size_t)rp * p.rot;
+        if (INTERLEAVED) {
+            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(at + c * 4)),
+                         s4 = __ldg(reinterpret_cast<const float4 *>(at + p.rot / 2 + c * 4));
+            const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                A[i] = mul2(A[i], pair(cs[i], cs[i]));
+                B[i] = mul2(pair(w[2 * i + 1], w[2 * i]), pair(-sn[i], sn[i]));
+            }
+        } else {
+            float cs[8], sn[8];
+            const int j = (c < half ? c : c - half) * 8;
+            load8(at + j, cs);
+            load8(at + p.rot / 2 + j, sn);
+            const float sign = c < half ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                A[i] = mul2(A[i], pair(cs[2 * i], cs[2 * i + 1]));
+                B[i] = mul2(pair(sign * wp[2 * i], sign * wp[2 * i + 1]), pair(sn[2 * i], sn[2 * i + 1]));
+            }
+        }
+    }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         if (r >= n) break;                           // (the group's lanes together)
-        float y[8];
-        half8_to_float(x[r], y);
-        uint4 xp = x[r];
-        if (!INTERLEAVED && p.rot) {
-            xp.x = __shfl_sync(group, x[r].x, partner, CPR);
-            xp.y = __shfl_sync(group, x[r].y, partner, CPR);
-            xp.z = __shfl_sync(group, x[r].z, partner, CPR);
-            xp.w = __shfl_sync(group, x[r].w, partner, CPR);
-        }
-        float yp[8];
-        half8_to_float(xp, yp);
-        if (weight) {
-            float sum = 0.0f;
+        const uint32_t in[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        uint64_t y[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+        for (int i = 0; i < 4; ++i) y[i] = widen(in[i]);
+        uint64_t inv = 0;
+        if (weight) {
+            uint64_t sum2 = mul2(y[0], y[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) sum2 = fma2(y[i], y[i], sum2);
+            const float2 s2 = both(sum2);
+            float sum = s2.x + s2.y;
 #pragma unroll
             for (int o = CPR / 2; o; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
-            const float inv = rsqrtf(sum * (1.0f / D) + p.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[i] *= inv * w[i];
-                if (!INTERLEAVED) yp[i] *= inv * wp[i];
-            }
+            const float f = rsqrtf(sum * (1.0f / D) + p.eps);
+            inv = pair(f, f);
         }
         uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float a = y[2 * i], b = y[2 * i + 1];
-            if (turns) {                             // (the others are not multiplied by a 1 and a 0: infinities stay)
+            uint64_t v = mul2(y[i], A[i]);
+            if (p.rot) {
+                // (lanes that do not turn take no partner: infinities stay theirs)
+                uint64_t q = 0;
                 if (INTERLEAVED) {
-                    const float a0 = a;
-                    a = fmaf(a0, cs[i], -b * sn[i]);
-                    b = fmaf(b, cs[i], a0 * sn[i]);
+                    if (turns) q = swapped(y[i]);
                 } else {
-                    a = fmaf(a, cs[2 * i], yp[2 * i] * sn[2 * i]);
-                    b = fmaf(b, cs[2 * i + 1], yp[2 * i + 1] * sn[2 * i + 1]);
+                    const uint32_t bits = __shfl_sync(group, in[i], partner, CPR);
+                    if (turns) q = widen(bits);
                 }
+                v = fma2(q, B[i], v);
             }
-            const __half2 h = __floats2half2_rn(a, b);
+            if (weight) v = mul2(v, inv);
+            const float2 o = both(v);
+            const __half2 h = __floats2half2_rn(o.x, o.y);
             out[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
         store(r, make_uint4(out[0], out[1], out[2], out[3]));

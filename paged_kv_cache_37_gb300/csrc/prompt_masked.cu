@@ -9,7 +9,7 @@ namespace pkv {
 namespace {
 
 int tile_tokens(const pf_pool *pool) {
-    return pool->head_dim == 64 ? prompt_masked::Cfg<64, false>::BN : prompt_masked::Cfg<128, false>::BN;
+    return pool->head_dim == 64 ? prompt_masked::Cfg<64, false, false>::BN : prompt_masked::Cfg<128, false, false>::BN;
 }
 
 // Rows that are looked up and copied together: what a page holds of a tile (the
@@ -117,12 +117,13 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
         p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * prompt_masked::ROWS);
     }
     const bool split = p.splits > 1;
+    const bool dual = rows <= prompt_masked::QT;
     p.n_work = (int)(blocks * p.splits);     // (cut: no more than SMs)
-    const prompt_masked::Kernels k = a.mask.kind == kMaskWindow ? prompt_masked::window_kernels(D, q8, split)
-                                                                : prompt_masked::tree_kernels(D, q8, split);
+    const prompt_masked::Kernels k = a.mask.kind == kMaskWindow ? prompt_masked::window_kernels(D, q8, split, dual)
+                                                                : prompt_masked::tree_kernels(D, q8, split, dual);
     // once per device and kernel (setting it twice does no harm)
-    static std::atomic<bool> ready[kMaxDevices][16];
-    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * q8 + 4 * split + 8 * (a.mask.kind == kMaskWindow)];
+    static std::atomic<bool> ready[kMaxDevices][32];
+    std::atomic<bool> &done = ready[dev][(D == 64) + 2 * q8 + 4 * split + 8 * (a.mask.kind == kMaskWindow) + 16 * dual];
     if (!done.load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k.main), cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
         if (e != cudaSuccess) return cuda_error(e, "attention: cudaFuncSetAttribute");

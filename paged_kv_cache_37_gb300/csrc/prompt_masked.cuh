@@ -31,6 +31,11 @@
 // So a block's first tiles, its query rows and its first scores are there when
 // the block before is written.
 //
+// Calls of at most 128 rows per (sequence, kv-head) (DUAL) have one query tile a
+// block: the two groups of softmax warps take its even and its odd tiles, each
+// with a maximum, a sum and an O of its own, and join them at the block's end, half
+// of the dims each.
+//
 // Per tile (see prefill_tc.cu): scores in tensor memory, a running maximum per row
 // in the log2 domain that is raised only past 2^8, weights rounded to fp16 into
 // tensor memory, row sums of the fp32 weights.  A row may see nothing of a tile, of
@@ -83,21 +88,22 @@ struct Regs {
     static_assert(SOFTMAX % 8 == 0 && 2 * 128 * (SOFTMAX + OTHER) == NTHREADS * 128, "the split is the launch's registers");
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool DUAL>
 struct Cfg {
     static constexpr int NS = Q8 ? 3 : 4;               // K/V stages
-    static constexpr int RAW = 2;                       // e4m3: stages of codes
+    static constexpr int RAW = 2;                       // e4m3: stages of codes (more, up to 5, changed nothing)
     static constexpr int BN = D == 64 ? 128 : 64;       // tokens per K/V tile (the scores' N)
     static constexpr int HALVES = D / 64;               // 64-element halves of a row
     static constexpr int Q_BYTES = QT * D * 2;          // one query tile
     static constexpr int KV_BYTES = BN * D * 2;         // one K or V tile
     static constexpr int OUT_BYTES = 32 * 128;          // a softmax warp's rows on their way out
-    static constexpr int OFF_K = 2 * Q_BYTES;
+    static constexpr int OFF_K = (DUAL ? 1 : 2) * Q_BYTES;
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
     static constexpr int OFF_OUT = OFF_V + NS * KV_BYTES;
     static constexpr int OFF_RAW = OFF_OUT + SOFTMAX_WARPS * OUT_BYTES;
     static constexpr int RAW_BYTES = Q8 ? BN * D + BN * 4 : 0;   // codes of a K or V tile, then the scales of its tokens
-    static constexpr int DATA = OFF_RAW + 2 * RAW * RAW_BYTES;
+    static constexpr int OFF_ML = OFF_RAW + 2 * RAW * RAW_BYTES;   // DUAL: maxima and sums of both groups
+    static constexpr int DATA = OFF_ML + (DUAL ? 2 * QT * 8 : 0);
     static constexpr int SMEM = DATA + 1024;            // slack to align the base to 1024 bytes
     // tensor memory (fp32 columns): S, O, and P (two weights per column) of both tiles
     static constexpr int COL_O = 2 * BN;
@@ -240,16 +246,18 @@ struct Bars {
     unsigned long long o_done[2];
     unsigned long long q_full[2];
     unsigned long long v_landed;     // a block's last V tile, for its loaders
+    unsigned long long ml_full[2];     // DUAL: a group's maxima and sums are there
+    unsigned long long o_read[2];      // DUAL: a group has read both products
     unsigned long long mma_done[2];
     unsigned long long info_full[kInfos];
     unsigned long long info_empty[kInfos];
     uint32_t tmem_base;
 };
 
-template <int D, bool Q8, bool SPLIT, int MASK>
+template <int D, bool Q8, bool SPLIT, int MASK, bool DUAL>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prompt_masked_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const Params p) {
-    using C = Cfg<D, Q8>;
+    using C = Cfg<D, Q8, DUAL>;
     constexpr bool WINDOW = MASK == kMaskWindow, TREE = MASK == kMaskTree;
     constexpr int BN = C::BN;
     constexpr int NS = C::NS;
@@ -293,6 +301,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 mbar_init(bar(bars.o_done[u]), 1);
                 mbar_init(bar(bars.mma_done[u]), 1);
                 mbar_init(bar(bars.q_full[u]), 128);
+                mbar_init(bar(bars.ml_full[u]), 128);
+                mbar_init(bar(bars.o_read[u]), 128);
             }
             mbar_init(bar(bars.v_landed), 2);
             for (int k = 0; k < kInfos; ++k) {
@@ -345,15 +355,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t t_p = tmem + lane_off + (uint32_t)(C::COL_P + g * (BN / 2));
         const uint32_t stage = smem_addr(sm + C::OFF_OUT) + warp * C::OUT_BYTES;
         const float sl = p.scale_log2;
+        const int row0_g = DUAL ? 0 : g * QT;                  // of the group's query tile in the block
+        float2 *ml = reinterpret_cast<float2 *>(sm + C::OFF_ML);   // DUAL: [group][row]
+        unsigned done_other = 0;                               // DUAL: tiles of the other group so far
         unsigned done = 0;                                     // tiles of this query tile so far
         bool ok = true;
         Rows f;
+        int nt_other = 0;
         auto take_rows = [&](unsigned k) {
             const unsigned slot = k % kInfos;
             if (!wait_lanes(bar(bars.info_full[slot]), (k / kInfos) & 1, p.status)) return false;
             const Info &in = infos[slot];
             f = Rows{in.blk, in.h, in.part, in.q0, in.n, in.base, in.r0, in.r_end, in.i0, in.rem0, in.lim[g], in.nt[g],
                      in.sinks, in.skip, in.tile0, in.n_parts};
+            nt_other = in.nt[g ^ 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bars.info_empty[slot]));
             return true;
@@ -361,11 +376,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // The warp's query rows in block f (zeros past the last), 16 bytes each and
         // neighbouring lanes neighbouring chunks: on their way, then there.
         auto fetch_rows = [&]() {
-            if (f.blk < 0 || f.nt == 0) return;
+            if (f.blk < 0 || f.nt == 0 || (DUAL && g)) return;   // (DUAL: the first group's rows serve both)
             constexpr int CH = D / 8;
             const int u = (warp % 4) * 32 + lane / CH, c = lane % CH;   // of the tile: this lane's first row, chunk
-            const int d0 = f.rem0 + g * QT + u;
-            const int left = f.r_end - f.r0 - g * QT - u;
+            const int d0 = f.rem0 + row0_g + u;
+            const int left = f.r_end - f.r0 - row0_g - u;
             const __half *src = p.q + ((size_t)(f.q0 + f.i0) * p.n_q_heads + (size_t)f.h * p.gh) * D + c * 8;
             const int apart = (p.n_q_heads - p.gh) * D;        // from a token's last row to the next one's first, less a row
             const uint32_t dst = smem_addr(sm) + g * C::Q_BYTES;
@@ -377,7 +392,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         };
         auto rows_there = [&]() {
-            if (f.blk < 0 || f.nt == 0) return;
+            if (f.blk < 0 || f.nt == 0 || (DUAL && g)) return;
             asm volatile("cp.async.wait_all;" ::: "memory");
             if (C::Q0_TMEM && g == 0) {
                 __syncwarp();
@@ -407,8 +422,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (unsigned block = 1; ok && f.blk >= 0; ++block) {
             const size_t part_row = SPLIT ? ((size_t)f.blk * p.splits + f.part) * ROWS : 0;
             const int nt = f.nt, i0 = f.i0, rem0 = f.rem0;
-            const bool valid = f.r0 + g * QT + t < f.r_end;
-            const int mine = valid ? i0 + (((rem0 + g * QT + t) * p.gh_magic) >> 16) : 0;   // this row's new token
+            const bool valid = f.r0 + row0_g + t < f.r_end;
+            const int mine = valid ? i0 + (((rem0 + row0_g + t) * p.gh_magic) >> 16) : 0;   // this row's new token
             // from the CTA's first tile on: the last virtual position that the row
             // sees, the sinks' end, the first draft
             const int from = f.tile0 * BN;
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
                 // What the row does not see: -inf.  A bit per column says what it
                 // sees (two compares and a select per column took longer).
-                const int x0 = j * BN;
+                const int x0 = (DUAL ? 2 * j + g : j) * BN;
                 const int cl = lim - x0, cw = cl - p.mask.window + 1, cs = sinks - x0;   // WINDOW
                 if (TREE ? x0 + BN > draft0 : cl < BN - 1 || (cw > 0 && cs < cw && cs < BN)) {
 #pragma unroll
@@ -494,6 +509,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     l += (a0 + a1) + (b0 + b1);
                 }
 
+                // DUAL: the other group has read the last block's O
+                if (DUAL && j == 0 && block > 1 && !wait_lanes(bar(bars.o_read[g ^ 1]), block & 1, p.status)) {
+                    ok = false;
+                    break;
+                }
                 // the previous product has finished reading P and adding to O
                 if (j > 0) {
                     if (!wait_lanes(bar(bars.o_done[g]), (done - 1) & 1, p.status)) {
@@ -528,40 +548,89 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // product and the output go on.
             const int left = f.r_end - f.r0, n_parts = f.n_parts;
             const size_t row0 = ((size_t)(f.q0 + i0) * p.n_q_heads + (size_t)f.h * p.gh) * D;   // of token i0
+            const int other = nt_other;
+            if (DUAL) {
+                // the second group's scores, over the same query rows, are done too
+                // (no further ones come before the next rows); the other group has
+                // read what this one left for the last block (above, with tiles)
+                done_other += other;
+                if (g == 0 && other > 0 && !wait_lanes(bar(bars.s_full[g ^ 1]), (done_other - 1) & 1, p.status)) break;
+                if (nt == 0 && block > 1 && !wait_lanes(bar(bars.o_read[g ^ 1]), block & 1, p.status)) break;
+                ml[g * QT + t] = make_float2(m, l);
+                mbar_arrive(bar(bars.ml_full[g]));
+            }
             ok = take_rows(block);
             if (!ok) break;
             fetch_rows();
-            if (nt == 0) {
+            if (!DUAL && nt == 0) {
                 rows_there();
                 continue;
             }
-            if (!wait_lanes(bar(bars.o_done[g]), (done - 1) & 1, p.status)) break;
+            if (nt > 0 && !wait_lanes(bar(bars.o_done[g]), (done - 1) & 1, p.status)) break;
+            float f_own = 1.0f, f_other = 0.0f;                // DUAL: factors that join the groups
+            if (DUAL) {
+                if ((other > 0 && !wait_lanes(bar(bars.o_done[g ^ 1]), (done_other - 1) & 1, p.status)) ||
+                    !wait_lanes(bar(bars.ml_full[g ^ 1]), (block - 1) & 1, p.status))
+                    break;
+                const float2 o = ml[(g ^ 1) * QT + t];
+                const float top = fmaxf(m, o.x);
+                if (top > -INFINITY) {
+                    f_own = ex2(m - top);
+                    f_other = ex2(o.x - top);
+                }
+                m = top;
+                l = l * f_own + o.y * f_other;
+            }
             tc_after_sync();
             const bool whole = !SPLIT || n_parts == 1;         // else a part: unscaled, fp32
             const float inv = !whole ? 1.0f : (TREE && l == 0.0f ? 0.0f : 1.0f / l);   // (a draft may see nothing)
-            if (!whole) p.part_ml[part_row + g * QT + t] = make_float2(m, l);
-            // The warp's 32 rows, 128 bytes of each at a time, through shared
+            if (!whole && !(DUAL && g)) p.part_ml[part_row + row0_g + t] = make_float2(m, l);
+            // The warp's 32 rows, up to 128 bytes of each at a time, through shared
             // memory: stored by rows straight from tensor memory, 16 bytes per
-            // lane and row, the output took 5,000 cycles.
+            // lane and row, the output took 5,000 cycles.  (DUAL: each group half of
+            // the dims, from both products.)
             const int t0 = (warp % 4) * 32;
+            const uint32_t o_0 = tmem + lane_off + (uint32_t)C::COL_O;
             auto store = [&](auto f32_c) {
                 constexpr bool F32 = decltype(f32_c)::value;
-                constexpr int DP = F32 ? 32 : 64;              // dims of 128 bytes
+                constexpr int DIMS = DUAL ? D / 2 : D;         // of this group
+                constexpr int DP = F32 ? 32 : (DIMS < 64 ? DIMS : 64);   // at a time
+                constexpr int CK = DP * (F32 ? 4 : 2) / 16;    // chunks of them
+                const int first = DUAL ? g * DIMS : 0;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += DP) {
+                for (int c0 = 0; c0 < DIMS; c0 += DP) {
 #pragma unroll
                     for (int half = 0; half < DP / 32; ++half) {
                         uint32_t o[32];
-                        tmem_ld32(t_o + c0 + half * 32, o);
-                        tmem_ld_wait();
+                        float by = inv;
+                        if constexpr (DUAL) {
+                            const int at = first + c0 + half * 32;
+                            const float f0 = (g ? f_other : f_own) * inv, f1 = (g ? f_own : f_other) * inv;
+                            uint32_t u[32];
+                            tmem_ld32(o_0 + at, o);
+                            if (g ? nt > 0 : other > 0) {      // (the second group has tiles)
+                                tmem_ld32(o_0 + D + at, u);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(fmaf(__uint_as_float(u[e]), f1, __uint_as_float(o[e]) * f0));
+                                by = 1.0f;
+                            } else {
+                                tmem_ld_wait();
+                                by = f0;
+                            }
+                        } else {
+                            tmem_ld32(t_o + c0 + half * 32, o);
+                            tmem_ld_wait();
+                        }
 #pragma unroll
                         for (int e = 0; e < (F32 ? 8 : 4); ++e) {
                             uint32_t v[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if constexpr (F32) v[k] = __float_as_uint(__uint_as_float(o[4 * e + k]) * inv);
-                                else v[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                                       __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                                if constexpr (F32) v[k] = __float_as_uint(__uint_as_float(o[4 * e + k]) * by);
+                                else v[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * by,
+                                                       __uint_as_float(o[8 * e + 2 * k + 1]) * by);
                             }
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz(lane, half * 4 + e, 32)),
                                          "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -569,22 +638,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                     __syncwarp();
+                    if (DUAL && c0 + DP == DIMS) {             // both products have been read
+                        tc_before_sync();
+                        mbar_arrive(bar(bars.o_read[g]));
+                    }
                     if (c0 == 0) rows_there();                 // the next block's scores can begin
 #pragma unroll
-                    for (int it = 0; it < 8; ++it) {
-                        const int row = it * 4 + lane / 8, c = lane % 8, d = g * QT + t0 + row;
+                    for (int it = 0; it < CK; ++it) {
+                        const int row = it * (32 / CK) + lane / CK, c = lane % CK, d = row0_g + t0 + row;
                         uint4 v;
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                      : "r"(stage + swz(row, c, 32)));
+                        const int col = first + c0 + c * (F32 ? 4 : 8);
                         if (SPLIT && !whole) {
-                            if (F32 && d < left)
-                                *reinterpret_cast<uint4 *>(p.part_o + (part_row + d) * D + c0 + c * 4) = v;
+                            if (F32 && d < left) *reinterpret_cast<uint4 *>(p.part_o + (part_row + d) * D + col) = v;
                         } else if (d < left) {
                             const int i = ((rem0 + d) * p.gh_magic) >> 16;   // tokens from i0 on
-                            const size_t at = row0 + ((size_t)i * p.n_q_heads + (rem0 + d - i * p.gh)) * D + c0;
-                            if constexpr (F32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at + c * 4) = v;
-                            else *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + at + c * 8) = v;
+                            const size_t at = row0 + ((size_t)i * p.n_q_heads + (rem0 + d - i * p.gh)) * D + col;
+                            if constexpr (F32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at) = v;
+                            else *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + at) = v;
                         }
                     }
                     __syncwarp();
@@ -858,7 +931,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        if (j >= f.nt[g]) continue;
+                        if (DUAL ? (j & 1) != g : j >= f.nt[g]) continue;
                         if (j == 0 && !mbar_wait(bar(bars.q_full[g]), blocks[g]++ & 1, p.status)) {
                             ok = false;
                             break;
@@ -870,11 +943,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                         ++done[g];
                         tc_after_sync();
-                        const uint64_t a = dq + g * (C::Q_BYTES / 16), kd = dk + st * (C::KV_BYTES / 16);
+                        const uint64_t a = dq + (DUAL ? 0 : g) * (C::Q_BYTES / 16), kd = dk + st * (C::KV_BYTES / 16);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t k16 = kd + (kk / 4) * (BN * 128 / 16) + (kk % 4) * 2;
-                            if (C::Q0_TMEM && g == 0) umma_ts(tmem, tmem + C::COL_Q + kk * 8, k16, ID_S, kk > 0);
+                            if (C::Q0_TMEM && (DUAL || g == 0)) umma_ts(tmem + g * BN, tmem + C::COL_Q + kk * 8, k16, ID_S, kk > 0);
                             else umma(tmem + g * BN, a + (kk / 4) * (QT * 128 / 16) + (kk % 4) * 2, k16, ID_S, kk > 0);
                         }
                         umma_commit(bar(bars.s_full[g]));
@@ -908,7 +981,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        if (j >= f.nt[g]) continue;
+                        if (DUAL ? (j & 1) != g : j >= f.nt[g]) continue;
                         if (!mbar_wait(bar(bars.p_full[g]), done[g]++ & 1, p.status)) {
                             ok = false;
                             break;
@@ -918,7 +991,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
                             umma_ts(tmem + C::COL_O + g * D, tmem + C::COL_P + g * (BN / 2) + kk * 8, vd + kk * (2048 / 16),
-                                    ID_PV, j > 0 || kk > 0);
+                                    ID_PV, j > (DUAL ? 1 : 0) || kk > 0);
                         umma_commit(bar(bars.o_done[g]));
                     }
                     if (ok) umma_commit(bar(bars.v_empty[st]));
@@ -1019,8 +1092,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 f.last = b.last, f.sinks = b.sinks, f.sink_end = b.sink_end, f.skip = b.skip;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    f.lim[g] = b.lim[g];
-                    f.nt[g] = b.lim[g] < 0 ? 0 : min(max(b.lim[g] / BN + 1 - f.tile0, 0), f.tiles);
+                    f.lim[g] = b.lim[DUAL ? 0 : g];
+                    f.nt[g] = DUAL ? (f.tiles + 1 - g) / 2 : b.lim[g] < 0 ? 0 : min(max(b.lim[g] / BN + 1 - f.tile0, 0), f.tiles);
                 }
             } else if (round < rounds) {
                 continue;                                      // (the last round is short of this CTA)
@@ -1051,7 +1124,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 constexpr int kMergeWarps = 8;
 template <int D, int MASK>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_masked_kernel(const Params p) {
-    constexpr int BN = Cfg<D, false>::BN;
+    constexpr int BN = Cfg<D, false, false>::BN;
     constexpr int V = D / 32;                // values of a lane
     const int blk = (int)blockIdx.x;
     const int item = blk / p.n_qp, qp = blk - item * p.n_qp;
@@ -1115,16 +1188,18 @@ struct Kernels {
     void (*merge)(Params);   // of the parts, when contexts are cut
     int smem;
 };
-Kernels window_kernels(int D, bool q8, bool split);
-Kernels tree_kernels(int D, bool q8, bool split);
+Kernels window_kernels(int D, bool q8, bool split, bool dual);
+Kernels tree_kernels(int D, bool q8, bool split, bool dual);
 
+template <int MASK, int D, bool Q8>
+Kernels kernels_of(bool split, bool dual) {
+    const auto main = split ? (dual ? prompt_masked_kernel<D, Q8, true, MASK, true> : prompt_masked_kernel<D, Q8, true, MASK, false>)
+                            : (dual ? prompt_masked_kernel<D, Q8, false, MASK, true> : prompt_masked_kernel<D, Q8, false, MASK, false>);
+    return {main, merge_masked_kernel<D, MASK>, dual ? Cfg<D, Q8, true>::SMEM : Cfg<D, Q8, false>::SMEM};
+}
 template <int MASK, int D>
-Kernels kernels_of(bool q8, bool split) {
-    if (q8)
-        return {split ? prompt_masked_kernel<D, true, true, MASK> : prompt_masked_kernel<D, true, false, MASK>,
-                merge_masked_kernel<D, MASK>, Cfg<D, true>::SMEM};
-    return {split ? prompt_masked_kernel<D, false, true, MASK> : prompt_masked_kernel<D, false, false, MASK>,
-            merge_masked_kernel<D, MASK>, Cfg<D, false>::SMEM};
+Kernels kernels_of(bool q8, bool split, bool dual) {
+    return q8 ? kernels_of<MASK, D, true>(split, dual) : kernels_of<MASK, D, false>(split, dual);
 }
 
 }  // namespace prompt_masked

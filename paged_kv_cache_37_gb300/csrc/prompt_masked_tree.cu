@@ -4,8 +4,8 @@
 namespace pkv {
 namespace prompt_masked {
 
-Kernels tree_kernels(int D, bool q8, bool split) {
-    return D == 64 ? kernels_of<kMaskTree, 64>(q8, split) : kernels_of<kMaskTree, 128>(q8, split);
+Kernels tree_kernels(int D, bool q8, bool split, bool dual) {
+    return D == 64 ? kernels_of<kMaskTree, 64>(q8, split, dual) : kernels_of<kMaskTree, 128>(q8, split, dual);
 }
 
 }  // namespace prompt_masked

@@ -4,8 +4,8 @@
 namespace pkv {
 namespace prompt_masked {
 
-Kernels window_kernels(int D, bool q8, bool split) {
-    return D == 64 ? kernels_of<kMaskWindow, 64>(q8, split) : kernels_of<kMaskWindow, 128>(q8, split);
+Kernels window_kernels(int D, bool q8, bool split, bool dual) {
+    return D == 64 ? kernels_of<kMaskWindow, 64>(q8, split, dual) : kernels_of<kMaskWindow, 128>(q8, split, dual);
 }
 
 }  // namespace prompt_masked

@@ -107,9 +107,11 @@ def test_workspace_refusals(pkv):
 
 def test_bindings_refuse_shapes(pkv, monkeypatch):
     import torch
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    # (a host tensor's device is -1: as if that were the current one, every shape is looked at)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
     pool = SimpleNamespace(handle=None, n_layers=1, n_blocks=8, block_size=16, n_kv_heads=2, head_dim=128, k_scale=None,
-                           device=0)
+                           device=-1)
     q = torch.zeros((6, 4, 128), dtype=torch.float16)
     table, lens = torch.zeros((3, 2), dtype=torch.int32), torch.ones(3, dtype=torch.int32)
     cu, bits = torch.arange(0, 8, 2, dtype=torch.int32), torch.zeros((6, 1), dtype=torch.int64)
@@ -127,15 +129,23 @@ def test_bindings_refuse_shapes(pkv, monkeypatch):
     both("block_tables", table=table[0])
     both("block_tables", lens=lens[:2])
     both("cu_q", cu=cu[:3])
-    both("CUDA")
+    both("int32", table=table.long())
+    both("int32", cu=cu.long())
+    both("float16", q=q.float(), out=q)
+    both("contiguous", q=q.transpose(0, 1).contiguous().transpose(0, 1))
+    both("pool is null")
     with pytest.raises(pkv.PagedKVError, match="row per sequence"):
         pkv.pf_paged_window_attention(pool, 0, q, table, lens, None, 1, 0.1, 5, 1, q.clone())
     with pytest.raises(pkv.PagedKVError, match="cu_q"):
         pkv.pf_paged_tree_attention(pool, 0, q[:3], table, lens, None, 1, 0.1, bits[:3], q[:3].clone())
     with pytest.raises(pkv.PagedKVError, match="row per query"):
         pkv.pf_paged_tree_attention(pool, 0, q, table, lens, cu, 2, 0.1, bits[:5], q.clone())
+    with pytest.raises(pkv.PagedKVError, match="int64"):
+        pkv.pf_paged_tree_attention(pool, 0, q, table, lens, cu, 2, 0.1, bits.int(), q.clone())
     pool.device = 1
     both("current device")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    both("CUDA")
 
 
 def test_packed_bits():
