@@ -529,8 +529,9 @@ PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_
  * cu_q NULL: one query per sequence, row s, at position context_lens[s] - 1
  * (max_new_tokens 1: a decode step); zeros where the context is empty.
  * A block that holds only tokens that no query of the call sees is not the
- * sequence's to keep: it may be freed, and its table entry may hold anything.
- * Tokens of other blocks up to a sequence's last position have been written.
+ * sequence's to keep: it may be freed, and its table entry may hold anything.  Rows
+ * of such tokens in other blocks may hold anything too.  (What is not finite in a V
+ * row that one query sees can reach the sequence's other queries: 0 times it.)
  * Either pool type.  With a workspace (pf_window_workspace_bytes, initialised once
  * with pf_decode_workspace_init, not shared by overlapping calls; one made for
  * other windows will do) and at most 16 query rows (tokens x q-heads) per
@@ -555,6 +556,7 @@ PF_API size_t pf_window_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q
  * all L - n_s tokens before the drafts, and draft j where bit j % 64 of word
  * tree[cu_q[s] + i][j / 64] is set: its ancestors and itself, or whatever the bits
  * say (bits of j >= n_s do not count).  A draft that sees nothing gives zeros.
+ * (Every draft's K and V rows are written and finite, also of one that none sees.)
  *   out[row][hq][d] = sum_t softmax_t(scale * q . K[slot(s, t)][h]) V[..][h][d]
  * tree: device [T_q][tree_words], 8-byte aligned, 64 * tree_words at least
  * max_draft_tokens, which bounds every n_s.  Arguments, pool types, kernels and

@@ -167,6 +167,7 @@ struct Block {
     int lim[2];               // per query tile: its last virtual position (-1: no row)
     int last;                 // the block's
     int sinks, sink_end, skip;
+    int lo;                   // virtual tokens sinks .. lo - 1 are seen by no row
     int tiles;
 
     // bad: the call does not allow these lengths
@@ -190,7 +191,7 @@ struct Block {
         r0 = qp * ROWS;
         r_end = min(r0 + ROWS, rows);
         base = L - n;
-        sinks = sink_end = skip = 0;
+        sinks = sink_end = skip = lo = 0;
         lim[0] = lim[1] = last = -1;
         tiles = 0;
         if (r0 >= rows || L == 0) return;
@@ -201,12 +202,13 @@ struct Block {
         }
         last = max(lim[0], lim[1]);
         if constexpr (WINDOW) {
-            const int lo = max(0, base + r0 / p.gh - p.mask.window + 1);   // the first row's window
+            lo = max(0, base + r0 / p.gh - p.mask.window + 1);   // the first row's window
             sinks = min(p.mask.sinks, last + 1);
             const int units = (sinks + (1 << p.unit_shift) - 1) >> p.unit_shift;
             sink_end = units << p.unit_shift;
             skip = max(0, (lo >> p.unit_shift) - units) << p.unit_shift;
             last -= skip;
+            lo -= skip;
 #pragma unroll
             for (int g = 0; g < 2; ++g)
                 if (lim[g] >= 0) lim[g] -= skip;    // (no position before the window's start)
@@ -225,9 +227,11 @@ struct Info {
     int r0, r_end;
     int i0, rem0;             // r0 = i0 * gh + rem0
     int lim[2], nt[2];        // per query tile: last virtual position, tiles of this part
-    int last, sinks, sink_end, skip;
+    int last, sinks, sink_end, skip, lo;
     int tile0, tiles, n_parts;
     __device__ __forceinline__ int token(int x) const { return x >= sink_end ? x + skip : x; }
+    // some row of the block sees virtual token x (which is not past the last)
+    __device__ __forceinline__ bool seen(int x) const { return x < sinks || x >= lo; }
 };
 
 // What a softmax thread keeps of it, for its query tile.
@@ -245,7 +249,7 @@ struct Bars {
     unsigned long long p_full[2];
     unsigned long long o_done[2];
     unsigned long long q_full[2];
-    unsigned long long v_landed;     // a block's last V tile, for its loaders
+    unsigned long long v_landed;     // a V tile with rows to clear, for its loaders
     unsigned long long ml_full[2];     // DUAL: a group's maxima and sums are there
     unsigned long long o_read[2];      // DUAL: a group has read both products
     unsigned long long mma_done[2];
@@ -725,11 +729,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
                             id = 0;
                         }
-                        // The last V tile's rows past the last token become zeros (a
-                        // zero weight times a non-finite value would not vanish): it
-                        // lands on a barrier of its own first.
+                        // Rows of V past the last token, and others that no row sees,
+                        // become zeros (a zero weight times a non-finite value would not
+                        // vanish): such a tile lands on a barrier of its own first.
                         const int rows = last - x0 + 1;
-                        const bool ragged = is_v && rows < BN;
+                        const bool ragged = is_v && (rows < BN || (WINDOW && f.sinks < f.lo && f.sinks < x0 + BN && f.lo > x0));
                         const uint32_t on = bar(ragged ? bars.v_landed : full[st]);
                         if (lane == 0) mbar_arrive_expect_tx(on, (uint32_t)((nb + 1 - li) / 2) * box * D * 2);
                         __syncwarp();
@@ -745,8 +749,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                 break;
                             }
                             ++landed;
-                            for (int e = lane; e < (BN - rows) * 4 * C::HALVES; e += 32) {
-                                const int row = rows + e / (4 * C::HALVES), rest = e % (4 * C::HALVES) * 2 + li;
+                            const int from = WINDOW ? 0 : rows;
+                            for (int e = lane; e < (BN - from) * 4 * C::HALVES; e += 32) {
+                                const int row = from + e / (4 * C::HALVES), rest = e % (4 * C::HALVES) * 2 + li;
+                                if (WINDOW && row < rows && f.seen(x0 + row)) continue;
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
                                                  dst + ((rest / 8) * BN + row) * 128 + (rest % 8) * 16), "r"(0u)
                                              : "memory");
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int k = 0; k < IDS; ++k) {
                     const int x = (f.tile0 + j) * BN + tile_token(lane + 32 * k);
-                    q_id[k] = x <= last ? bt_row[f.token(x) >> p.block_shift] : -2;
+                    q_id[k] = x <= last && (!WINDOW || f.seen(x)) ? bt_row[f.token(x) >> p.block_shift] : -2;
                 }
             };
             // this lane's chunk 0 in a stage of codes, in the pool and in a swizzled
@@ -1089,7 +1095,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 f.q0 = b.q0, f.n = b.n, f.base = b.base, f.r0 = b.r0, f.r_end = b.r_end;
                 f.i0 = b.r0 / p.gh;
                 f.rem0 = b.r0 - f.i0 * p.gh;
-                f.last = b.last, f.sinks = b.sinks, f.sink_end = b.sink_end, f.skip = b.skip;
+                f.last = b.last, f.sinks = b.sinks, f.sink_end = b.sink_end, f.skip = b.skip, f.lo = b.lo;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     f.lim[g] = b.lim[DUAL ? 0 : g];

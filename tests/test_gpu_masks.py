@@ -47,9 +47,22 @@ class Ctx:
         return (self.c.bt if self.cache == "f16" else self.c.table)[s]
 
     def forget(self, seen, poison):
-        """Blocks that hold only tokens that no query sees: their entries hold anything,
-        and (fp16) their contents are not numbers."""
+        """What no query sees: rows hold no numbers; blocks of nothing else are gone, their entries
+        hold anything (poison: they stay in the table, with scales that are no numbers)."""
         gone = []
+        blk, at = [], []
+        for s, x in enumerate(seen):
+            L = int(self.lens[s])
+            t = np.flatnonzero(~x.any(0)) if len(x) else np.arange(L)
+            blk.append(self.table_as_made(s)[t // self.page])
+            at.append(t % self.page)
+        blk, at = (dev(np.concatenate(v).astype(np.int64), self.device) for v in (blk, at))
+        if self.cache == "f16":
+            for x in (self.c.k_dev, self.c.v_dev):
+                x[1, blk, at] = float("nan")
+        else:
+            for x in (self.c.k, self.c.v):
+                x.view(self.c.torch.uint8)[1, blk, at] = 0x7f
         for s, x in enumerate(seen):
             L = int(self.lens[s])
             any_row = x.any(0) if len(x) else np.zeros(L, bool)
@@ -60,12 +73,7 @@ class Ctx:
                         self.table[s, j] = 1 << 30
         if poison and gone:
             ids = dev(np.array(gone), self.device)
-            if self.cache == "f16":
-                for x in (self.c.k_dev, self.c.v_dev):
-                    x[1, ids] = float("nan")
-            else:
-                for x in (self.c.k, self.c.v):
-                    x.view(self.c.torch.uint8)[1, ids] = 0x7f
+            if self.cache == "e4m3":
                 for x in (self.c.ks, self.c.vs):
                     x[1, ids] = float("nan")
         return len(gone)
@@ -220,6 +228,7 @@ TREES = [
     ([9000], [200], 4, 2, 128, 64),
     ([4200, 65, 129], [70, 65, 3], 3, 1, 64, 1),
     ([300, 300], [300, 260], 1, 1, 64, 16),
+    ([1500, 900], [700, 1], 2, 1, 128, 16),
 ]
 
 
@@ -357,6 +366,63 @@ def test_far_blocks(pkv, cuda_dev):
                 out = torch.empty((n, 16, D), dtype=torch.float16, device=cuda_dev)
                 call(out, w)
                 assert_within(host(out), want, tol)
+
+
+@pytest.mark.parametrize("hq,d", [(1, 64), (16, 128), (3, 128)])
+@pytest.mark.parametrize("n", [1, 40])
+def test_very_long_context(pkv, cuda_dev, hq, d, n):
+    """A table that names the same eight pages over and over: a window of whole rounds of them and one
+    round of sinks, or drafts that see nothing but the context, give what those pages give once."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [8 * 256], hq, 1, d, 256)
+    rounds = 500
+    table = dev(np.concatenate([np.tile(c.bt, (1, rounds)), c.bt[:, :1]], 1), cuda_dev)
+    t = np.arange(8 * 256)
+    k, v = (x[0][c.bt[0][t // 256], t % 256] for x in (c.k_host, c.v_host))
+    rng = np.random.default_rng(1)
+    q = rng.standard_normal((n, hq, d)).astype(np.float16)
+    scale = float(np.float32(d ** -0.5))
+    want, tol = masked64(q, k, v, scale, np.ones((n, len(t)), bool), F16, F16)
+    # sums over 2^20 terms, not over the eight pages': at most 2^14 stages or tiles in order, each step off by
+    # 2^-23 of the sum, then 2^8 parts at most
+    tol = tol + np.abs(v.astype(np.float64)).mean() * 2 * (2.0 ** 14 + 2.0 ** 8) * 2.0 ** -23
+    L = rounds * len(t)
+    cu = dev(np.array([0, n], np.int32), cuda_dev)
+    ws = pkv.make_tree_workspace(c.pool, 1, hq, table.shape[1], n)
+    out = torch.empty((n, hq, d), dtype=torch.float16, device=cuda_dev)
+    pkv.pf_device_status(reset=True)
+    for w in (ws, None):
+        pkv.pf_paged_window_attention(c.pool, 0, dev(q, cuda_dev), table, dev(np.array([L], np.int32), cuda_dev), cu, n, scale,
+                                      400 * len(t), len(t), out, w)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out), want, tol)
+        bits = torch.zeros((n, 1), dtype=torch.int64, device=cuda_dev)
+        pkv.pf_paged_tree_attention(c.pool, 0, dev(q, cuda_dev), table, dev(np.array([L + n], np.int32), cuda_dev), cu, n, scale,
+                                    bits, out, w)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out), want, tol)
+
+
+def test_two_calls_at_once(pkv, cuda_dev):
+    """Calls on two streams over one pool, each with a workspace of its own."""
+    import torch
+    c = Ctx(pkv, cuda_dev, "e4m3", [3000, 500], 4, 2, 64, 16)
+    table, lens = dev(c.table, cuda_dev), dev(c.lens, cuda_dev)
+    jobs = []
+    for n, W in ((1, 700), (60, 1500), (3, 40), (200, 100)):
+        offs = offsets([n, n])
+        q = c.rng.standard_normal((2 * n, 4, 64)).astype(np.float16)
+        seen = [window_seen(L, n, W, 5) for L in c.lens]
+        jobs.append((n, W, dev(q, cuda_dev), dev(offs, cuda_dev), torch.empty((2 * n, 4, 64), dtype=torch.float16, device=cuda_dev),
+                     pkv.make_window_workspace(c.pool, 2, 4, table.shape[1], n, W, 5), torch.cuda.Stream(), *c.want(q, offs, seen, F16, F16)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for n, W, q, cu, out, ws, stream, _, _ in jobs:
+            pkv.pf_paged_window_attention(c.pool, 1, q, table, lens, cu, n, c.scale, W, 5, out, ws, stream=stream)
+    torch.cuda.synchronize()
+    for n, W, q, cu, out, ws, stream, want, tol in jobs:
+        assert_within(host(out), want, tol, f"{n} {W}")
+    assert pkv.pf_device_status(reset=True) == 0
 
 
 def test_replays_share_a_workspace(pkv, cuda_dev):

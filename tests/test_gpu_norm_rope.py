@@ -155,6 +155,31 @@ def test_k_out_beside_the_cache(pkv, cuda_dev):
     assert_within(host(r.out)[:-1], *rotated64(r.q, r.qw, 1e-6, r.angles, rope_pos, False))
 
 
+def test_keys_alone_into_the_cache(pkv, cuda_dev):
+    """Without queries, and with a norm of one kind only."""
+    r = Rows(pkv, cuda_dev, [90, 40], [12, 7], 4, 2, 64, 16)
+    pkv.pf_norm_rope_write(r.c.pool, 1, None, r.kd, r.vd, r.c.bt_dev, *r.ids, r.angles_dev, None)
+    r.check_cache(1, *rotated64(r.k, None, 0, r.angles, r.pos, False))
+    r = Rows(pkv, cuda_dev, [90, 40], [12, 7], 4, 2, 64, 16, packed=True)
+    pkv.pf_norm_rope_write(r.c.pool, 1, r.qd, r.kd, r.vd, r.c.bt_dev, *r.ids, r.angles_dev, r.out[:-1],
+                           k_weight=r.weights["k_weight"], eps=0.0)
+    r.check_cache(1, *rotated64(r.k, r.kw, 0.0, r.angles, r.pos, False))
+    assert_within(host(r.out)[:-1], *rotated64(r.q, None, 0, r.angles, r.pos, False))
+
+
+def test_broadcast_rows(pkv, cuda_dev):
+    """One token's rows for all positions (a stride of 0 between tokens)."""
+    import torch
+    r = Rows(pkv, cuda_dev, [30], [9], 3, 3, 128, 16)
+    one = r.qd[:1].expand(9, 3, 128)
+    out = torch.empty((9, 3, 128), dtype=torch.float16, device=cuda_dev)
+    pkv.pf_norm_rope_write(r.c.pool, 0, one, r.kd[:1].expand(9, 3, 128), r.vd, r.c.bt_dev, *r.ids, r.angles_dev, out)
+    want, tol = rotated64(np.repeat(r.q[:1], 9, 0), None, 0, r.angles, r.pos, False)
+    assert_within(host(out), want, tol)
+    with pytest.raises(pkv.PagedKVError, match="overlap"):
+        pkv.pf_norm_rope_write(r.c.pool, 0, r.qd, None, None, None, None, None, r.angles_dev, one, rope_pos=r.ids[1])
+
+
 def test_flags(pkv, cuda_dev):
     """Bad positions and blocks are flagged; their rows stay as they were, all others are written."""
     pkv.pf_device_status(reset=True)
