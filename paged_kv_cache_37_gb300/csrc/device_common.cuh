@@ -66,15 +66,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Wait until the phase with the given parity has completed.  Bounded: after
-// kWaitLimitNs it ORs PF_DEV_WAIT_TIMEOUT into *status and returns false.
+// limit_ns it ORs PF_DEV_WAIT_TIMEOUT into *status and returns false.
 // sleep_ns > 0 backs off between polls (for waits off the critical path).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *status, uint32_t sleep_ns = 0) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *status, uint32_t sleep_ns = 0,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     unsigned long long t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
         if (sleep_ns) __nanosleep(sleep_ns);
         if (mbar_try_wait(bar, parity)) return true;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             atomicOr(status, PF_DEV_WAIT_TIMEOUT);
             return false;
         }

@@ -1052,6 +1052,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Work next = work_at(0);
         Seq next_seq = seq_of(next);
         unsigned k = 0;
+        int longest = 0;                                       // tiles
         for (int round = 0; round <= rounds; ++round) {
             const Work w = next;
             const Seq seq = next_seq;
@@ -1105,7 +1106,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 continue;                                      // (the last round is short of this CTA)
             }
             const unsigned slot = k % kInfos;
-            if (k >= kInfos && !wait_lanes(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1, p.status)) break;
+            // The one wait that lasts as long as a block does (the others: a tile):
+            // its limit leaves 15 us for each tile of the longest.
+            if (k >= kInfos && !__all_sync(FULL, mbar_wait(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1, p.status, 0,
+                                                           kWaitLimitNs * (1 + longest / 65536))))
+                break;
+            longest = max(longest, f.tiles);
             if (lane == 0) {
                 infos[slot] = f;
                 mbar_arrive(bar(bars.info_full[slot]));

@@ -403,6 +403,25 @@ def test_very_long_context(pkv, cuda_dev, hq, d, n):
         assert_within(host(out), want, tol)
 
 
+def test_blocks_of_more_than_a_second(pkv, cuda_dev):
+    """Six blocks of rows one after another for each SM, over 140 million tokens each (eight pages, over and over)."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [8 * 256], 16, 1, 128, 256)
+    c.v_dev.fill_(0.75)
+    rounds = 70000
+    table = dev(c.bt, cuda_dev).repeat(1, rounds)
+    n = 16 * torch.cuda.get_device_properties(cuda_dev).multi_processor_count * 5 + 16
+    q = torch.randn((n, 16, 128), dtype=torch.float16, device=cuda_dev)
+    out = torch.full_like(q, float("nan"))
+    cu = dev(np.array([0, n], np.int32), cuda_dev)
+    L = rounds * 8 * 256
+    pkv.pf_device_status(reset=True)
+    pkv.pf_paged_window_attention(c.pool, 0, q, table, dev(np.array([L], np.int32), cuda_dev), cu, n, 128 ** -0.5, L, 0, out)
+    assert pkv.pf_device_status(reset=True) == 0
+    # every row is there (sums of so many tokens in fp32 are not to be exact)
+    assert bool((out > 0).all()) and bool((out < 1.5).all())
+
+
 def test_two_calls_at_once(pkv, cuda_dev):
     """Calls on two streams over one pool, each with a workspace of its own."""
     import torch
