@@ -1013,19 +1013,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         wait_lanes(bar(bars.mma_done[1]), 0, p.status);
     } else if (warp == INFO_WARP) {
         // ----------------------------------------------- what the blocks are
-        // Work w: part w mod splits of block w / splits.  Round k of the CTAs goes
-        // up or down over the next gridDim.x of them.
+        // Work w: part w mod splits of block w / splits, the longest blocks first.  Of
+        // n = (rounds - 1) grid + few, the first (rounds - 1) (grid - few) go to
+        // grid - few CTAs, rounds - 1 each, and the last rounds x few to `few` CTAs, to
+        // and fro over either: who takes a block more takes the short ones.
+        const int grid = (int)gridDim.x, rounds = (p.n_work - 1) / grid + 1, few = p.n_work - (rounds - 1) * grid;
+        const bool more = (int)blockIdx.x >= grid - few;
+        const int mine = more ? rounds : rounds - 1, width = more ? few : grid - few;
+        const int col = more ? (int)blockIdx.x - (grid - few) : (int)blockIdx.x;
+        const int first = more ? (rounds - 1) * (grid - few) : 0;
         struct Work {
             int s, h, qp, part, blk;                           // blk < 0: none
         };
         auto work_at = [&](int round) {
             Work w;
-            const long long at = (long long)round * gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
             w.blk = -1;
             w.s = w.h = w.qp = w.part = 0;
-            if (at >= p.n_work) return w;
-            const int b = SPLIT ? (int)at / p.splits : (int)at;
-            w.part = SPLIT ? (int)at - b * p.splits : 0;
+            if (round >= mine) return w;
+            const int at = first + round * width + (round & 1 ? width - 1 - col : col);
+            const int b = SPLIT ? at / p.splits : at;
+            w.part = SPLIT ? at - b * p.splits : 0;
             if (TREE) {                                        // by sequences
                 const int per = p.n_kv_heads * p.n_qp, rank = b / per, rest = b - rank * per;
                 w.s = ordered ? order[rank] : rank;
@@ -1048,12 +1055,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             q.q1 = step ? w.s + 1 : p.cu_q[w.s + 1];
             return q;
         };
-        const int rounds = (int)(((long long)p.n_work + gridDim.x - 1) / gridDim.x);
         Work next = work_at(0);
         Seq next_seq = seq_of(next);
         unsigned k = 0;
         int longest = 0;                                       // tiles
-        for (int round = 0; round <= rounds; ++round) {
+        for (int round = 0; round <= mine; ++round) {
             const Work w = next;
             const Seq seq = next_seq;
             next = work_at(round + 1);
@@ -1102,8 +1108,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     f.lim[g] = b.lim[DUAL ? 0 : g];
                     f.nt[g] = DUAL ? (f.tiles + 1 - g) / 2 : b.lim[g] < 0 ? 0 : min(max(b.lim[g] / BN + 1 - f.tile0, 0), f.tiles);
                 }
-            } else if (round < rounds) {
-                continue;                                      // (the last round is short of this CTA)
             }
             const unsigned slot = k % kInfos;
             // The one wait that lasts as long as a block does (the others: a tile):
