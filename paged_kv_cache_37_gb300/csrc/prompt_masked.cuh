@@ -34,7 +34,8 @@
 // Calls of at most 128 rows per (sequence, kv-head) (DUAL) have one query tile a
 // block: the two groups of softmax warps take its even and its odd tiles, each
 // with a maximum, a sum and an O of its own, and join them at the block's end, half
-// of the dims each.
+// of the dims each.  A 64-token tile, 16 blocks that stay in L2: fp16 x 128 0.56 us,
+// 0.76 with both query tiles; fp16 x 64 0.33 and 0.62; e4m3 x 128 0.73 and 0.99.
 //
 // Per tile (see prefill_tc.cu): scores in tensor memory, a running maximum per row
 // in the log2 domain that is raised only past 2^8, weights rounded to fp16 into
@@ -42,16 +43,18 @@
 // a part or (tree) at all: its maximum stays -inf, its sum 0, its output zeros.
 //
 // Measured (GB300; 4 prompts of 4,096 tokens, 32 q-heads over 8 kv-heads x 128,
-// window 512, 4 sinks): 140 us.  A CTA per block took 205, of which 6.4 us a block
+// window 512, 4 sinks): 142 us, 902 TFLOP/s, tensor pipe busy 47 % of the cycles.  A CTA per block took 205, of which 6.4 us a block
 // beside 0.76 us a tile (blocks of 4, 10 and 18 tiles): the chain lengths, block
 // ids, rows, scores, weights, product, output, of which nothing overlapped.  Two
 // CTAs of 128 rows per SM instead took 198 (each is such a chain).  Here the query
 // rows fetched by warps of their own took 203, by the softmax warps 168; with the
 // blocks' lengths and divisions left to warp 14, and query tile 0 read from tensor
-// memory, 140.  The latter because at head_dim 128 a tile was bound by shared
-// memory: with 64 tokens on the N side an MMA of the scores reads 6 KB for 32 cycles
-// of products, and a tile moved 160 KB, 1,280 cycles at 128 bytes; it took 1,300.
-// Two softmax warps per 32 rows were slower (188): nothing waits for the softmax there.
+// memory, 140.  The latter fits a bound by shared memory at head_dim 128: with
+// 64 tokens on the N side an MMA of the scores reads 6 KB for 32 cycles of products,
+// and a tile moved 160 KB, 1,280 cycles at 128 bytes; it took 1,300.  Two softmax
+// warps per 32 rows were slower (188).  Trees of 100 to 200 drafts (8 sequences of
+// 1,024 to 2,048 tokens, 40 heads x 128): 60 us, 4.6 TB/s, 69.9 before CTAs
+// that take a block more took the short ones.
 #pragma once
 
 #include <type_traits>
