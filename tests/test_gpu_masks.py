@@ -487,7 +487,7 @@ def test_replays_share_a_workspace(pkv, cuda_dev):
 
 @pytest.mark.parametrize("cache", ["f16", "e4m3"])
 def test_a_layer_with_drafts(pkv, cuda_dev, cache):
-    """The calls together, as a checker of drafts uses them: the prompt rotated, written and attended under a
+    """The calls together, as drafts are checked with them: the prompt rotated, written and attended under a
     window; drafts rotated for their depth, written and attended as a tree; the accepted path written again
     where it belongs; a decode step over the result."""
     import torch
