@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <new>
@@ -430,17 +431,42 @@ static bool prompt_kernel_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
     const long long waves = (items + a.plan.sms - 1) / a.plan.sms;
     const int step = a.pool->head_dim == 64 ? 128 : 64;
     long long steps = ((long long)a.max_blocks * a.pool->block_size + step - 1) / step;
-    if (a.mask.kind == pkv::kMaskWindow)   // a block's: its sinks, and its window (and one of either is cut)
-        steps = std::min(steps, (a.mask.sinks + step - 1ll) / step + (a.mask.window + step - 1ll) / step + 1);
     if (a.pool->block_size < 16 && a.pool->dtype == PF_F16) steps *= 2;
     if (!wide_rows(a.pool, a.rows)) return waves == 1 && steps <= 8;
     if (waves > 1) return waves == 2 && steps <= (a.rows * a.pool->head_dim > 1024 ? 8 : 4);
-    const int tokens = a.rows / (a.n_q_heads / a.pool->n_kv_heads);
-    const int parts = a.mask.kind == pkv::kMaskNone
-                          ? pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks, tokens,
-                                               a.plan.sms, ws_bytes)
-                          : pkv::masked_splits(a.pool, a.mask, a.n_seqs, a.n_q_heads, a.max_blocks, tokens, a.plan.sms, ws_bytes);
-    return steps <= 32 || parts > 1;
+    return steps <= 32 || pkv::prompt_splits(a.pool, a.causal && a.cu_q, a.n_seqs, a.n_q_heads, a.max_blocks,
+                                             a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes) > 1;
+}
+
+// The same for calls under a mask, whose prompt kernel stays on the SMs: its later
+// waves cost less.  Both kernels' microseconds at the longest contexts (a
+// window's tokens), fitted to 8 kv-heads, 1 to 16 rows, 4 to 64 sequences, 128 to
+// 2,112 tokens seen, both head_dims and types, pages of 1 and 16 (272 cases): the
+// choice costs 0.4 % on average and 28 % at most.  Few-rows kernel / prompt kernel: 16 sequences, window
+// 2,048, 16 rows x 128 fp16 52.4 / 29.1, 1 row 32.0 / 28.9, x 64 17.8 / 18.5; 64
+// sequences, window 512, 16 rows x 128 45.3 / 37.8, 7 rows 34.6 / 37.7, 1 row x 64 16.1 /
+// 29.5; 32 trees of 16 drafts, 1,024 tokens, x 128 e4m3 39.7 / 30.0, x 64 23.4 / 25.1.
+static bool masked_prompt_pays(const pkv::RowsArgs &a, size_t ws_bytes) {
+    if (a.out_dtype != PF_F16) return false;
+    const int D = a.pool->head_dim;
+    const bool q8 = a.pool->dtype == PF_E4M3;
+    const long long items = (long long)a.n_seqs * a.pool->n_kv_heads;
+    const long long waves = (items + a.plan.sms - 1) / a.plan.sms;
+    const int tile = D == 64 ? 128 : 64;
+    long long tiles = ((long long)a.max_blocks * a.pool->block_size + tile - 1) / tile;
+    if (a.mask.kind == pkv::kMaskWindow)   // a block's: its sinks, and its window (and one of either is cut)
+        tiles = std::min(tiles, (a.mask.sinks + tile - 1ll) / tile + (a.mask.window + tile - 1ll) / tile + 1);
+    const double tokens = (double)(tiles * tile), bytes = (double)items * tokens * D * (q8 ? 2 : 4);
+    if (a.pool->block_size < 16 && !q8) tiles *= 2;
+    const int parts = pkv::masked_splits(a.pool, a.mask, a.n_seqs, a.n_q_heads, a.max_blocks,
+                                         a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.plan.sms, ws_bytes);
+    const double per_tile = q8 ? (D == 64 ? 1.15 : 0.8) : (D == 64 ? 0.75 : 0.67);
+    const double prompt = parts > 1 ? 10.5 + per_tile * (double)((tiles + parts - 1) / parts)
+                                    : 4.5 + (double)waves * (2.3 + per_tile * (double)tiles);
+    const double doublings = std::max(0.0, std::log2(tokens / 160.0));
+    const double more_rows = std::max(0, a.rows * D - 300) * 1e-3 * (7.0 + 0.6 * doublings * doublings);
+    const double few = std::max(10.0 + std::min(5.0, 2.0 * doublings) + more_rows, 10.0 + bytes / 7e6 + 0.65 * more_rows);
+    return prompt < few;
 }
 
 // The few-rows kernel with a checked workspace (decode and short appends over
@@ -456,7 +482,7 @@ static int rows_call(pkv::RowsArgs &a, void *workspace, size_t ws_bytes, const c
     if (ws_bytes < a.plan.bytes)
         return pkv::set_error(PF_ERR_INVALID, std::string(fn) + ": workspace has " + std::to_string(ws_bytes) +
                                                   " bytes, needs " + std::to_string(a.plan.bytes));
-    if (prompt_kernel_pays(a, ws_bytes)) {
+    if (a.mask.kind == pkv::kMaskNone ? prompt_kernel_pays(a, ws_bytes) : masked_prompt_pays(a, ws_bytes)) {
         pkv::PrefillArgs b{a.pool, a.layer, a.q, a.block_tables, a.max_blocks, a.context_lens, a.cu_q, a.n_seqs,
                            a.rows / (a.n_q_heads / a.pool->n_kv_heads), a.n_q_heads, a.scale, a.out, a.out_dtype,
                            a.causal && a.cu_q, workspace, ws_bytes, a.mask};
