@@ -109,7 +109,7 @@ static int pool_create(pf_pool **out, void *k_base, void *v_base, float *k_scale
     p->dtype = dtype;
     for (int i = 0; i < pkv::kMaxDevices; ++i) {
         for (int j = 0; j < 6; ++j) p->tmap_ready[i][j] = false;
-        p->tmap_pf_ready[i][0] = p->tmap_pf_ready[i][1] = false;
+        p->tmap_pf_ready[i][0] = p->tmap_pf_ready[i][1] = p->tmap_pf_ready[i][2] = false;
     }
     *out = p;
     return PF_OK;

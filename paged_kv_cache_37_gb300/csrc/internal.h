@@ -66,11 +66,11 @@ struct pf_pool {
     CUtensorMap tmap_k[pkv::kMaxDevices][6];
     CUtensorMap tmap_v[pkv::kMaxDevices][6];
     // per device: the prompt kernels' boxes (one 64-element half of up to a
-    // page of rows of one kv-head, swizzled), at most a tile of prefill_tc.cu, and
-    // at most a tile of prompt_masked.cuh
-    bool tmap_pf_ready[pkv::kMaxDevices][2];
-    CUtensorMap tmap_pf_k[pkv::kMaxDevices][2];
-    CUtensorMap tmap_pf_v[pkv::kMaxDevices][2];
+    // page of rows of one kv-head, swizzled): at most a tile of prefill_tc.cu, 16
+    // rows, at most a tile of prompt_masked.cuh
+    bool tmap_pf_ready[pkv::kMaxDevices][3];
+    CUtensorMap tmap_pf_k[pkv::kMaxDevices][3];
+    CUtensorMap tmap_pf_v[pkv::kMaxDevices][3];
 };
 
 namespace pkv {

@@ -12,11 +12,17 @@ int tile_tokens(const pf_pool *pool) {
     return pool->head_dim == 64 ? prompt_masked::Cfg<64, false, false>::BN : prompt_masked::Cfg<128, false, false>::BN;
 }
 
-// Rows that are looked up and copied together: what a page holds of a tile (the
-// TMA boxes of fp16 pools), 16 of e4m3 pages.
-int unit_rows(const pf_pool *pool) {
+// Rows that are looked up and copied together (the TMA boxes of fp16 pools): 16 of
+// e4m3 pages and under windows, whose blocks walk whole boxes from their first token
+// on, otherwise what a page holds of a tile.  Boxes of 16 / 64 rows of pages of 64: 4
+// prompts of 4,096 tokens, window 512, 32 q-heads over 8 kv-heads x 128 142 / 154 us; a tile of
+// one query tile (dual) 0.56 / 0.50 us, so that long windows of those take the
+// larger; with two query tiles 0.75 either way.
+constexpr int kSmallBoxWindow = 512;
+int unit_rows(const pf_pool *pool, const AttnMask &mask, bool dual) {
     if (pool->block_size < 16) return 1;
-    return pool->dtype == PF_E4M3 ? 16 : std::min(pool->block_size, tile_tokens(pool));
+    if (pool->dtype == PF_E4M3 || (mask.kind == kMaskWindow && !(dual && mask.window > kSmallBoxWindow))) return 16;
+    return std::min(pool->block_size, tile_tokens(pool));
 }
 
 // Workspace of a block's part.
@@ -41,7 +47,7 @@ int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q
     long long tokens = (long long)max_blocks * pool->block_size;
     if (mask.kind == kMaskWindow)   // of a block: its sinks, and its rows' windows
         tokens = std::min(tokens, (long long)mask.sinks + mask.window + std::min<long long>(max_new, prompt_masked::ROWS / group + 1) +
-                                      2 * unit_rows(pool));
+                                      2 * unit_rows(pool, mask, all_rows <= prompt_masked::QT));
     const long long tiles = (tokens + tile_tokens(pool) - 1) / tile_tokens(pool);
     const long long room = ws_bytes < kWorkspaceFront ? 0 : (long long)((ws_bytes - kWorkspaceFront) / part_bytes(pool));
     const long long n = std::min(std::min(std::min((long long)sms, room) / blocks, tiles / prompt_masked::kMinTiles),
@@ -73,6 +79,11 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     const long long n_items = (long long)a.n_seqs * pool->n_kv_heads;
     const long long n_qp = (rows + prompt_masked::ROWS - 1) / prompt_masked::ROWS;
     const long long blocks = n_items * n_qp;
+    // One query tile a block: both softmax groups take its tiles, even and odd.  With
+    // the second group idle instead, 32 sequences of 256 to 2,048 tokens, 8 kv-heads,
+    // 12 to 32 drafts x 4 q-heads: x 64 28.9 us for 22.7, x 128 36.9 for 36.3, e4m3 x
+    // 128 40.5 for 39.3.  (More rows need both query tiles.)
+    const bool dual = rows <= prompt_masked::QT;
     if (blocks > 0x7fffffffll) return set_error(PF_ERR_INVALID, "attention: too many query tiles for one launch");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -80,7 +91,8 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     if (dev < 0 || dev >= kMaxDevices) return set_error(PF_ERR_UNSUPPORTED, "device index out of range");
     int rc = device_sms(true, &sms);
     if (rc) return rc;
-    if (!q8 && (rc = encode_prompt_tmaps(pool, dev, 1, unit_rows(pool))) != PF_OK) return rc;   // e4m3 tiles are not copied by TMA
+    const int unit = unit_rows(pool, a.mask, dual), boxes = unit == 16 ? 1 : 2;
+    if (!q8 && (rc = encode_prompt_tmaps(pool, dev, boxes, unit)) != PF_OK) return rc;   // e4m3 tiles are not copied by TMA
     prompt_masked::Params p;
     p.q = static_cast<const __half *>(a.q);
     p.k_pool = pool->k_base;
@@ -103,7 +115,7 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     p.block_shift = 0;
     while ((1 << p.block_shift) < pool->block_size) ++p.block_shift;
     p.unit_shift = 0;
-    while ((1 << p.unit_shift) < unit_rows(pool)) ++p.unit_shift;
+    while ((1 << p.unit_shift) < unit) ++p.unit_shift;
     p.n_seqs = a.n_seqs;
     p.n_items = (int)n_items;
     p.n_qp = (int)n_qp;
@@ -121,11 +133,6 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
         p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)blocks * p.splits * prompt_masked::ROWS);
     }
     const bool split = p.splits > 1;
-    // One query tile a block: both softmax groups take its tiles, even and odd.  With
-    // the second group idle instead, 32 sequences of 256 to 2,048 tokens, 8 kv-heads,
-    // 12 to 32 drafts x 4 q-heads: x 64 28.9 us for 22.7, x 128 36.9 for 36.3, e4m3 x
-    // 128 40.5 for 39.3.  (More rows need both query tiles.)
-    const bool dual = rows <= prompt_masked::QT;
     p.n_work = (int)(blocks * p.splits);     // (cut: no more than SMs)
     const prompt_masked::Kernels k = a.mask.kind == kMaskWindow ? prompt_masked::window_kernels(D, q8, split, dual)
                                                                 : prompt_masked::tree_kernels(D, q8, split, dual);
@@ -138,7 +145,7 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
         done.store(true, std::memory_order_release);
     }
     const unsigned grid = (unsigned)std::min(p.n_work, sms);
-    k.main<<<grid, prompt_masked::NTHREADS, k.smem, stream>>>(pool->tmap_pf_k[dev][1], pool->tmap_pf_v[dev][1], p);
+    k.main<<<grid, prompt_masked::NTHREADS, k.smem, stream>>>(pool->tmap_pf_k[dev][boxes], pool->tmap_pf_v[dev][boxes], p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_error(e, "attention: launch");
     if (split) {
