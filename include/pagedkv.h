@@ -537,7 +537,7 @@ PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_
  * other windows will do) and at most 16 query rows (tokens x q-heads) per
  * kv-head, the kernel and the roundings of pf_paged_cross_attention's few rows
  * (fp32 output with the weights to about 22 bits); otherwise, and for fp16 output
- * of small batches, the tcgen05 kernel, the weights rounded to fp16, which with a
+ * where it is the faster, the tcgen05 kernel, the weights rounded to fp16, which with a
  * workspace cuts long windows of few blocks over the SMs.  A max_new_tokens above
  * what the table holds counts as that. */
 PF_API int pf_paged_window_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,

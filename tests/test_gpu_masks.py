@@ -174,7 +174,7 @@ def test_window(pkv, cuda_dev, lens, new, hq, h, d, page, W, S, cache, f32, ws):
 @pytest.mark.parametrize("lens,new,hq,h,d,page,W,S", WINDOWS)
 @pytest.mark.parametrize("cache", ["f16", "e4m3"])
 def test_window_wide_table(pkv, cuda_dev, lens, new, hq, h, d, page, W, S, cache):
-    """Tables much wider than the contexts (few rows: the few-rows kernel; more: parts that have no tiles),
+    """Tables much wider than the contexts (more than a few rows: parts that have no tiles),
     and unseen blocks that are in the table but hold no numbers."""
     window_case(pkv, cuda_dev, cache, lens, new, hq, h, d, page, W, S, False, True, wide=True, poison=True)
 
