@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // copy) and copies the scales of the warp's tokens l, l + 32 (in order).
     const uint32_t raw = smem_addr(sm + C::OFF_RAW) + (is_v ? kRawStages * C::RAW_BYTES : 0);
     const float *scale_base = is_v ? p.v_scale : p.k_scale;
-    int q_id[IDS];                                           // raw ids of the next tile to copy (-2: no token)
+    int q_id[IDS];                                           // raw ids of the next tile to copy (any number; -2 past the last token)
     auto q8_look_up = [&](int j) {
 #pragma unroll
         for (int k = 0; k < IDS; ++k) {
@@ -445,8 +445,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int k = 0; k < IDS; ++k) {
                 const int id = q_id[k], lt = lane + 32 * k;
                 const bool ok = (unsigned)id < (unsigned)p.n_blocks;
-                if (!ok && id != -2) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
-                row[k] = ok ? (int)p.layer_row0 + (id << p.block_shift) + ((tok0 + j * BN + tile_token(lt)) & (B - 1)) : -1;
+                const int tok = j * BN + tile_token(lt);
+                if (!ok && tok <= p_max) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                row[k] = ok ? (int)p.layer_row0 + (id << p.block_shift) + ((tok0 + tok) & (B - 1)) : -1;
                 whole = whole && ok;
                 cp_async4_zfill(dst + BN * D + (li * TW + lt) * 4,
                                 scale_base + (ok ? (size_t)(unsigned)((int)p.layer_page0 + id) * p.n_kv_heads + h : 0),

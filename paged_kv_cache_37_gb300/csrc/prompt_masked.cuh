@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             auto tile_token = [&](int lt) { return lt / TPI * (2 * TPI) + li * TPI + lt % TPI; };
             const uint32_t raw = smem_addr(sm + C::OFF_RAW) + (is_v ? C::RAW * C::RAW_BYTES : 0);
             const float *scale_base = is_v ? p.v_scale : p.k_scale;
-            int q_id[IDS];                                     // raw ids of the next tile to copy (-2: no token)
+            int q_id[IDS];                                     // raw ids of the next tile to copy (any number; -2 where no row sees the token)
             auto look_up = [&](int j) {
 #pragma unroll
                 for (int k = 0; k < IDS; ++k) {
@@ -837,10 +837,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     for (int k = 0; k < IDS; ++k) {
                         const int id = q_id[k], lt = lane + 32 * k;
                         const bool good = (unsigned)id < (unsigned)p.n_blocks;
-                        if (!good && id != -2) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
-                        row[k] = good ? (int)p.layer_row0 + (id << p.block_shift) +
-                                            (f.token((f.tile0 + j) * BN + tile_token(lt)) & (B - 1))
-                                      : -1;
+                        const int x = (f.tile0 + j) * BN + tile_token(lt);
+                        if (!good && x <= last && (!WINDOW || f.seen(x))) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                        row[k] = good ? (int)p.layer_row0 + (id << p.block_shift) + (f.token(x) & (B - 1)) : -1;
                         whole = whole && good;
                         cp_async4_zfill(dst + BN * D + (li * TW + lt) * 4,
                                         scale_base + (good ? (size_t)(unsigned)((int)p.layer_page0 + id) * p.n_kv_heads + h : 0),

@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
     constexpr int KSTEP = Q8 ? TI / 2 : TI;
     auto v_xor = [](int i) { return RB == 64 ? 0u : (uint32_t)((i * TI) & 7) << 4; };
     // A stage to copy.  PAGED: lane l holds the block id of tile (l / 2) mod
-    // U; otherwise that of token l mod ST (-2: no such token).
+    // U; otherwise that of token l mod ST.  What is not looked up has no id
+    // (a table may hold any number): -2 there.
     struct Ahead {
         int id, tok0, h, n;              // first token, kv-head, tokens (0: nothing to copy)
         int lo, sinks;                   // WINDOW: of these the first, and those from lo on, are seen
@@ -539,7 +540,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                     const int id = __shfl_sync(FULL, a.id, 2 * u);
                     int left = a.n - 16 * u;
                     if ((unsigned)id >= (unsigned)p.n_blocks) {
-                        if (left > 0 && lane == 0 && !(WINDOW && id == -2)) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                        const bool looked_up = left > 0 && (!WINDOW || 16 * u + 15 >= a.lo || 16 * u < a.sinks);
+                        if (looked_up && lane == 0) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
                         left = 0;
                     }
                     const bool whole = left >= 16 && (!WINDOW || 16 * u >= a.lo || 16 * u + 16 <= a.sinks);
@@ -579,7 +581,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, PAGED>::THREADS, 1) rows_atten
                 }
             } else {
                 const bool ok = (unsigned)a.id < (unsigned)p.n_blocks;
-                if (!ok && a.id != -2) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
+                const int i0 = lane & (ST - 1);
+                if (!ok && i0 < a.n && (!WINDOW || i0 >= a.lo || i0 < a.sinks)) atomicOr(p.status, PF_DEV_BAD_BLOCK_ID);
                 const int row = ok ? (int)(p.layer_row0 + a.id) : -1;
 #pragma unroll
                 for (int i = 0; i < ST / TI; ++i) {
