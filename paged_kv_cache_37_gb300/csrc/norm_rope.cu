@@ -245,22 +245,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p)
         for (int i = 0; i < 4; ++i) {
             uint64_t v = mul2(y[i], A[i]);
             if (p.rot) {
-                // (lanes that do not turn take no partner: infinities stay theirs)
-                uint64_t q = 0;
+                // (lanes that do not turn take and add nothing: infinities stay
+                // their rows', zeros keep their signs)
                 if (INTERLEAVED) {
-                    if (turns) q = swapped(y[i]);
+                    if (turns) v = fma2(swapped(y[i]), B[i], v);
                 } else {
                     const uint32_t bits = __shfl_sync(group, in[i], partner, CPR);
-                    if (turns) q = widen(bits);
+                    if (turns) v = fma2(widen(bits), B[i], v);
                 }
-                v = fma2(q, B[i], v);
             }
             if (weight) v = mul2(v, inv);
             const float2 o = both(v);
             const __half2 h = __floats2half2_rn(o.x, o.y);
             out[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        store(r, make_uint4(out[0], out[1], out[2], out[3]));
+        // neither normed nor turned: as they are, NaNs too
+        store(r, weight || turns ? make_uint4(out[0], out[1], out[2], out[3]) : x[r]);
     }
 }
 

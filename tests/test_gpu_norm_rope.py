@@ -299,3 +299,29 @@ def test_far_blocks_and_wide_rows(pkv, cuda_dev):
     for i, (blk, at) in enumerate(((n_blocks - 1, 0), (n_blocks - 1, 255), (n_blocks - 2, 87))):
         assert_within(host(k[0, blk, at])[None], *rotated64(rows[i:i + 1, 8:16], None, 0, host(angles), pos[i:i + 1], False))
         assert np.array_equal(host(v[0, blk, at]), rows[i, 16:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [0, 16, 48])
+def test_values_outside_the_rotated_part_stay_as_they_are(pkv, cuda_dev, d, interleaved, rot):
+    """Without a norm bit for bit: every fp16 number, zeros of either sign, infinities and NaNs; with one a
+    zero keeps its sign."""
+    import torch
+    T = 65536 // (d - rot) + 1
+    r = Rows(pkv, cuda_dev, [T], [T], 2, 1, d, 16, norm=True, rot=rot)
+    every = np.resize(np.arange(65536, dtype=np.uint16), T * (d - rot)).reshape(T, 1, d - rot)
+    bits, kbits = r.q.view(np.uint16).copy(), r.k.view(np.uint16).copy()
+    bits[..., rot:], kbits[..., rot:] = every, every
+    q, k = (dev(x.view(np.float16), cuda_dev) for x in (bits, kbits))
+    pkv.pf_norm_rope_write(r.c.pool, 1, q, k, r.vd, r.c.bt_dev, *r.ids, r.angles_dev, r.out[:-1], interleaved=interleaved)
+    assert np.array_equal(host(r.out)[:-1, :, rot:].view(np.uint16), bits[..., rot:])
+    blk, at = r.slots()
+    assert np.array_equal(host(r.c.k_dev)[1, blk, at][..., rot:].view(np.uint16), kbits[..., rot:])
+    zeros = np.zeros((T, 2, d), np.float16)
+    zeros[:, 1] = -0.0
+    zeros[..., 0] = 1
+    pkv.pf_norm_rope_write(r.c.pool, 1, dev(zeros, cuda_dev), None, None, None, None, r.ids[1], r.angles_dev, r.out[:-1],
+                           interleaved=interleaved, q_weight=torch.ones(d, device=cuda_dev))
+    out = host(r.out)[:-1, :, max(rot, 1):]
+    assert not out.any() and not np.signbit(out[:, 0]).any() and np.signbit(out[:, 1]).all()
