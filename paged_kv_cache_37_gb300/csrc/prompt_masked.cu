@@ -25,6 +25,15 @@ int unit_rows(const pf_pool *pool, const AttnMask &mask, bool dual) {
     return std::min(pool->block_size, tile_tokens(pool));
 }
 
+// Tokens that a block sees at most: the table's, or a window's (its sinks, and its
+// rows' windows), in whole boxes.
+long long block_tokens(const pf_pool *pool, const AttnMask &mask, int n_q_heads, int max_blocks, int max_new) {
+    const long long group = n_q_heads / pool->n_kv_heads, tokens = (long long)max_blocks * pool->block_size;
+    if (mask.kind != kMaskWindow) return tokens;
+    return std::min(tokens, (long long)mask.sinks + mask.window + std::min<long long>(max_new, prompt_masked::ROWS / group + 1) +
+                                2 * unit_rows(pool, mask, max_new * group <= prompt_masked::QT));
+}
+
 // Workspace of a block's part.
 size_t part_bytes(const pf_pool *pool) {
     return (size_t)prompt_masked::ROWS * (pool->head_dim + 2) * sizeof(float);
@@ -44,11 +53,7 @@ int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q
     const long long group = n_q_heads / pool->n_kv_heads, all_rows = max_new * group;
     const long long blocks = (long long)n_seqs * pool->n_kv_heads * ((all_rows + prompt_masked::ROWS - 1) / prompt_masked::ROWS);
     if (blocks <= 0) return 1;
-    long long tokens = (long long)max_blocks * pool->block_size;
-    if (mask.kind == kMaskWindow)   // of a block: its sinks, and its rows' windows
-        tokens = std::min(tokens, (long long)mask.sinks + mask.window + std::min<long long>(max_new, prompt_masked::ROWS / group + 1) +
-                                      2 * unit_rows(pool, mask, all_rows <= prompt_masked::QT));
-    const long long tiles = (tokens + tile_tokens(pool) - 1) / tile_tokens(pool);
+    const long long tiles = (block_tokens(pool, mask, n_q_heads, max_blocks, max_new) + tile_tokens(pool) - 1) / tile_tokens(pool);
     const long long room = ws_bytes < kWorkspaceFront ? 0 : (long long)((ws_bytes - kWorkspaceFront) / part_bytes(pool));
     const long long n = std::min(std::min(std::min((long long)sms, room) / blocks, tiles / prompt_masked::kMinTiles),
                                  (long long)prompt_masked::kMaxParts);
@@ -124,6 +129,10 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     p.out_f32 = a.out_dtype == PF_F32;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.mask = a.mask;
+    // A wait may last as long as kInfos + 1 blocks: beside what any wait has, 33 us for
+    // each tile of the longest (one takes 0.3 to 2.5).
+    const long long most_tiles = block_tokens(pool, a.mask, a.n_q_heads, a.max_blocks, a.max_new) / tile_tokens(pool) + 1;
+    p.wait_ns = kWaitLimitNs + ((unsigned long long)most_tiles << 15);
     p.splits = 1;
     p.part_ml = nullptr;
     p.part_o = nullptr;

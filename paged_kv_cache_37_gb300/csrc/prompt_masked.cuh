@@ -148,6 +148,7 @@ struct Params {
     int out_f32;
     float scale_log2;
     AttnMask mask;
+    unsigned long long wait_ns;   // of any wait on chip
     int splits;       // parts at most
     float2 *part_ml;  // [block][part][ROWS]: a row's reference maximum (log2) and sum of weights
     float *part_o;    // [block][part][ROWS][D]: its sum of weighted values
@@ -277,6 +278,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int warp = (int)threadIdx.x / 32;
     const int lane = (int)threadIdx.x % 32;
     auto bar = [](unsigned long long &x) { return smem_addr(&x); };
+    // Every wait has the launch's limit: most last a tile, but warp 14's for a free
+    // description a block, and those of a softmax group without tiles in some blocks
+    // (their rows fit one query tile; the group goes on, up to kInfos blocks ahead)
+    // as long as the other takes for them.  (wait_one: by one thread.)
+    auto wait = [&](uint32_t b, uint32_t parity) { return wait_lanes(b, parity, p.status, p.wait_ns); };
+    auto wait_one = [&](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, p.status, 0, p.wait_ns); };
 
     // ---------------------------------------------------------------- setup
     const bool ordered = TREE && p.n_seqs > 1 && p.n_seqs <= kOrderSeqs && (p.max_blocks << p.block_shift) >= kOrderContext;
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // The k-th block; false: a wait ran out.  (take_one: by one thread of the warp.)
     auto take = [&](unsigned k, Info &f) {
         const unsigned slot = k % kInfos;
-        if (!wait_lanes(bar(bars.info_full[slot]), (k / kInfos) & 1, p.status)) return false;
+        if (!wait(bar(bars.info_full[slot]), (k / kInfos) & 1)) return false;
         f = infos[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.info_empty[slot]));
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     auto take_one = [&](unsigned k, Info &f) {
         const unsigned slot = k % kInfos;
-        if (!mbar_wait(bar(bars.info_full[slot]), (k / kInfos) & 1, p.status)) return false;
+        if (!wait_one(bar(bars.info_full[slot]), (k / kInfos) & 1)) return false;
         f = infos[slot];
         mbar_arrive(bar(bars.info_empty[slot]));
         return f.blk >= 0;
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         int nt_other = 0;
         auto take_rows = [&](unsigned k) {
             const unsigned slot = k % kInfos;
-            if (!wait_lanes(bar(bars.info_full[slot]), (k / kInfos) & 1, p.status)) return false;
+            if (!wait(bar(bars.info_full[slot]), (k / kInfos) & 1)) return false;
             const Info &in = infos[slot];
             f = Rows{in.blk, in.h, in.part, in.q0, in.n, in.base, in.r0, in.r_end, in.i0, in.rem0, in.lim[g], in.nt[g],
                      in.sinks, in.skip, in.tile0, in.n_parts};
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             float m = -INFINITY;                               // reference maximum, log2 units
             float l = 0.0f;                                    // sum of the weights
             for (int j = 0; j < nt; ++j, ++done) {
-                if (!wait_lanes(bar(bars.s_full[g]), done & 1, p.status)) {
+                if (!wait(bar(bars.s_full[g]), done & 1)) {
                     ok = false;
                     break;
                 }
@@ -517,13 +524,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
 
                 // DUAL: the other group has read the last block's O
-                if (DUAL && j == 0 && block > 1 && !wait_lanes(bar(bars.o_read[g ^ 1]), block & 1, p.status)) {
+                if (DUAL && j == 0 && block > 1 && !wait(bar(bars.o_read[g ^ 1]), block & 1)) {
                     ok = false;
                     break;
                 }
                 // the previous product has finished reading P and adding to O
                 if (j > 0) {
-                    if (!wait_lanes(bar(bars.o_done[g]), (done - 1) & 1, p.status)) {
+                    if (!wait(bar(bars.o_done[g]), (done - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -561,8 +568,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 // (no further ones come before the next rows); the other group has
                 // read what this one left for the last block (above, with tiles)
                 done_other += other;
-                if (g == 0 && other > 0 && !wait_lanes(bar(bars.s_full[g ^ 1]), (done_other - 1) & 1, p.status)) break;
-                if (nt == 0 && block > 1 && !wait_lanes(bar(bars.o_read[g ^ 1]), block & 1, p.status)) break;
+                if (g == 0 && other > 0 && !wait(bar(bars.s_full[g ^ 1]), (done_other - 1) & 1)) break;
+                if (nt == 0 && block > 1 && !wait(bar(bars.o_read[g ^ 1]), block & 1)) break;
                 ml[g * QT + t] = make_float2(m, l);
                 mbar_arrive(bar(bars.ml_full[g]));
             }
@@ -573,11 +580,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 rows_there();
                 continue;
             }
-            if (nt > 0 && !wait_lanes(bar(bars.o_done[g]), (done - 1) & 1, p.status)) break;
+            if (nt > 0 && !wait(bar(bars.o_done[g]), (done - 1) & 1)) break;
             float f_own = 1.0f, f_other = 0.0f;                // DUAL: factors that join the groups
             if (DUAL) {
-                if ((other > 0 && !wait_lanes(bar(bars.o_done[g ^ 1]), (done_other - 1) & 1, p.status)) ||
-                    !wait_lanes(bar(bars.ml_full[g ^ 1]), (block - 1) & 1, p.status))
+                if ((other > 0 && !wait(bar(bars.o_done[g ^ 1]), (done_other - 1) & 1)) ||
+                    !wait(bar(bars.ml_full[g ^ 1]), (block - 1) & 1))
                     break;
                 const float2 o = ml[(g ^ 1) * QT + t];
                 const float top = fmaxf(m, o.x);
@@ -691,7 +698,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         unsigned issued = 0;                                   // tiles so far
         // the stage of the next tile, once the MMAs over what it holds are done
         auto stage_free = [&]() {
-            return issued < (unsigned)NS || wait_lanes(bar(empty[issued % NS]), (issued / NS - 1) & 1, p.status);
+            return issued < (unsigned)NS || wait(bar(empty[issued % NS]), (issued / NS - 1) & 1);
         };
         bool ok = true;
         Info f = {};
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                 tma_load_4d_plain(dst + (uint32_t)(hf * BN + lane * box) * 128u, map, 0, row, hf, h, on);
                         }
                         if (ragged) {
-                            if (!wait_lanes(on, landed & 1, p.status)) {
+                            if (!wait(on, landed & 1)) {
                                 ok = false;
                                 break;
                             }
@@ -795,7 +802,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // exits (those of a last V tile have been waited for)
             if (B >= 16) {
                 for (unsigned k = issued < (unsigned)NS ? 0 : issued - NS; k < issued; ++k)
-                    wait_lanes(bar(full[k % NS]), (k / NS) & 1, p.status);
+                    wait(bar(full[k % NS]), (k / NS) & 1);
             }
         } else {
             // The tile's 512 16-byte chunks of codes are dealt to the 64 lanes of
@@ -936,19 +943,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             Info f;
             for (unsigned block = 0; ok && take_one(block, f); ++block) {
                 for (int j = 0; ok && j < f.tiles; ++j) {
-                    if (!mbar_wait(bar(bars.k_full[st]), phase, p.status)) {
+                    if (!wait_one(bar(bars.k_full[st]), phase)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (DUAL ? (j & 1) != g : j >= f.nt[g]) continue;
-                        if (j == 0 && !mbar_wait(bar(bars.q_full[g]), blocks[g]++ & 1, p.status)) {
+                        if (j == 0 && !wait_one(bar(bars.q_full[g]), blocks[g]++ & 1)) {
                             ok = false;
                             break;
                         }
                         // S of this query tile has been read (its previous tile)
-                        if (done[g] > 0 && !mbar_wait(bar(bars.s_free[g]), (done[g] - 1) & 1, p.status)) {
+                        if (done[g] > 0 && !wait_one(bar(bars.s_free[g]), (done[g] - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -974,7 +981,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             umma_commit(bar(bars.mma_done[0]));
         }
         __syncwarp();
-        wait_lanes(bar(bars.mma_done[0]), 0, p.status);
+        wait(bar(bars.mma_done[0]), 0);
     } else if (warp == MMA_PV_WARP) {
         // ------------------------------------------------ MMA: O += P V
         constexpr uint32_t ID_PV = idesc_f16(QT, D, true);
@@ -986,14 +993,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             Info f;
             for (unsigned block = 0; ok && take_one(block, f); ++block) {
                 for (int j = 0; ok && j < f.tiles; ++j) {
-                    if (!mbar_wait(bar(bars.v_full[st]), phase, p.status)) {
+                    if (!wait_one(bar(bars.v_full[st]), phase)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (DUAL ? (j & 1) != g : j >= f.nt[g]) continue;
-                        if (!mbar_wait(bar(bars.p_full[g]), done[g]++ & 1, p.status)) {
+                        if (!wait_one(bar(bars.p_full[g]), done[g]++ & 1)) {
                             ok = false;
                             break;
                         }
@@ -1015,7 +1022,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             umma_commit(bar(bars.mma_done[1]));
         }
         __syncwarp();
-        wait_lanes(bar(bars.mma_done[1]), 0, p.status);
+        wait(bar(bars.mma_done[1]), 0);
     } else if (warp == INFO_WARP) {
         // ----------------------------------------------- what the blocks are
         // Work w: part w mod splits of block w / splits, the longest blocks first.  Of
@@ -1063,7 +1070,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Work next = work_at(0);
         Seq next_seq = seq_of(next);
         unsigned k = 0;
-        int longest = 0;                                       // tiles
         for (int round = 0; round <= mine; ++round) {
             const Work w = next;
             const Seq seq = next_seq;
@@ -1115,12 +1121,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             }
             const unsigned slot = k % kInfos;
-            // The one wait that lasts as long as a block does (the others: a tile):
-            // its limit leaves 15 us for each tile of the longest.
-            if (k >= kInfos && !__all_sync(FULL, mbar_wait(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1, p.status, 0,
-                                                           kWaitLimitNs * (1 + longest / 65536))))
-                break;
-            longest = max(longest, f.tiles);
+            if (k >= kInfos && !wait(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1)) break;
             if (lane == 0) {
                 infos[slot] = f;
                 mbar_arrive(bar(bars.info_full[slot]));

@@ -119,8 +119,9 @@ __device__ __forceinline__ float ex2(float x) {
 // observes the completion itself; cheaper than one lane polling and a
 // broadcast when the phase has already completed); true on every lane only
 // if it completed for all of them, so the warp leaves its loops together.
-__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, int *status) {
-    return __all_sync(FULL, mbar_wait(bar, parity, status));
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, int *status,
+                                           unsigned long long limit_ns = kWaitLimitNs) {
+    return __all_sync(FULL, mbar_wait(bar, parity, status, 0, limit_ns));
 }
 
 // Packed pairs of fp32 for Blackwell's two-wide add.

@@ -581,3 +581,33 @@ def test_a_layer_with_drafts(pkv, cuda_dev, cache):
     if cache == "f16":
         assert_within(accepted[None], want, 2 * tol)
     assert pkv.pf_device_status(reset=True) == 0
+
+
+def test_long_blocks_with_rows_for_one_query_tile(pkv, cuda_dev):
+    """Two blocks of more than a second one after another on each SM, the first of 64 rows, so that half of the
+    softmax warps wait as long as the others work; 205 million tokens, of whose pages three, the first, one in the
+    middle and the last, hold values that are not 0, each in dims of its own.  All scores are 0, so an output
+    is such a page's values over the number of tokens seen: sums of 256 times 60000 and of ones are exact in fp32
+    (but for the last tile's ones, 2^-24), and the quotient is off by 2^-22 and its rounding."""
+    import torch
+    c = PagedCase(pkv, cuda_dev, [8 * 256], 16, 1, 128, 256)
+    c.v_dev.zero_()
+    ids = [int(x) for x in c.bt[0]]
+    for i, page in enumerate(ids[:3]):
+        c.v_dev[0, page, :, :, 32 * i:32 * i + 32] = 60000.0
+    seqs = torch.cuda.get_device_properties(cuda_dev).multi_processor_count
+    pages, n = 800001, 20
+    row = torch.tensor(ids[3:], dtype=torch.int32, device=cuda_dev).repeat(pages // 5 + 1)[:pages]
+    row[0], row[pages // 2], row[pages - 1] = ids[0], ids[1], ids[2]
+    table = row.expand(seqs, pages).contiguous()
+    L = 256 * (pages - 1) + 128
+    q = torch.zeros((seqs * n, 16, 128), dtype=torch.float16, device=cuda_dev)
+    out = torch.full_like(q, float("nan"))
+    cu = dev(np.arange(seqs + 1, dtype=np.int32) * n, cuda_dev)
+    pkv.pf_device_status(reset=True)
+    pkv.pf_paged_window_attention(c.pool, 0, q, table, dev(np.full(seqs, L, np.int32), cuda_dev), cu, n, 128 ** -0.5, L, 0, out)
+    assert pkv.pf_device_status(reset=True) == 0
+    seen = L - n + 1 + np.arange(n)
+    count = np.stack([np.full(n, 256), np.full(n, 256), seen - 256 * (pages - 1), np.zeros(n)], 1)      # of each page's
+    want = np.tile(np.repeat(60000.0 * count / seen[:, None], 32, 1), (seqs, 1))[:, None]
+    assert_within(host(out), np.broadcast_to(want, out.shape), np.broadcast_to(want * (F16 + 2.0 ** -21), out.shape))
