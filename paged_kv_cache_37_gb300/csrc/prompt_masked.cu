@@ -129,10 +129,6 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     p.out_f32 = a.out_dtype == PF_F32;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.mask = a.mask;
-    // A wait may last as long as kInfos + 1 blocks: beside what any wait has, 33 us for
-    // each tile of the longest (one takes 0.3 to 2.5).
-    const long long most_tiles = block_tokens(pool, a.mask, a.n_q_heads, a.max_blocks, a.max_new) / tile_tokens(pool) + 1;
-    p.wait_ns = kWaitLimitNs + ((unsigned long long)most_tiles << 15);
     p.splits = 1;
     p.part_ml = nullptr;
     p.part_o = nullptr;
@@ -143,6 +139,12 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
     }
     const bool split = p.splits > 1;
     p.n_work = (int)(blocks * p.splits);     // (cut: no more than SMs)
+    const unsigned grid = (unsigned)std::min(p.n_work, sms);
+    // A wait may last as long as kInfos + 1 blocks, and as long as all of a CTA's blocks
+    // are looked at: beside what any wait has, 33 us for each tile of the longest (one
+    // takes 0.3 to 2.5) and 0.13 us for each block (0.02).
+    const long long most_tiles = block_tokens(pool, a.mask, a.n_q_heads, a.max_blocks, a.max_new) / tile_tokens(pool) + 1;
+    p.wait_ns = kWaitLimitNs + ((unsigned long long)most_tiles << 15) + ((unsigned long long)(p.n_work / grid) << 7);
     const prompt_masked::Kernels k = a.mask.kind == kMaskWindow ? prompt_masked::window_kernels(D, q8, split, dual)
                                                                 : prompt_masked::tree_kernels(D, q8, split, dual);
     // once per device and kernel (setting it twice does no harm)
@@ -153,7 +155,6 @@ int launch_prompt_masked(const PrefillArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_error(e, "attention: cudaFuncSetAttribute");
         done.store(true, std::memory_order_release);
     }
-    const unsigned grid = (unsigned)std::min(p.n_work, sms);
     k.main<<<grid, prompt_masked::NTHREADS, k.smem, stream>>>(pool->tmap_pf_k[dev][boxes], pool->tmap_pf_v[dev][boxes], p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_error(e, "attention: launch");

@@ -1067,18 +1067,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             q.q1 = step ? w.s + 1 : p.cu_q[w.s + 1];
             return q;
         };
-        Work next = work_at(0);
-        Seq next_seq = seq_of(next);
+        // to the roles; false: a wait ran out
         unsigned k = 0;
-        for (int round = 0; round <= mine; ++round) {
-            const Work w = next;
-            const Seq seq = next_seq;
-            next = work_at(round + 1);
-            next_seq = seq_of(next);                           // on its way
-            Block<BN, MASK> b;
-            Info f = {};
-            f.blk = -1;
-            if (w.blk >= 0) {
+        auto publish = [&](const Info &f) {
+            const unsigned slot = k % kInfos;
+            if (k >= kInfos && !wait(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1)) return false;
+            if (lane == 0) {
+                infos[slot] = f;
+                mbar_arrive(bar(bars.info_full[slot]));
+            }
+            ++k;
+            return true;
+        };
+        // 32 rounds are looked at together, a lane each: blocks without rows (with a
+        // loose max_new most of them) are passed over.  The first of a (sequence,
+        // kv-head) is always taken: its lengths may be bad, its output zeros.
+        bool ok = true;
+        for (int round0 = 0; ok && round0 < mine; round0 += 32) {
+            const Work look = work_at(round0 + lane);
+            const Seq look_seq = seq_of(look);
+            unsigned todo = __ballot_sync(
+                FULL, look.blk >= 0 && (look.qp == 0 || min(look_seq.q1 - look_seq.q0, p.max_new) * p.gh > look.qp * ROWS));
+            for (; ok && todo; todo &= todo - 1) {
+                const int from = __ffs(todo) - 1;
+                Work w;
+                Seq seq;
+                w.s = __shfl_sync(FULL, look.s, from);
+                w.h = __shfl_sync(FULL, look.h, from);
+                w.qp = __shfl_sync(FULL, look.qp, from);
+                w.part = __shfl_sync(FULL, look.part, from);
+                w.blk = __shfl_sync(FULL, look.blk, from);
+                seq.L = __shfl_sync(FULL, look_seq.L, from);
+                seq.q0 = __shfl_sync(FULL, look_seq.q0, from);
+                seq.q1 = __shfl_sync(FULL, look_seq.q1, from);
+                Block<BN, MASK> b;
+                Info f = {};
                 bool bad;
                 b.make(p, seq, w.qp, bad);
                 if (bad && w.qp == 0 && w.h == 0 && w.part == 0 && lane == 0) atomicOr(p.status, PF_DEV_BAD_LENGTH);
@@ -1119,14 +1142,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     f.lim[g] = b.lim[DUAL ? 0 : g];
                     f.nt[g] = DUAL ? (f.tiles + 1 - g) / 2 : b.lim[g] < 0 ? 0 : min(max(b.lim[g] / BN + 1 - f.tile0, 0), f.tiles);
                 }
+                ok = publish(f);
             }
-            const unsigned slot = k % kInfos;
-            if (k >= kInfos && !wait(bar(bars.info_empty[slot]), (k / kInfos - 1) & 1)) break;
-            if (lane == 0) {
-                infos[slot] = f;
-                mbar_arrive(bar(bars.info_full[slot]));
-            }
-            ++k;
+        }
+        if (ok) {
+            Info f = {};
+            f.blk = -1;                                        // no more
+            publish(f);
         }
     }
     }

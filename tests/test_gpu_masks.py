@@ -611,3 +611,26 @@ def test_long_blocks_with_rows_for_one_query_tile(pkv, cuda_dev):
     count = np.stack([np.full(n, 256), np.full(n, 256), seen - 256 * (pages - 1), np.zeros(n)], 1)      # of each page's
     want = np.tile(np.repeat(60000.0 * count / seen[:, None], 32, 1), (seqs, 1))[:, None]
     assert_within(host(out), np.broadcast_to(want, out.shape), np.broadcast_to(want * (F16 + 2.0 ** -21), out.shape))
+
+
+@pytest.mark.parametrize("cache,d", [("f16", 64), ("e4m3", 128)])
+def test_bounds_as_loose_as_there_are(pkv, cuda_dev, cache, d):
+    """max_new_tokens as large as a table of 2^26 tokens (2 thousand million blocks of rows, nearly all of them
+    empty) and drafts of up to 2^20: 480 (sequence, kv-head) pairs, some without tokens or without new ones."""
+    import torch
+    page, seqs, h, g = 256, 60, 8, 16
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 500, seqs)]
+    new = [min(L, int(n)) for L, n in zip(lens, rng.integers(0, 24, seqs))]
+    lens[7] = new[7] = new[20] = 0
+    c = Ctx(pkv, cuda_dev, cache, lens, h * g, h, d, page)
+    offs = offsets(new)
+    q = c.rng.standard_normal((int(offs[-1]), h * g, d)).astype(np.float16)
+    table = torch.nn.functional.pad(dev(c.table, cuda_dev), (0, 2 ** 26 // page - c.table.shape[1]), value=1 << 30)
+    qd, ld, cu = dev(q, cuda_dev), dev(c.lens, cuda_dev), dev(offs, cuda_dev)
+    check(c, q, offs, [window_seen(L, n, 90, 5) for L, n in zip(lens, new)],
+          lambda out, w: pkv.pf_paged_window_attention(c.pool, 1, qd, table, ld, cu, 2 ** 31 - 1, c.scale, 90, 5, out, w), None, False)
+    trees = trees_for(c.rng, "empty", new)
+    bits = torch.nn.functional.pad(dev(pack(trees, 1), cuda_dev), (0, 2 ** 14 - 1), value=-1)
+    check(c, q, offs, [tree_seen(L, x) for L, x in zip(lens, trees)],
+          lambda out, w: pkv.pf_paged_tree_attention(c.pool, 1, qd, table, ld, cu, 2 ** 20, c.scale, bits, out, w), None, False)
