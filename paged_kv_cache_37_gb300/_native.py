@@ -167,6 +167,14 @@ def _rows_ptr(t, name, shape, dev, float16):
     return t.data_ptr(), apart if shape[0] > 1 else shape[1] * shape[2]
 
 
+def _need_tensors(**arguments):
+    """TypeError for the first argument that is no tensor (after an attribute of one was missing)."""
+    import torch
+    for name, t in arguments.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor") from None
+
+
 def _stream_ptr(stream):
     import torch
     if stream is None:
@@ -503,23 +511,28 @@ def _masked_args(pool, q, block_tables, context_lens, cu_q, out, workspace):
     """Checked arguments that the masked attention calls share: addresses of q,
     tables, lengths, cu_q, out and workspace, and the sizes among the arguments."""
     import torch
-    shape, table = q.shape, block_tables.shape
-    n = context_lens.numel()
-    if len(table) != 2 or table[0] != n or (cu_q is not None and cu_q.numel() != n + 1):
-        raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
-    if len(shape) != 3 or shape[2] != pool.head_dim or out.shape != shape:
-        raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out of its shape")
-    if cu_q is None and shape[0] != n:
-        raise PagedKVError(PF_ERR_INVALID, "without cu_q, q must have a row per sequence")
-    out_dtype = PF_F16 if out.dtype is torch.float16 else PF_F32
-    if out_dtype == PF_F32 and out.dtype is not torch.float32:
-        raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
-    dev, i32 = _pool_device(pool), torch.int32
-    return (dev, shape[0], n, shape[1], table[1], out_dtype, _dev_ptr(q, "q", torch.float16, dev),
-            _dev_ptr(block_tables, "block_tables", i32, dev), _dev_ptr(context_lens, "context_lens", i32, dev),
-            None if cu_q is None else _dev_ptr(cu_q, "cu_q", i32, dev), _dev_ptr(out, "out", None, dev),
-            None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
-            0 if workspace is None else workspace.nbytes)
+    try:
+        shape, table = q.shape, block_tables.shape
+        n = context_lens.numel()
+        if len(table) != 2 or table[0] != n or (cu_q is not None and cu_q.numel() != n + 1):
+            raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]; cu_q [n_seqs + 1]")
+        if len(shape) != 3 or shape[2] != pool.head_dim or out.shape != shape:
+            raise PagedKVError(PF_ERR_INVALID, "q must be [T_q, n_q_heads, head_dim], out of its shape")
+        if cu_q is None and shape[0] != n:
+            raise PagedKVError(PF_ERR_INVALID, "without cu_q, q must have a row per sequence")
+        out_dtype = PF_F16 if out.dtype is torch.float16 else PF_F32
+        if out_dtype == PF_F32 and out.dtype is not torch.float32:
+            _need_tensors(out=out)
+            raise PagedKVError(PF_ERR_INVALID, "out must be float16 or float32")
+        dev, i32 = _pool_device(pool), torch.int32
+        return (dev, shape[0], n, shape[1], table[1], out_dtype, _dev_ptr(q, "q", torch.float16, dev),
+                _dev_ptr(block_tables, "block_tables", i32, dev), _dev_ptr(context_lens, "context_lens", i32, dev),
+                None if cu_q is None else _dev_ptr(cu_q, "cu_q", i32, dev), _dev_ptr(out, "out", None, dev),
+                None if workspace is None else _dev_ptr(workspace, "workspace", None, dev),
+                0 if workspace is None else workspace.nbytes)
+    except AttributeError:
+        _need_tensors(q=q, block_tables=block_tables, context_lens=context_lens, cu_q=cu_q, out=out, workspace=workspace)
+        raise
 
 
 def pf_window_workspace_bytes(pool, n_seqs, n_q_heads, max_blocks_per_seq, max_new_tokens, window, n_sinks=0):
@@ -556,7 +569,10 @@ def pf_paged_tree_attention(pool, layer, q, block_tables, context_lens, cu_q, ma
         raise PagedKVError(PF_ERR_INVALID, "cu_q must be given")
     dev, rows, n, hq, width, out_dtype, q_p, bt_p, len_p, cu_p, out_p, ws_p, ws_bytes = _masked_args(
         pool, q, block_tables, context_lens, cu_q, out, workspace)
-    bits = tree.shape
+    try:
+        bits = tree.shape
+    except AttributeError:
+        raise TypeError("tree must be a torch tensor") from None
     if len(bits) != 2 or bits[0] != rows:
         raise PagedKVError(PF_ERR_INVALID, "tree must be [T_q, words], a row per query")
     if rows == 0:
@@ -601,60 +617,65 @@ def pf_norm_rope_write(pool, layer, q, k, v, block_tables, seq_idx, pos, angles,
     import torch
     f16, f32, i32 = torch.float16, torch.float32, torch.int32
     dev = _pool_device(pool)
-    first = k if q is None else q
-    if first is None:
-        raise PagedKVError(PF_ERR_INVALID, "neither queries nor keys")
-    if first.dim() != 3:
-        raise PagedKVError(PF_ERR_INVALID, "q and k must be [n_tokens, heads, head_dim]")
-    n, hq, D = first.shape
-    if D != pool.head_dim:
-        raise PagedKVError(PF_ERR_INVALID, f"q and k must have head_dim {pool.head_dim}")
-    if (q is None) != (q_out is None):
-        raise PagedKVError(PF_ERR_INVALID, "q needs q_out, and q_out q")
-    keys = (n, pool.n_kv_heads, D)
-    q_ptr = k_ptr = v_ptr = q_to = k_to = w_q = w_k = ang = rp = bt = seq = at = None
-    q_apart = k_apart = v_apart = q_to_apart = k_to_apart = n_positions = rot = rows = width = 0
-    if q is None:
-        hq = 0
-    else:
-        q_ptr, q_apart = _rows_ptr(q, "q", (n, hq, D), dev, f16)
-        q_to, q_to_apart = _rows_ptr(q_out, "q_out", (n, hq, D), dev, f16)
-    if k is not None:
-        k_ptr, k_apart = _rows_ptr(k, "k", keys, dev, f16)
-    if v is not None:
-        v_ptr, v_apart = _rows_ptr(v, "v", keys, dev, f16)
-    if k_out is not None:
-        k_to, k_to_apart = _rows_ptr(k_out, "k_out", keys, dev, f16)
-    if q_weight is not None:
-        if q_weight.numel() != D:
-            raise PagedKVError(PF_ERR_INVALID, "q_weight must be [head_dim]")
-        w_q = _dev_ptr(q_weight, "q_weight", f32, dev)
-    if k_weight is not None:
-        if k_weight.numel() != D:
-            raise PagedKVError(PF_ERR_INVALID, "k_weight must be [head_dim]")
-        w_k = _dev_ptr(k_weight, "k_weight", f32, dev)
-    if angles is not None:
-        if angles.dim() != 2:
-            raise PagedKVError(PF_ERR_INVALID, "angles must be [n_positions, rot_dim]")
-        n_positions, rot = angles.shape
-        ang = _dev_ptr(angles, "angles", f32, dev)
-    if rope_pos is not None:
-        if rope_pos.numel() != n:
-            raise PagedKVError(PF_ERR_INVALID, "rope_pos must have n_tokens entries")
-        rp = _dev_ptr(rope_pos, "rope_pos", i32, dev)
-    if block_tables is not None:
-        if block_tables.dim() != 2:
-            raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
-        rows, width = block_tables.shape
-        bt = _dev_ptr(block_tables, "block_tables", i32, dev)
-    if seq_idx is not None:
-        if seq_idx.numel() != n:
-            raise PagedKVError(PF_ERR_INVALID, "seq_idx must have n_tokens entries")
-        seq = _dev_ptr(seq_idx, "seq_idx", i32, dev)
-    if pos is not None:
-        if pos.numel() != n:
-            raise PagedKVError(PF_ERR_INVALID, "pos must have n_tokens entries")
-        at = _dev_ptr(pos, "pos", i32, dev)
+    try:
+        first = k if q is None else q
+        if first is None:
+            raise PagedKVError(PF_ERR_INVALID, "neither queries nor keys")
+        if first.dim() != 3:
+            raise PagedKVError(PF_ERR_INVALID, "q and k must be [n_tokens, heads, head_dim]")
+        n, hq, D = first.shape
+        if D != pool.head_dim:
+            raise PagedKVError(PF_ERR_INVALID, f"q and k must have head_dim {pool.head_dim}")
+        if (q is None) != (q_out is None):
+            raise PagedKVError(PF_ERR_INVALID, "q needs q_out, and q_out q")
+        keys = (n, pool.n_kv_heads, D)
+        q_ptr = k_ptr = v_ptr = q_to = k_to = w_q = w_k = ang = rp = bt = seq = at = None
+        q_apart = k_apart = v_apart = q_to_apart = k_to_apart = n_positions = rot = rows = width = 0
+        if q is None:
+            hq = 0
+        else:
+            q_ptr, q_apart = _rows_ptr(q, "q", (n, hq, D), dev, f16)
+            q_to, q_to_apart = _rows_ptr(q_out, "q_out", (n, hq, D), dev, f16)
+        if k is not None:
+            k_ptr, k_apart = _rows_ptr(k, "k", keys, dev, f16)
+        if v is not None:
+            v_ptr, v_apart = _rows_ptr(v, "v", keys, dev, f16)
+        if k_out is not None:
+            k_to, k_to_apart = _rows_ptr(k_out, "k_out", keys, dev, f16)
+        if q_weight is not None:
+            if q_weight.numel() != D:
+                raise PagedKVError(PF_ERR_INVALID, "q_weight must be [head_dim]")
+            w_q = _dev_ptr(q_weight, "q_weight", f32, dev)
+        if k_weight is not None:
+            if k_weight.numel() != D:
+                raise PagedKVError(PF_ERR_INVALID, "k_weight must be [head_dim]")
+            w_k = _dev_ptr(k_weight, "k_weight", f32, dev)
+        if angles is not None:
+            if angles.dim() != 2:
+                raise PagedKVError(PF_ERR_INVALID, "angles must be [n_positions, rot_dim]")
+            n_positions, rot = angles.shape
+            ang = _dev_ptr(angles, "angles", f32, dev)
+        if rope_pos is not None:
+            if rope_pos.numel() != n:
+                raise PagedKVError(PF_ERR_INVALID, "rope_pos must have n_tokens entries")
+            rp = _dev_ptr(rope_pos, "rope_pos", i32, dev)
+        if block_tables is not None:
+            if block_tables.dim() != 2:
+                raise PagedKVError(PF_ERR_INVALID, "block_tables must be [n_seqs, max_blocks]")
+            rows, width = block_tables.shape
+            bt = _dev_ptr(block_tables, "block_tables", i32, dev)
+        if seq_idx is not None:
+            if seq_idx.numel() != n:
+                raise PagedKVError(PF_ERR_INVALID, "seq_idx must have n_tokens entries")
+            seq = _dev_ptr(seq_idx, "seq_idx", i32, dev)
+        if pos is not None:
+            if pos.numel() != n:
+                raise PagedKVError(PF_ERR_INVALID, "pos must have n_tokens entries")
+            at = _dev_ptr(pos, "pos", i32, dev)
+    except AttributeError:
+        _need_tensors(q=q, k=k, v=v, block_tables=block_tables, seq_idx=seq_idx, pos=pos, angles=angles, q_out=q_out,
+                      k_out=k_out, q_weight=q_weight, k_weight=k_weight, rope_pos=rope_pos)
+        raise
     _check(lib().pf_norm_rope_write(
         pool.handle, layer, q_ptr, q_apart, k_ptr, k_apart, v_ptr, v_apart, n, hq, w_q, w_k, float(eps), ang, n_positions,
         rot, PF_ROPE_INTERLEAVED if interleaved else 0, rp, bt, rows, width, seq, at, q_to, q_to_apart, k_to,
