@@ -219,8 +219,6 @@ struct Block {
         }
         tiles = last / BN + 1;
     }
-    // context token of virtual token x
-    __device__ __forceinline__ int token(int x) const { return MASK == kMaskWindow && x >= sink_end ? x + skip : x; }
 };
 
 // What the roles need of a block.
@@ -233,6 +231,7 @@ struct Info {
     int lim[2], nt[2];        // per query tile: last virtual position, tiles of this part
     int last, sinks, sink_end, skip, lo;
     int tile0, tiles, n_parts;
+    // context token of virtual token x (trees: itself, sink_end and skip are 0)
     __device__ __forceinline__ int token(int x) const { return x >= sink_end ? x + skip : x; }
     // some row of the block sees virtual token x (which is not past the last)
     __device__ __forceinline__ bool seen(int x) const { return x < sinks || x >= lo; }
