@@ -634,3 +634,116 @@ def test_bounds_as_loose_as_there_are(pkv, cuda_dev, cache, d):
     bits = torch.nn.functional.pad(dev(pack(trees, 1), cuda_dev), (0, 2 ** 14 - 1), value=-1)
     check(c, q, offs, [tree_seen(L, x) for L, x in zip(lens, trees)],
           lambda out, w: pkv.pf_paged_tree_attention(c.pool, 1, qd, table, ld, cu, 2 ** 20, c.scale, bits, out, w), None, False)
+
+
+class Marked:
+    """A long context of one sequence: eight pages of zeros over and over, but for `marked` entries of its table,
+    each a page of its own with values in dims of its own.  Weights of the zero rows are all alike, so a few
+    thousand tokens and a count give the 64-bit result, and a marked page or token read in the wrong place shows.
+    All numbers are e4m3's, so that both pool types hold the same."""
+
+    def __init__(self, device, cache, hq, d, pages, marked, loud, pkv, seed=11):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.d, self.hq, self.marked, B = d, hq, np.asarray(marked), 256
+        k, v = np.zeros((8 + len(marked), B, 1, d), np.float32), np.zeros((8 + len(marked), B, 1, d), np.float32)
+        k[8:] = rng.choice([-3.0, -2.0, -1.5, -1.0, 1.0, 1.5, 2.0, 3.0], k[8:].shape)
+        own = d // len(marked)
+        for i, entry in enumerate(marked):
+            v[8 + i, :, 0, own * i:own * (i + 1)] = rng.choice([5.0, 6.0, 7.0], (B, own))
+            for t in loud:                                # tokens at a border: 64 times as much
+                if t // B == entry:
+                    v[8 + i, t % B] *= 64
+        to = torch.float16 if cache == "f16" else torch.float8_e4m3fn
+        pools = [dev(x, device)[None].to(to) for x in (k, v)]
+        scales = [] if cache == "f16" else [torch.ones((1, len(k), 1), device=device) for _ in range(2)]
+        self.keep = pools + scales
+        self.pool = pkv.pf_pool_create(*pools, *scales)
+        table = np.resize(np.arange(8, dtype=np.int32), pages)
+        table[self.marked] = 8 + np.arange(len(marked))
+        self.table = dev(table[None], device)
+        self.at = (self.marked[:, None] * B + np.arange(B)).reshape(-1)      # marked tokens, and their rows
+        self.k, self.v = (x[8:].astype(np.float64).reshape(-1, d) for x in (k, v))
+        self.scale = float(np.float32(d ** -0.5))
+
+    def want(self, q, seen, total, tiles):
+        """seen [n, marked tokens], total [n]: tokens seen of all.  The bound is masked64's, with fp32 sums of the
+        weights over `tiles` steps, each off by 2^-24 of the sum (twice: the products' too)."""
+        q = q.astype(np.float64)
+        z = np.where(seen[:, None], np.einsum("nhd,td->nht", q, self.k) * self.scale, -np.inf)
+        size = np.einsum("nhd,td->nht", np.abs(q), np.abs(self.k)).max(-1) * self.scale
+        zeros = (total - seen.sum(-1))[:, None].astype(np.float64)
+        assert (zeros > 0).all()
+        m = np.maximum(z.max(-1), 0.0)
+        w = np.exp(z - m[..., None])
+        sum_w = w.sum(-1) + zeros * np.exp(-m)
+        out, A = (np.einsum("nht,td->nhd", w, x) / sum_w[..., None] for x in (self.v, np.abs(self.v)))
+        e = size * (self.d + 4) * 2.0 ** -23 + (np.maximum(m, np.where(seen[:, None], np.abs(z), 0).max(-1)) + 16) * 2.0 ** -22
+        tol = A * (2 * e[..., None] + F16 + tiles * 2.0 ** -23)
+        small = np.einsum("nt,td->nd", seen.astype(np.float64), np.abs(self.v)) * 2.0 ** -25
+        return out, tol + small[:, None] / sum_w[..., None] + np.abs(out) * F16 + 2.0 ** -25
+
+
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+@pytest.mark.parametrize("hq,d", [(1, 64), (16, 128), (3, 128)])
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_places_in_a_very_long_context(pkv, cuda_dev, cache, hq, d, n):
+    """A million tokens: sinks, what lies behind them, both sides of the window's border, its middle and the end,
+    each a page of its own; every border lies inside a page."""
+    import torch
+    pages, first, S = 4000, 1500, 100
+    L = 256 * pages - 90
+    W = L - n + 1 - (256 * first + 77)                    # the first query sees tokens from 77 of page `first` on
+    loud = [*range(S - 4, S + 4), *range(256 * first + 70, 256 * first + 90), *range(L - n - 4, L)]
+    c = Marked(cuda_dev, cache, hq, d, pages, [0, 1, first - 1, first, 2700, pages - 2, pages - 1], loud, pkv)
+    q = np.random.default_rng(n).standard_normal((n, hq, d)).astype(np.float16)
+    p = np.arange(L - n, L)[:, None]
+    lens, cu = dev(np.array([L], np.int32), cuda_dev), dev(np.array([0, n], np.int32), cuda_dev)
+    qd, out = dev(q, cuda_dev), torch.empty((n, hq, d), dtype=torch.float16, device=cuda_dev)
+    pkv.pf_device_status(reset=True)
+    seen = (c.at <= p) & ((c.at > p - W) | (c.at < S))
+    ws = pkv.make_window_workspace(c.pool, 1, hq, pages, n, W, S)
+    want = c.want(q, seen, (np.minimum(W, p + 1) + np.minimum(S, np.maximum(0, p - W + 1)))[:, 0], 2 ** 14 + 2 ** 8)
+    for w in (ws, None):
+        pkv.pf_paged_window_attention(c.pool, 0, qd, c.table, lens, cu, n, c.scale, W, S, out, w)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out), *want)
+    sees = random_tree(np.random.default_rng(n), n)
+    bits = dev(pack([sees], -(-n // 64)), cuda_dev)
+    draft = c.at - (L - n)
+    seen = np.where(draft < 0, True, sees[:, np.clip(draft, 0, n - 1)] & (draft < n))
+    ws = pkv.make_tree_workspace(c.pool, 1, hq, pages, n)
+    want = c.want(q, seen, L - n + sees.sum(1), 2 ** 14 + 2 ** 8)
+    for w in (ws, None):
+        pkv.pf_paged_tree_attention(c.pool, 0, qd, c.table, lens, cu, n, c.scale, bits, out, w)
+        assert pkv.pf_device_status(reset=True) == 0
+        assert_within(host(out), *want)
+
+
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+@pytest.mark.parametrize("lens,n,hq,h,d", [([3000, 40, 700], 1, 14, 2, 64), ([6000, 5], 3, 8, 2, 128), ([9000], 30, 7, 1, 64),
+                                           ([900, 1200, 300], 60, 8, 2, 128), ([2000] * 40, 20, 8, 8, 64)])
+def test_the_same_bits_again(pkv, cuda_dev, cache, lens, n, hq, h, d):
+    """Contexts cut over the SMs are joined in one order: a call gives the same bits every time, also between others."""
+    import torch
+    c = Ctx(pkv, cuda_dev, cache, lens, hq, h, d, 16)
+    new = [min(n, L) for L in lens]
+    offs = offsets(new)
+    table, ld, cu = dev(c.table, cuda_dev), dev(c.lens, cuda_dev), dev(offs, cuda_dev)
+    q = dev(c.rng.standard_normal((int(offs[-1]), hq, d)).astype(np.float16), cuda_dev)
+    bits = dev(pack(trees_for(c.rng, "empty", new), 1), cuda_dev)
+    win, tre = (make(c.pool, len(lens), hq, table.shape[1], n, *more) for make, more in (
+        (pkv.make_window_workspace, (800, 4)), (pkv.make_tree_workspace, ())))
+    jobs = []
+    for dtype in (torch.float16, torch.float32):
+        jobs.append((lambda o: pkv.pf_paged_window_attention(c.pool, 1, q, table, ld, cu, n, c.scale, 800, 4, o, win), dtype))
+        jobs.append((lambda o: pkv.pf_paged_tree_attention(c.pool, 1, q, table, ld, cu, n, c.scale, bits, o, tre), dtype))
+    first = []
+    for i in range(6):
+        for j, (call, dtype) in enumerate(jobs):
+            out = torch.empty(q.shape, dtype=dtype, device=cuda_dev)
+            call(out)
+            if i == 0:
+                first.append(out)
+            else:
+                assert torch.equal(out, first[j]), (i, j)
