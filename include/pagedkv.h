@@ -537,10 +537,11 @@ PF_API size_t pf_cross_workspace_bytes(const pf_pool *pool, int n_seqs, int n_q_
  * other windows will do) and at most 16 query rows (tokens x q-heads) per
  * kv-head, the kernel and the roundings of pf_paged_cross_attention's few rows
  * (fp32 output with the weights to about 22 bits); otherwise, and for fp16 output
- * where it is the faster, the tcgen05 kernel, the weights rounded to fp16, which with a
- * workspace cuts long windows of few blocks over the SMs.  A max_new_tokens above
- * what the table holds counts as that; a loose one costs time (kernels and launches
- * are chosen for it), not exactness. */
+ * where an estimate of both times has it the faster, the tcgen05 kernel, the weights
+ * rounded to fp16 (2^-11 relative, fp32 output too), which with a workspace cuts long
+ * windows of few blocks over the SMs.  A max_new_tokens above what the table holds
+ * counts as that.  Kernels are chosen by it, so a loose one costs time, and hides
+ * that a call with fp32 output has few rows. */
 PF_API int pf_paged_window_attention(const pf_pool *pool, int layer, const void *q, const int32_t *block_tables,
                               int max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_q,
                               int n_seqs, int max_new_tokens, int n_q_heads, float scale, int window, int n_sinks,

@@ -7,7 +7,8 @@
 //   (a, b) -> (a c_i - b s_i, b c_i + a s_i),  c_i = angles[p][i],
 //                                              s_i = angles[p][rot / 2 + i],
 // over the pairs (y_i, y_{i + rot / 2}), or (y_2i, y_2i+1), i < rot / 2.  All in
-// fp32 and rounded once, to the fp16 result.  V rows are copied.
+// fp32 and rounded once, to the fp16 result.  V rows are copied, and so are chunks
+// without a norm outside the rotated part.
 //
 // Floor: 2 bytes read and 2 written per value, so it is HBM's.  Measured on
 // GB300: four prompts of 2,048 tokens, 40 heads x 128 (503 MB) 87 us, 5.8 TB/s,

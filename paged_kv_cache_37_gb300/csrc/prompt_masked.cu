@@ -15,9 +15,13 @@ int tile_tokens(const pf_pool *pool) {
 // Rows that are looked up and copied together (the TMA boxes of fp16 pools): 16 of
 // e4m3 pages and under windows, whose blocks walk whole boxes from their first token
 // on, otherwise what a page holds of a tile.  Boxes of 16 / 64 rows of pages of 64: 4
-// prompts of 4,096 tokens, window 512, 32 q-heads over 8 kv-heads x 128 142 / 154 us; a tile of
-// one query tile (dual) 0.56 / 0.50 us, so that long windows of those take the
-// larger; with two query tiles 0.75 either way.
+// prompts of 4,096 tokens, window 512, 32 q-heads over 8 kv-heads x 128 142 / 154 us.  With
+// one query tile a block (dual; 30 rows x 4, 8 kv-heads) it depends on more than the
+// window: x 128, 2 sequences, not cut, window 512 11.9 / 12.1, 768 14.2 / 14.2, 1,024
+// 16.8 / 16.5, 2,048 26.5 / 25.1, 4,000 45.2 / 41.3; but 64 sequences, window 256 28.8 /
+// 35.2, 512 41.2 / 46.3, 1,024 64.1 / 67.6, 2,048 107.5 / 109.1; x 64 within 2 % over
+// pages of 64, over pages of 256 (boxes of 128) 64 sequences, window 512 30.4 / 37.0, 2,048
+// 65.8 / 69.7.  The border serves the uncut calls of few blocks.
 constexpr int kSmallBoxWindow = 512;
 int unit_rows(const pf_pool *pool, const AttnMask &mask, bool dual) {
     if (pool->block_size < 16) return 1;
@@ -46,8 +50,11 @@ size_t part_bytes(const pf_pool *pool) {
 // pays: 0.9 us a tile saved against 4 us for the second launch and the parts'
 // bytes.  Uncut -> cut, trees over fp16 x 128: 8 blocks of 128 rows, 1,024 tokens
 // 15.0 -> 12.2 us, 4,096 42.2 -> 13.2; 64 blocks of 256 rows 1,024 tokens 19.2 ->
-// 22.6 (not taken), 2,048 31.9 -> 30.1; x 64 and e4m3 alike, the choice at most 2 us
-// from the better side.
+// 22.6 (not taken), 2,048 31.9 -> 30.1.  A tile takes from 0.56 us (fp16 x 128, one
+// query tile) to 1.24 (fp16 x 64, two); with 0.9 for all of them the choice costs 0.4 %
+// on average and 1.9 us at most (e4m3 x 64, 16 blocks of 1,024 tokens, 15.2 cut, 17.1
+// taken) over 152 cases: both types and head_dims, 30 to 250 drafts x 4 of 1 to 8
+// sequences, 8 kv-heads, 512 to 8,192 tokens.
 int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new,
                   int sms, size_t ws_bytes) {
     const long long group = n_q_heads / pool->n_kv_heads, all_rows = max_new * group;

@@ -34,8 +34,9 @@
 // Calls of at most 128 rows per (sequence, kv-head) (DUAL) have one query tile a
 // block: the two groups of softmax warps take its even and its odd tiles, each
 // with a maximum, a sum and an O of its own, and join them at the block's end, half
-// of the dims each.  A 64-token tile, 16 blocks that stay in L2: fp16 x 128 0.56 us,
-// 0.76 with both query tiles; fp16 x 64 0.33 and 0.62; e4m3 x 128 0.73 and 0.99.
+// of the dims each.  64 tokens (a tile at head_dim 128, half of one at 64), 16 blocks
+// that stay in L2: fp16 x 128 0.56 us, 0.76 with both query tiles; fp16 x 64 0.33 and
+// 0.62; e4m3 x 128 0.73 and 0.99.
 //
 // Per tile (see prefill_tc.cu): scores in tensor memory, a running maximum per row
 // in the log2 domain that is raised only past 2^8, weights rounded to fp16 into
@@ -43,8 +44,10 @@
 // a part or (tree) at all: its maximum stays -inf, its sum 0, its output zeros.
 //
 // Measured (GB300; 4 prompts of 4,096 tokens, 32 q-heads over 8 kv-heads x 128,
-// window 512, 4 sinks): 142 us, 902 TFLOP/s, tensor pipe busy 47 % of the cycles.  A CTA per block took 205, of which 6.4 us a block
-// beside 0.76 us a tile (blocks of 4, 10 and 18 tiles): the chain lengths, block
+// window 512, 4 sinks): 142 us in a CUDA graph, 902 TFLOP/s (146 on another board), tensor
+// pipe busy 47 % of the cycles; over an 8-bit pool 184, over fp16 pages of one token 209
+// (a tile's copies are waited for before the next tile's).  A CTA per block took 205, of
+// which 6.4 us a block beside 0.76 us a tile (blocks of 4, 10 and 18 tiles): the chain lengths, block
 // ids, rows, scores, weights, product, output, of which nothing overlapped.  Two
 // CTAs of 128 rows per SM instead took 198 (each is such a chain).  Here the query
 // rows fetched by warps of their own took 203, by the softmax warps 168; with the
