@@ -52,8 +52,8 @@ size_t part_bytes(const pf_pool *pool) {
 // 15.0 -> 12.2 us, 4,096 42.2 -> 13.2; 64 blocks of 256 rows 1,024 tokens 19.2 ->
 // 22.6 (not taken), 2,048 31.9 -> 30.1.  A tile takes from 0.56 us (fp16 x 128, one
 // query tile) to 1.24 (fp16 x 64, two); with 0.9 for all of them the choice costs 0.4 %
-// on average and 1.9 us at most (e4m3 x 64, 16 blocks of 1,024 tokens, 15.2 cut, 17.1
-// taken) over 152 cases: both types and head_dims, 30 to 250 drafts x 4 of 1 to 8
+// on average and 1.9 us at most (e4m3 x 64, 8 blocks of 1,024 tokens, 15.2 cut, 17.1
+// as chosen) over 152 cases: both types and head_dims, 30 to 250 drafts x 4 of 1 to 8
 // sequences, 8 kv-heads, 512 to 8,192 tokens.
 int masked_splits(const pf_pool *pool, const AttnMask &mask, int n_seqs, int n_q_heads, int max_blocks, int max_new,
                   int sms, size_t ws_bytes) {
